@@ -61,7 +61,8 @@ typedef enum {
   TLA_F16 = 0,  /* IEEE binary16                                        */
   TLA_BF16 = 1, /* bfloat16                                             */
   TLA_E4M3 = 2, /* OCP FP8 E4M3FN (bias 7, max 448, no inf)             */
-  TLA_F32 = 3   /* IEEE binary32 (bias / C only)                        */
+  TLA_F32 = 3,  /* IEEE binary32 (bias / C; gradients; quantizer input)  */
+  TLA_I8 = 4    /* signed 8-bit integer (grouped and int8 products)      */
 } tla_dtype;
 
 typedef enum { TLA_ROW_MAJOR = 0, TLA_COL_MAJOR = 1 } tla_order;
@@ -169,6 +170,123 @@ typedef struct {
   int32_t lds_bytes, vgprs, blocks_per_cu;
 } tla_gemm_kernel_info;
 int tla_gemm_variant_info(int32_t variant, int32_t a_type, tla_gemm_kernel_info *out);
+
+/* ------------------------------------------- expert-grouped products */
+/*
+ * Products of rows grouped by expert.  Row r of A belongs to the expert e
+ * with offsets[e] <= r < offsets[e + 1]; each expert has a K x N matrix B_e
+ * of its own:
+ *   z[r, n] = scale_a[r] * scale_b[e, n] * sum_k A[r, k] B_e[k, n] + bias[e, n]
+ *   z_mode TLA_Z_NONE    D = act(z)
+ *          TLA_Z_STORE   D = act(z) and Z = z (what the backward pass needs)
+ *          TLA_Z_GRAD    D = z * act'(Z), Z read: with A the gradient of a
+ *                        layer's output and B_e the next layer's weights in
+ *                        the other order this is the gradient of the
+ *                        activation's input
+ * act': 1 for z > 0 else 0 (ReLU); Phi(z) + z phi(z) (GELU, phi the normal
+ * density); 1 (none, Z is then not read).
+ *
+ * offsets: groups + 1 int32 values in device memory, from 0 to rows, not
+ * decreasing; experts without rows are allowed.  NULL with groups == 1 means
+ * one expert with every row.  The values are not checked on the host; the
+ * kernels clamp them into [0, rows], so wrong ones cost wrong results, never
+ * an access outside the buffers.  Rows that belong to no expert are not
+ * written.
+ *
+ * A: rows x K row-major (pitch lda).  B_e starts stride_b elements after
+ * B_(e-1) and is K x N in b_order: TLA_COL_MAJOR with pitch ldb >= K (each
+ * column's K values together: weights stored [N, K]) or TLA_ROW_MAJOR with
+ * ldb >= N (weights stored [K, N]; the fast paths need 16-bit operands).
+ * D, Z: rows x N row-major.
+ *
+ * Types: A and B both F16, BF16, E4M3 or I8; D F16 or BF16, Z of D's type;
+ * bias (groups x N, dense, or NULL) F16, BF16 or F32; scale_a (rows) and
+ * scale_b (groups x N, dense) fp32, either or both NULL (1), for 8-bit
+ * operands only.  16-bit and e4m3 products are summed in fp32, int8 ones in
+ * 32-bit integers without rounding, which holds up to K = 131071
+ * (TLA_ERR_UNSUPPORTED beyond).  The epilogue runs in fp32 and rounds once,
+ * to nearest even, for each output.  NaN passes through every activation.
+ *
+ * rows, N or groups == 0 is a no-op; K == 0 gives z = bias.  Padding is never
+ * read or written.  Device pointers must be aligned to their elements; D and
+ * Z must not overlap each other or an input.  groups, rows, N and K below
+ * 2^31 (TLA_ERR_UNSUPPORTED).
+ */
+enum { TLA_Z_NONE = 0, TLA_Z_STORE = 1, TLA_Z_GRAD = 2 };
+
+typedef struct {
+  int64_t groups, rows, N, K;
+  const int32_t *offsets;
+  const void *A; int32_t type; int64_t lda;
+  const void *B; int32_t b_order; int64_t ldb, stride_b;
+  void *D; int32_t d_type; int64_t ldd;
+  const float *scale_a, *scale_b;
+  const void *bias; int32_t bias_type;
+  void *Z; int64_t ldz; int32_t z_mode;
+  int32_t act; /* tla_act */
+} tla_grouped_gemm_args;
+
+int tla_grouped_gemm(const tla_grouped_gemm_args *args, void *stream);
+
+/* Name of the kernel tla_grouped_gemm would launch (as tla_gemm_variant;
+ * "noop" when there is nothing to do).  Host only. */
+int tla_grouped_gemm_variant(const tla_grouped_gemm_args *args, char *buf, int32_t cap);
+
+/*
+ * The weight and bias gradients of a grouped product:
+ *   D_e[k, n] = sum over e's rows r of A[r, k] Y[r, n]     (K x N)
+ *   dbias[e, n] = sum over e's rows r of Y[r, n]           (fp32, or NULL)
+ * A: rows x K row-major, Y: rows x N row-major, both F16 or both BF16; D_e
+ * starts stride_d elements after D_(e-1), F16, BF16 or F32, in d_order
+ * (TLA_ROW_MAJOR: [K, N] weights, ldd >= N; TLA_COL_MAJOR: [N, K] weights,
+ * ldd >= K).  Sums are fp32, rounded once at the end, in an order that does
+ * not change from call to call.  An expert without rows gets zeros; D is
+ * overwritten.  offsets as for tla_grouped_gemm.  K or N == 0 writes no D.
+ */
+typedef struct {
+  int64_t groups, rows, N, K;
+  const int32_t *offsets;
+  const void *A; int64_t lda;
+  const void *Y; int64_t ldy;
+  int32_t type;
+  void *D; int32_t d_type, d_order; int64_t ldd, stride_d;
+  float *dbias;
+} tla_grouped_wgrad_args;
+
+int tla_grouped_gemm_wgrad(const tla_grouped_wgrad_args *args, void *stream);
+
+/* ------------------------------------------------------- int8 product */
+/*
+ * D[m, n] = act( scale_a[m] * scale_b[n] * sum_k A[m, k] B[k, n] + bias[n] )
+ * with int8 A (M x K row-major) and B (K x N in b_order), exact 32-bit sums
+ * (K <= 131071), a scale for each token (row) and each channel (column).
+ * Types, defaults and limits as for tla_grouped_gemm with one expert.
+ */
+typedef struct {
+  int64_t M, N, K;
+  const void *A; int64_t lda;
+  const void *B; int32_t b_order; int64_t ldb;
+  void *D; int32_t d_type; int64_t ldd;
+  const float *scale_a, *scale_b;
+  const void *bias; int32_t bias_type;
+  int32_t act;
+} tla_gemm_i8_args;
+
+int tla_gemm_i8(const tla_gemm_i8_args *args, void *stream);
+
+/*
+ * int8 codes and a scale for each row of X (M x K row-major, F16, BF16 or
+ * F32, pitch ldx; Q int8 row-major, pitch ldq; scale fp32[M]):
+ *   scale[m] = max_k |X[m, k]| * (1/127 rounded to fp32)
+ *   Q[m, k] = X[m, k] / scale[m] to the nearest integer, ties to even,
+ *             clamped to [-127, 127]
+ * exactly (the quotient is rounded as if it were known to all digits).  A
+ * row of zeros, or one whose scale rounds to 0, gets zero codes; so does a
+ * row with an infinity or a NaN, whose scale is that infinity or NaN.
+ * M == 0 is a no-op, K == 0 gives zero scales.
+ */
+int tla_quantize_rows(int64_t M, int64_t K, const void *X, int32_t x_type, int64_t ldx, void *Q,
+                      int64_t ldq, float *scale, void *stream);
 
 /* --------------------------------------------------------- transpose */
 /*

@@ -1,0 +1,200 @@
+"""The expert-grouped and int8 entry points without a GPU: refusals come back
+as status codes before any device work, no-ops need no buffers, the binding
+refuses host tensors and wrong index types, and the 64-bit oracle agrees with
+its definitions."""
+import ctypes
+
+import pytest
+import torch
+
+import tiled_layout_algebra_amd as tla
+from oracle import grouped as og
+
+FAKE = 1 << 20  # aligned, never dereferenced on these paths
+
+
+def _product(**kw):
+    base = dict(groups=4, rows=64, N=64, K=64, offsets=FAKE, A=FAKE, type=tla.BF16, lda=64, B=FAKE,
+                b_order=tla.COL_MAJOR, ldb=64, stride_b=4096, D=2 * FAKE, d_type=tla.BF16, ldd=64,
+                scale_a=None, scale_b=None, bias=None, bias_type=tla.BF16, Z=None, ldz=64,
+                z_mode=tla.Z_NONE, act=tla.ACT_NONE)
+    base.update(kw)
+    return tla.GroupedGemmArgs(**base)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(groups=-1), tla.ERR_INVALID_ARG),
+    (dict(rows=-1), tla.ERR_INVALID_ARG),
+    (dict(N=-1), tla.ERR_INVALID_ARG),
+    (dict(K=-1), tla.ERR_INVALID_ARG),
+    (dict(b_order=2), tla.ERR_INVALID_ARG),
+    (dict(act=3), tla.ERR_INVALID_ARG),
+    (dict(z_mode=3), tla.ERR_INVALID_ARG),
+    (dict(z_mode=-1), tla.ERR_INVALID_ARG),
+    (dict(type=tla.F32), tla.ERR_UNSUPPORTED),
+    (dict(type=5), tla.ERR_UNSUPPORTED),
+    (dict(d_type=tla.F32), tla.ERR_UNSUPPORTED),
+    (dict(d_type=tla.I8), tla.ERR_UNSUPPORTED),
+    (dict(bias=FAKE, bias_type=tla.I8), tla.ERR_UNSUPPORTED),
+    (dict(scale_a=FAKE), tla.ERR_UNSUPPORTED),                 # 16-bit operands take no scales
+    (dict(scale_b=FAKE), tla.ERR_UNSUPPORTED),
+    (dict(type=tla.I8, K=131072, lda=131072, ldb=131072), tla.ERR_UNSUPPORTED),
+    (dict(rows=1 << 31), tla.ERR_UNSUPPORTED),
+    (dict(N=1 << 31), tla.ERR_UNSUPPORTED),
+    (dict(groups=1 << 31), tla.ERR_UNSUPPORTED),
+    (dict(offsets=None), tla.ERR_INVALID_ARG),                 # needed with more than one expert
+    (dict(A=None), tla.ERR_INVALID_ARG),
+    (dict(B=None), tla.ERR_INVALID_ARG),
+    (dict(D=None), tla.ERR_INVALID_ARG),
+    (dict(lda=63), tla.ERR_INVALID_ARG),
+    (dict(ldb=63), tla.ERR_INVALID_ARG),
+    (dict(b_order=tla.ROW_MAJOR, ldb=63), tla.ERR_INVALID_ARG),
+    (dict(stride_b=-1), tla.ERR_INVALID_ARG),
+    (dict(ldd=63), tla.ERR_INVALID_ARG),
+    (dict(z_mode=tla.Z_STORE), tla.ERR_INVALID_ARG),           # Z missing
+    (dict(z_mode=tla.Z_GRAD, act=tla.ACT_RELU), tla.ERR_INVALID_ARG),
+    (dict(z_mode=tla.Z_STORE, Z=2 * FAKE), tla.ERR_INVALID_ARG),   # Z is D
+    (dict(z_mode=tla.Z_STORE, Z=FAKE, ldz=63), tla.ERR_INVALID_ARG),
+    (dict(A=FAKE + 1), tla.ERR_INVALID_ARG),                   # element alignment
+    (dict(D=FAKE + 1), tla.ERR_INVALID_ARG),
+    (dict(offsets=FAKE + 2), tla.ERR_INVALID_ARG),
+    (dict(type=tla.I8, scale_a=FAKE + 2), tla.ERR_INVALID_ARG),
+    (dict(bias=FAKE + 2, bias_type=tla.F32), tla.ERR_INVALID_ARG),
+])
+def test_product_refusals(kw, status):
+    a = _product(**kw)
+    assert tla.lib().tla_grouped_gemm(ctypes.byref(a), None) == status
+    buf = ctypes.create_string_buffer(64)
+    assert tla.lib().tla_grouped_gemm_variant(ctypes.byref(a), buf, 64) == status
+
+
+def _variant(**kw):
+    buf = ctypes.create_string_buffer(64)
+    rc = tla.lib().tla_grouped_gemm_variant(ctypes.byref(_product(**kw)), buf, 64)
+    assert rc == tla.OK
+    return buf.value.decode()
+
+
+def test_noops_and_small_buffers():
+    L = tla.lib()
+    for kw in (dict(rows=0), dict(N=0), dict(groups=0)):
+        a = _product(A=None, B=None, D=None, offsets=None, **kw)
+        assert L.tla_grouped_gemm(ctypes.byref(a), None) == tla.OK
+        assert _variant(A=None, B=None, D=None, offsets=None, **kw) == "noop"
+    assert L.tla_grouped_gemm(None, None) == tla.ERR_INVALID_ARG
+    assert L.tla_gemm_i8(None, None) == tla.ERR_INVALID_ARG
+    assert L.tla_grouped_gemm_wgrad(None, None) == tla.ERR_INVALID_ARG
+    assert L.tla_grouped_gemm_variant(ctypes.byref(_product()), None, 64) == tla.ERR_INVALID_ARG
+    buf = ctypes.create_string_buffer(b"xxxxxxxx", 8)
+    assert L.tla_grouped_gemm_variant(ctypes.byref(_product()), buf, 4) == tla.OK
+    assert len(buf.value) == 3
+    # one expert needs no offsets, no K needs no operands, the identity no Z
+    assert _variant(groups=1, offsets=None) != "noop"
+    assert _variant(K=0, A=None, B=None) != "noop"
+    assert _variant(z_mode=tla.Z_GRAD, act=tla.ACT_NONE) != "noop"
+
+
+def _i8(**kw):
+    base = dict(M=8, N=64, K=64, A=FAKE, lda=64, B=FAKE, b_order=tla.COL_MAJOR, ldb=64, D=FAKE,
+                d_type=tla.BF16, ldd=64, scale_a=None, scale_b=None, bias=None, bias_type=tla.BF16,
+                act=tla.ACT_NONE)
+    base.update(kw)
+    return tla.GemmI8Args(**base)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(M=-1), tla.ERR_INVALID_ARG), (dict(K=131072, lda=131072, ldb=131072), tla.ERR_UNSUPPORTED),
+    (dict(d_type=tla.F32), tla.ERR_UNSUPPORTED), (dict(lda=1), tla.ERR_INVALID_ARG),
+    (dict(A=None), tla.ERR_INVALID_ARG), (dict(act=-1), tla.ERR_INVALID_ARG),
+    (dict(M=0, A=None, B=None, D=None), tla.OK), (dict(N=0, A=None, B=None, D=None), tla.OK),
+])
+def test_int8_refusals(kw, status):
+    assert tla.lib().tla_gemm_i8(ctypes.byref(_i8(**kw)), None) == status
+
+
+def _wgrad(**kw):
+    base = dict(groups=4, rows=64, N=64, K=32, offsets=FAKE, A=FAKE, lda=32, Y=FAKE, ldy=64,
+                type=tla.BF16, D=FAKE, d_type=tla.F32, d_order=tla.ROW_MAJOR, ldd=64,
+                stride_d=2048, dbias=None)
+    base.update(kw)
+    return tla.GroupedWgradArgs(**base)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(groups=-1), tla.ERR_INVALID_ARG), (dict(rows=-2), tla.ERR_INVALID_ARG),
+    (dict(d_order=3), tla.ERR_INVALID_ARG), (dict(type=tla.I8), tla.ERR_UNSUPPORTED),
+    (dict(type=tla.E4M3), tla.ERR_UNSUPPORTED), (dict(d_type=tla.E4M3), tla.ERR_UNSUPPORTED),
+    (dict(offsets=None), tla.ERR_INVALID_ARG), (dict(A=None), tla.ERR_INVALID_ARG),
+    (dict(Y=None), tla.ERR_INVALID_ARG), (dict(D=None), tla.ERR_INVALID_ARG),
+    (dict(lda=31), tla.ERR_INVALID_ARG), (dict(ldy=63), tla.ERR_INVALID_ARG),
+    (dict(ldd=63), tla.ERR_INVALID_ARG), (dict(stride_d=2047), tla.ERR_INVALID_ARG),
+    (dict(d_order=tla.COL_MAJOR, ldd=31), tla.ERR_INVALID_ARG),
+    (dict(D=FAKE + 2), tla.ERR_INVALID_ARG), (dict(dbias=FAKE + 2), tla.ERR_INVALID_ARG),
+    (dict(N=1 << 31), tla.ERR_UNSUPPORTED),
+    (dict(groups=0), tla.OK), (dict(N=0), tla.OK), (dict(K=0), tla.OK),
+])
+def test_wgrad_refusals(kw, status):
+    assert tla.lib().tla_grouped_gemm_wgrad(ctypes.byref(_wgrad(**kw)), None) == status
+
+
+@pytest.mark.parametrize("args,status", [
+    ((-1, 8, FAKE, tla.BF16, 8, FAKE, 8, FAKE), tla.ERR_INVALID_ARG),
+    ((4, -8, FAKE, tla.BF16, 8, FAKE, 8, FAKE), tla.ERR_INVALID_ARG),
+    ((4, 8, FAKE, tla.E4M3, 8, FAKE, 8, FAKE), tla.ERR_UNSUPPORTED),
+    ((4, 8, FAKE, tla.I8, 8, FAKE, 8, FAKE), tla.ERR_UNSUPPORTED),
+    ((4, 8, None, tla.BF16, 8, FAKE, 8, FAKE), tla.ERR_INVALID_ARG),
+    ((4, 8, FAKE, tla.BF16, 8, None, 8, FAKE), tla.ERR_INVALID_ARG),
+    ((4, 8, FAKE, tla.BF16, 8, FAKE, 8, None), tla.ERR_INVALID_ARG),
+    ((4, 8, FAKE, tla.BF16, 7, FAKE, 8, FAKE), tla.ERR_INVALID_ARG),
+    ((4, 8, FAKE, tla.BF16, 8, FAKE, 7, FAKE), tla.ERR_INVALID_ARG),
+    ((4, 8, FAKE + 2, tla.F32, 8, FAKE, 8, FAKE), tla.ERR_INVALID_ARG),
+    ((4, 8, FAKE, tla.F32, 8, FAKE, 8, FAKE + 1), tla.ERR_INVALID_ARG),
+    ((0, 8, None, tla.F32, 8, None, 8, None), tla.OK),
+])
+def test_quantizer_refusals(args, status):
+    assert tla.lib().tla_quantize_rows(*args, None) == status
+
+
+def test_binding_refuses_host_tensors_and_other_index_types():
+    t = torch.zeros(64)
+    with pytest.raises(ValueError, match="CUDA"):
+        tla.quantize_rows(1, 64, t, tla.F32, 64, t, 64, t)
+    with pytest.raises(ValueError, match="int32"):
+        tla.grouped_gemm(1, 1, 8, 8, torch.zeros(2, dtype=torch.int64), t, tla.BF16, 8, t,
+                         tla.COL_MAJOR, 8, 64, t, tla.BF16, 8)
+    with pytest.raises(ValueError, match="float32"):
+        tla.gemm_i8(1, 8, 8, None, 8, None, tla.COL_MAJOR, 8, None, tla.BF16, 8,
+                    scale_a=torch.zeros(1, dtype=torch.float16))
+
+
+def test_oracle_against_its_definitions():
+    gen = torch.Generator().manual_seed(0)
+    A, B = torch.randn(7, 5, generator=gen), torch.randn(3, 5, 4, generator=gen)
+    off = [0, 3, 3, 7]
+    z, S = og.pre_activation(A, B, off, bias=torch.ones(3, 4))
+    for r in range(7):
+        e = 0 if r < 3 else 2
+        for n in range(4):
+            want = sum(float(A[r, k]) * float(B[e, k, n]) for k in range(5)) + 1
+            assert abs(float(z[r, n]) - want) < 1e-12 and float(S[r, n]) >= abs(want)
+    zz = torch.linspace(-6, 6, 101, dtype=torch.float64, requires_grad=True)
+    for kind in (og.ACT_NONE, og.ACT_RELU, og.ACT_GELU):
+        (slope,) = torch.autograd.grad(og.act(zz, kind).sum(), zz)
+        keep = zz != 0
+        assert (slope - og.act_slope(zz, kind))[keep].abs().max() < 1e-12
+    D, _, db, _ = og.wgrad(A, A[:, :4], off)
+    assert torch.allclose(D[2], A[3:].double().t() @ A[3:, :4].double())
+    assert (D[1] == 0).all() and torch.allclose(db[0], A[:3, :4].double().sum(0))
+
+
+def test_quantizer_oracle_rounds_exactly():
+    """The float64 quotients against exact rational rounding."""
+    from fractions import Fraction
+    gen = torch.Generator().manual_seed(1)
+    x = torch.randn(4, 60, generator=gen)
+    x[0, :5] = torch.tensor([127.0, 0.5, 1.5, -2.5, 63.5])
+    q, s = og.quantize_rows(x)
+    for r in range(4):
+        for c in range(60):
+            f = Fraction(float(x[r, c])) / Fraction(float(s[r]))
+            assert int(q[r, c]) == max(-127, min(127, round(f)))

@@ -18,9 +18,10 @@ LIB_PATH = os.path.join(_HERE, "libtla.so")
 
 # enums of tla.h
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_OVERLAP, ERR_HIP = 0, -1, -2, -3, -4
-F16, BF16, E4M3, F32 = 0, 1, 2, 3
+F16, BF16, E4M3, F32, I8 = 0, 1, 2, 3, 4
 ROW_MAJOR, COL_MAJOR = 0, 1
 ACT_NONE, ACT_RELU, ACT_GELU = 0, 1, 2
+Z_NONE, Z_STORE, Z_GRAD = 0, 1, 2
 MAX_MODES, MAX_LEAVES = 8, 16
 
 EXPORTED = [
@@ -31,6 +32,8 @@ EXPORTED = [
     "tla_thread_map_eval", "tla_logical_product", "tla_coalesce", "tla_composition",
     "tla_logical_divide_modes", "tla_thread_map_ex", "tla_thread_map_eval_ex",
     "tla_status_string", "tla_version",
+    "tla_grouped_gemm", "tla_grouped_gemm_variant", "tla_grouped_gemm_wgrad", "tla_gemm_i8",
+    "tla_quantize_rows",
 ]
 
 
@@ -101,6 +104,12 @@ def lib() -> ctypes.CDLL:
         L.tla_thread_map_ex.argtypes = [I64, I64, I32, I32, I32, I32, I32, LP]
         L.tla_thread_map_eval_ex.argtypes = [I64, I64, I32, I32, I32, I32, I32, I32, I64, I64,
                                              P, P, P]
+        L.tla_grouped_gemm.argtypes = [ctypes.POINTER(GroupedGemmArgs), P]
+        L.tla_grouped_gemm_variant.argtypes = [ctypes.POINTER(GroupedGemmArgs), ctypes.c_char_p,
+                                               I32]
+        L.tla_grouped_gemm_wgrad.argtypes = [ctypes.POINTER(GroupedWgradArgs), P]
+        L.tla_gemm_i8.argtypes = [ctypes.POINTER(GemmI8Args), P]
+        L.tla_quantize_rows.argtypes = [I64, I64, P, I32, I64, P, I64, P, P]
         L.tla_status_string.argtypes = [ctypes.c_int]
         L.tla_status_string.restype = ctypes.c_char_p
         for name in EXPORTED:
@@ -255,6 +264,114 @@ def gemm_variant(*args, **kw) -> str:
     buf = ctypes.create_string_buffer(64)
     _check(lib().tla_gemm_variant(ctypes.byref(a), buf, 64), "tla_gemm_variant")
     return buf.value.decode()
+
+
+# ------------------------------------- expert-grouped and int8 products
+
+class GroupedGemmArgs(ctypes.Structure):
+    _fields_ = [
+        ("groups", ctypes.c_int64), ("rows", ctypes.c_int64), ("N", ctypes.c_int64),
+        ("K", ctypes.c_int64), ("offsets", ctypes.c_void_p),
+        ("A", ctypes.c_void_p), ("type", ctypes.c_int32), ("lda", ctypes.c_int64),
+        ("B", ctypes.c_void_p), ("b_order", ctypes.c_int32), ("ldb", ctypes.c_int64),
+        ("stride_b", ctypes.c_int64),
+        ("D", ctypes.c_void_p), ("d_type", ctypes.c_int32), ("ldd", ctypes.c_int64),
+        ("scale_a", ctypes.c_void_p), ("scale_b", ctypes.c_void_p),
+        ("bias", ctypes.c_void_p), ("bias_type", ctypes.c_int32),
+        ("Z", ctypes.c_void_p), ("ldz", ctypes.c_int64), ("z_mode", ctypes.c_int32),
+        ("act", ctypes.c_int32),
+    ]
+
+
+class GroupedWgradArgs(ctypes.Structure):
+    _fields_ = [
+        ("groups", ctypes.c_int64), ("rows", ctypes.c_int64), ("N", ctypes.c_int64),
+        ("K", ctypes.c_int64), ("offsets", ctypes.c_void_p),
+        ("A", ctypes.c_void_p), ("lda", ctypes.c_int64),
+        ("Y", ctypes.c_void_p), ("ldy", ctypes.c_int64), ("type", ctypes.c_int32),
+        ("D", ctypes.c_void_p), ("d_type", ctypes.c_int32), ("d_order", ctypes.c_int32),
+        ("ldd", ctypes.c_int64), ("stride_d", ctypes.c_int64), ("dbias", ctypes.c_void_p),
+    ]
+
+
+class GemmI8Args(ctypes.Structure):
+    _fields_ = [
+        ("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
+        ("A", ctypes.c_void_p), ("lda", ctypes.c_int64),
+        ("B", ctypes.c_void_p), ("b_order", ctypes.c_int32), ("ldb", ctypes.c_int64),
+        ("D", ctypes.c_void_p), ("d_type", ctypes.c_int32), ("ldd", ctypes.c_int64),
+        ("scale_a", ctypes.c_void_p), ("scale_b", ctypes.c_void_p),
+        ("bias", ctypes.c_void_p), ("bias_type", ctypes.c_int32), ("act", ctypes.c_int32),
+    ]
+
+
+def _dev32(t, kind, what):
+    """_dev for a buffer whose element type the library fixes ("int32" or
+    "float32"): another dtype would be misread, so it is refused."""
+    if t is not None and str(t.dtype) != "torch." + kind:
+        raise ValueError("%s must be a %s tensor" % (what, kind))
+    return _dev(t, what)
+
+
+def _grouped_gemm_args(groups, rows, N, K, offsets, A, type, lda, B, b_order, ldb, stride_b, D,
+                       d_type, ldd, scale_a=None, scale_b=None, bias=None, bias_type=None, Z=None,
+                       ldz=0, z_mode=Z_NONE, act=ACT_NONE):
+    return GroupedGemmArgs(
+        groups, rows, N, K, _dev32(offsets, "int32", "offsets"), _dev(A, "A"), type, lda,
+        _dev(B, "B"), b_order, ldb, stride_b, _dev(D, "D"), d_type, ldd,
+        _dev32(scale_a, "float32", "scale_a"), _dev32(scale_b, "float32", "scale_b"),
+        _dev(bias, "bias"), d_type if bias_type is None else bias_type, _dev(Z, "Z"), ldz, z_mode,
+        act)
+
+
+def grouped_gemm(groups, rows, N, K, offsets, A, type, lda, B, b_order, ldb, stride_b, D, d_type,
+                 ldd, scale_a=None, scale_b=None, bias=None, bias_type=None, Z=None, ldz=0,
+                 z_mode=Z_NONE, act=ACT_NONE, stream=None):
+    """Rows grouped by expert times their expert's matrix (tla_grouped_gemm):
+    z = scale_a scale_b A.B_e + bias; D = act(z), with Z = z for Z_STORE, or
+    D = z act'(Z) for Z_GRAD.  offsets: int32 CUDA tensor of groups + 1
+    values (None: one expert)."""
+    a = _grouped_gemm_args(groups, rows, N, K, offsets, A, type, lda, B, b_order, ldb, stride_b, D,
+                           d_type, ldd, scale_a, scale_b, bias, bias_type, Z, ldz, z_mode, act)
+    _check(lib().tla_grouped_gemm(ctypes.byref(a), _stream(stream, A, B, D)), "tla_grouped_gemm")
+
+
+def grouped_gemm_variant(*args, **kw) -> str:
+    """Name of the kernel grouped_gemm would launch (host only)."""
+    kw.pop("stream", None)
+    a = _grouped_gemm_args(*args, **kw)
+    buf = ctypes.create_string_buffer(64)
+    _check(lib().tla_grouped_gemm_variant(ctypes.byref(a), buf, 64), "tla_grouped_gemm_variant")
+    return buf.value.decode()
+
+
+def grouped_gemm_wgrad(groups, rows, N, K, offsets, A, lda, Y, ldy, type, D, d_type, d_order, ldd,
+                       stride_d, dbias=None, stream=None):
+    """D_e = A_e^T Y_e and dbias_e = the column sums of Y_e for every expert
+    (tla_grouped_gemm_wgrad)."""
+    a = GroupedWgradArgs(groups, rows, N, K, _dev32(offsets, "int32", "offsets"), _dev(A, "A"),
+                         lda, _dev(Y, "Y"), ldy, type, _dev(D, "D"), d_type, d_order, ldd,
+                         stride_d, _dev32(dbias, "float32", "dbias"))
+    _check(lib().tla_grouped_gemm_wgrad(ctypes.byref(a), _stream(stream, A, Y, D)),
+           "tla_grouped_gemm_wgrad")
+
+
+def gemm_i8(M, N, K, A, lda, B, b_order, ldb, D, d_type, ldd, scale_a=None, scale_b=None,
+            bias=None, bias_type=None, act=ACT_NONE, stream=None):
+    """D = act(scale_a[m] scale_b[n] A.B + bias[n]) with int8 A and B and exact
+    integer sums (tla_gemm_i8)."""
+    a = GemmI8Args(M, N, K, _dev(A, "A"), lda, _dev(B, "B"), b_order, ldb, _dev(D, "D"), d_type,
+                   ldd, _dev32(scale_a, "float32", "scale_a"),
+                   _dev32(scale_b, "float32", "scale_b"), _dev(bias, "bias"),
+                   d_type if bias_type is None else bias_type, act)
+    _check(lib().tla_gemm_i8(ctypes.byref(a), _stream(stream, A, B, D)), "tla_gemm_i8")
+
+
+def quantize_rows(M, K, X, x_type, ldx, Q, ldq, scale, stream=None):
+    """int8 codes Q and a scale for each row of X (tla_quantize_rows)."""
+    _check(lib().tla_quantize_rows(M, K, _dev(X, "X"), x_type, ldx, _dev(Q, "Q"), ldq,
+                                   _dev32(scale, "float32", "scale"), _stream(stream, X, Q, scale)),
+           "tla_quantize_rows")
 
 
 # -------------------------------------------------------------- transpose

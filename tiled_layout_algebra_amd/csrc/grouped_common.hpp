@@ -1,0 +1,422 @@
+// grouped_common.hpp -- what the expert-grouped kernels share: the lookup of
+// a workgroup's tile from the experts' row offsets, the int8 matrix-core
+// atom and the epilogue of the grouped products.
+#pragma once
+
+#include "gemm_common.hpp"
+#include "operators.hpp"
+
+namespace tla {
+
+typedef int i32x16 __attribute__((ext_vector_type(16)));
+
+// A matrix-core step of each operand type: MfmaAtom's 32x32 instruction with
+// the accumulator type beside it.  int8 takes 16 bytes of K per lane like the
+// 16-bit types (32x32x32, exact 32-bit sums), so it shares their slabs,
+// fragment reads and instruction schedule.
+template <int kCode>
+struct OpAtom : MfmaAtom<kCode> {
+  typedef f32x16 Acc;
+};
+template <>
+struct OpAtom<kI8> {
+  static constexpr int kK = 32;
+  static constexpr int kLaneBytes = 16;
+  typedef i32x4 Frag;
+  typedef i32x16 Acc;
+  static __device__ __forceinline__ void mma(i32x16& acc, const Frag& a, const Frag& b) {
+    acc = __builtin_amdgcn_mfma_i32_32x32x32_i8(a, b, acc, 0, 0, 0);
+  }
+};
+// e4m3 through the 16-bit instruction, as f16, which holds every e4m3 value:
+// the same fragments as the 8-bit instruction's (32 consecutive K per lane,
+// taken 8 at a time).  The 8-bit instructions align a step's products to the
+// largest and drop what falls below about its 2^-15 (measured: 2^-14.3 of two
+// terms' magnitudes, 2^-15.8 of 64 terms'), which only sums of many steps
+// bury under their own fp32 rounding; here every product and sum is fp32.
+struct E4m3AsF16 {
+  static constexpr int kK = 64;
+  static constexpr int kLaneBytes = 32;
+  typedef i32x8 Frag;
+  typedef f32x16 Acc;
+  static __device__ __forceinline__ i32x4 widen(const Frag& f, int q) {
+    typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+    i32x4 r;
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      const f16x2 lo = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(f[2 * q + w], 1.0f, false);
+      const f16x2 hi = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(f[2 * q + w], 1.0f, true);
+      r[2 * w] = __builtin_bit_cast(int, lo);
+      r[2 * w + 1] = __builtin_bit_cast(int, hi);
+    }
+    return r;
+  }
+  static __device__ __forceinline__ void mma(f32x16& acc, const Frag& a, const Frag& b) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) MfmaAtom<kF16>::mma(acc, widen(a, q), widen(b, q));
+  }
+};
+// load_frag's geometry depends only on the bytes of a K step and of a lane's
+// share of it, which int8 shares with the 16-bit types.
+template <int kCode>
+constexpr int kFragCode = kCode == kI8 ? (int)kBF16 : kCode;
+
+namespace {
+
+// ------------------------------------------------------------- tile lookup
+// The rows of expert e, clamped into [0, rows] and in order, so no offsets
+// array, however wrong, leads an access outside A, D or Z.
+__device__ __forceinline__ void expert_rows(const GroupedParams& p, int e, int& lo, int& hi) {
+  if (!p.offsets) {
+    lo = 0;
+    hi = p.rows;
+    return;
+  }
+  lo = min(max(p.offsets[e], 0), p.rows);
+  hi = min(max(p.offsets[e + 1], lo), p.rows);
+}
+
+__device__ __forceinline__ int wave_scan(int x, int lane) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int y = __shfl_up(x, d);
+    if (lane >= d) x += y;
+  }
+  return x;
+}
+
+// Workgroup `bid`'s tile of the ragged tiling: experts one after another,
+// each cut into blocks of BM rows.  The grid holds the largest number of
+// tiles that any offsets could need (row_tiles_bound); workgroups past the
+// actual number get false.  Every wave finds the tile by itself with a scan
+// over the experts' block counts, 64 experts at a time.  Tiles are handed to
+// the XCDs (bid % 8) in contiguous runs, kGroupM blocks of rows at a time,
+// rows fastest, so the workgroups sharing an L2 share an expert's columns.
+struct RowTile {
+  int e, r0, r1, tn;  // expert, first row, end of the expert's rows, column tile
+};
+template <int BM, int kGroupM = 4>
+__device__ __forceinline__ bool row_tile(const GroupedParams& p, int bid, RowTile& t) {
+  const int lane = threadIdx.x & 63;
+  auto blocks = [&](int e) {
+    int lo, hi;
+    if (e >= p.groups) return 0;
+    expert_rows(p, e, lo, hi);
+    return (int)(((int64_t)hi - lo + BM - 1) / BM);
+  };
+  int total = 0, incl = 0;
+  for (int g0 = 0; g0 < p.groups; g0 += 64) {
+    incl = wave_scan(blocks(g0 + lane), lane);
+    total += __builtin_amdgcn_readlane(incl, 63);
+  }
+  const int64_t tiles = (int64_t)total * p.tiles_n;
+  if (bid >= tiles) return false;
+  const int per = (int)(tiles / 8), rest = (int)(tiles % 8), xcd = bid & 7;
+  const int id = xcd * per + min(xcd, rest) + (bid >> 3);
+  const int per_group = kGroupM * p.tiles_n;
+  const int first = (id / per_group) * kGroupM;
+  const int gm = min(total - first, kGroupM);
+  const int in = id % per_group;
+  const int tm = first + in % gm;
+  t.tn = in / gm;
+  int before = 0;
+  for (int g0 = 0; g0 < p.groups; g0 += 64) {
+    if (p.groups > 64) incl = wave_scan(blocks(g0 + lane), lane);
+    const uint64_t mask = __ballot(tm < before + incl);
+    if (mask) {
+      const int l = __builtin_ctzll(mask);
+      const int excl = l ? __builtin_amdgcn_readlane(incl, l - 1) : 0;
+      t.e = g0 + l;
+      int lo, hi;
+      expert_rows(p, t.e, lo, hi);
+      t.r0 = __builtin_amdgcn_readfirstlane(lo + (tm - before - excl) * BM);
+      t.r1 = __builtin_amdgcn_readfirstlane(hi);
+      return true;
+    }
+    before += __builtin_amdgcn_readlane(incl, 63);
+  }
+  return false;
+}
+
+// Blocks of BM rows that `rows` rows in `groups` groups can need: every
+// non-empty group's last block may hold a single row.
+int64_t row_tiles_bound(int64_t rows, int64_t groups, int64_t BM) {
+  const int64_t live = rows < groups ? rows : groups;
+  return (rows + live * (BM - 1)) / BM;
+}
+
+// ---------------------------------------------------------------- epilogue
+// Activations that hand a NaN on (a comparison with NaN is false, so it
+// takes the last branch).  gelu's erfc form is gemm_common.hpp's, with the
+// same |error| <= 3e-7 in Phi.
+__device__ __forceinline__ float relu_nan(float y) { return y < 0.f ? 0.f : y; }
+
+// h = erfc(|y| / sqrt 2) / 2 and, in `pe`, e^(-y^2/2)
+__device__ __forceinline__ float half_erfc(float ay, float& pe) {
+  const float b = ay * 0.8493218003f;  // |y| sqrt(log2(e) / 2)
+  const float t = __builtin_amdgcn_rcpf(fmaf(0.2727374809f, b, 1.0f));
+  float q = fmaf(t, 0.5307027145f, -0.7265760135f);
+  q = fmaf(t, q, 0.7107068705f);
+  q = fmaf(t, q, -0.142248368f);
+  q = fmaf(t, q, 0.127414796f);
+  pe = __builtin_amdgcn_exp2f(b * -b);
+  return q * t * pe;
+}
+__device__ __forceinline__ float gelu_nan(float y) {
+  const float ay = fminf(fabsf(y), 3.40282347e38f);
+  float pe;
+  const float h = half_erfc(ay, pe);
+  return fmaf(-ay, h, relu_nan(y));
+}
+// d/dz z Phi(z) = Phi(z) + z e^(-z^2/2) / sqrt(2 pi), Phi = h or 1 - h.
+// |z| is clamped to the largest float, where e^(-z^2/2) is 0.
+__device__ __forceinline__ float gelu_slope(float z) {
+  const float az = fminf(fabsf(z), 3.40282347e38f);
+  float pe;
+  const float h = half_erfc(az, pe);
+  const float s = fmaf(az * 0.3989422804f, pe, -h);  // odd part: slope = 1 + s or -s
+  return z != z ? z : (z < 0.f ? -s : 1.f + s);
+}
+
+// 16 bytes from an even address (one load: vector loads need no alignment
+// beyond the element's here)
+__device__ __forceinline__ i32x4 load16_even(const uint8_t* p) {
+  typedef int i32x4_a2 __attribute__((ext_vector_type(4), aligned(2)));
+  return *(const i32x4_a2*)p;
+}
+
+// A wave's 32 FM x 32 FN piece of D in 16-bit form in its LDS region: rows
+// of 64 FN bytes, the 16-byte chunks XOR-swizzled by row so that the
+// lane-per-row accesses of the MFMA layout fall into distinct banks.  Lane l
+// holds row 32 i + l % 32, columns 32 j + 8 g + 4 (l / 32) .. + 3.
+template <int FM, int FN>
+struct WaveRegion {
+  static constexpr int kRowB = 64 * FN, kCh = kRowB / 16, kRowsPerKiB = 1024 / kRowB;
+  static constexpr int kIters = 32 * FM * kRowB / 1024;
+  static_assert(kCh == 4 || kCh == 8 || kCh == 16, "row width");
+  static __device__ __forceinline__ int swz(int r, int c) {
+    return c ^ ((r / (16 / kCh)) & (kCh - 1));
+  }
+  static __device__ __forceinline__ uint8_t* slot(uint8_t* region, int lane, int i, int j, int g) {
+    const int r = 32 * i + (lane & 31);
+    return region + r * kRowB + swz(r, 4 * j + g) * 16 + 8 * (lane >> 5);
+  }
+  // region -> rows x cols of a row-major 16-bit matrix at `base`, whole rows
+  // per instruction; v16: rows are 16-byte aligned
+  static __device__ __forceinline__ void store(uint8_t* base, int64_t ld, const uint8_t* region,
+                                               int lane, int rows, int cols, bool v16) {
+    const int rr = lane / kCh, cs = lane % kCh;
+#pragma unroll
+    for (int t = 0; t < kIters; ++t) {
+      const int r = kRowsPerKiB * t + rr;
+      const int c0 = 8 * swz(r, cs);
+      const i32x4 v = *(const i32x4*)(region + t * 1024 + lane * 16);
+      uint8_t* dst = base + ((int64_t)r * ld + c0) * 2;
+      if (r < rows) {
+        if (c0 + 8 <= cols) {
+          if (v16) *(i32x4*)dst = v;
+          else store16_even(dst, v);
+        } else if (c0 < cols) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (c0 + e < cols)
+              ((uint16_t*)dst)[e] = (uint16_t)((uint32_t)v[e >> 1] >> (16 * (e & 1)));
+        }
+      }
+    }
+  }
+  // the other way round; elements outside rows x cols are left as they are
+  static __device__ __forceinline__ void load(const uint8_t* base, int64_t ld, uint8_t* region,
+                                              int lane, int rows, int cols) {
+    const int rr = lane / kCh, cs = lane % kCh;
+#pragma unroll
+    for (int t = 0; t < kIters; ++t) {
+      const int r = kRowsPerKiB * t + rr;
+      const int c0 = 8 * swz(r, cs);
+      const uint8_t* src = base + ((int64_t)min(r, rows - 1) * ld + c0) * 2;
+      i32x4 x = {0, 0, 0, 0};
+      if (c0 + 8 <= cols) x = load16_even(src);
+      else if (c0 < cols) x = gather16<2>(src - c0 * 2, 2, c0, cols, cols - 1);
+      *(i32x4*)(region + t * 1024 + lane * 16) = x;
+    }
+  }
+};
+
+template <int FM, int FN, class F>
+__device__ __forceinline__ void each_group(F&& f) {
+  static_for<FM>([&](auto i) {
+    static_for<FN>([&](auto j) { static_for<4>([&](auto g) { f(i, j, g); }); });
+  });
+}
+
+// Four values of sb or bias (fp32 or 16-bit) at columns n .. n + 3 of a row
+// of N, clamped to the last column.
+__device__ __forceinline__ void load_cols(const uint8_t* base, int type, int n, int N, bool vec,
+                                          float (&x)[4]) {
+  if (vec && n + 3 < N) {
+    load4(base, type, n, x);
+  } else {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) x[q] = load_elem(base, type, min(n + q, N - 1));
+  }
+}
+
+// The grouped product's epilogue for one wave's accumulators: rows row ..,
+// columns col .. of D, the expert's rows end at r1.
+//   y = sa sb acc + bias;  D = act(y), or y act'(Z);  Z = y when it is kept.
+// fp32 throughout; one rounding to D's type at the store (Z holds y rounded
+// to the same type).  region: 64 FN x 32 FM bytes of LDS of the wave's own.
+template <int kCode, int FM, int FN>
+__device__ __forceinline__ void grouped_epilogue(const GroupedParams& p, int e, int r1, int row,
+                                                 int col, int lane,
+                                                 const typename OpAtom<kCode>::Acc (&acc)[FM][FN],
+                                                 uint8_t* region) {
+  using R = WaveRegion<FM, FN>;
+  constexpr bool kScaled = kCode == kI8 || kCode == kE4M3;
+  const int rows = min(32 * FM, r1 - row), cols = min(32 * FN, p.N - col);
+  if (rows <= 0 || cols <= 0) return;
+  const int half = lane >> 5;
+  const bool vec = p.flags & kOpVec4;
+  f32x16 y[FM][FN];
+  float sa[FM];
+  if constexpr (kScaled) {
+    static_for<FM>([&](auto i) {
+      const int r = 32 * i + (lane & 31);
+      sa[i] = p.sa ? p.sa[row + min(r, rows - 1)] : 1.f;
+    });
+  }
+  static_for<FN>([&](auto j) {
+    static_for<4>([&](auto g) {
+      float b[4] = {0.f, 0.f, 0.f, 0.f}, s[4] = {1.f, 1.f, 1.f, 1.f};
+      const int n = col + 32 * j + 8 * g + 4 * half;
+      if (p.bias)
+        load_cols(p.bias + (int64_t)e * p.N * type_bytes(p.bias_type), p.bias_type, n, p.N, vec, b);
+      if constexpr (kScaled) {
+        if (p.sb) load_cols((const uint8_t*)(p.sb + (int64_t)e * p.N), TLA_F32, n, p.N, vec, s);
+      }
+      static_for<FM>([&](auto i) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float a = (float)acc[i][j][4 * g + q];
+          if constexpr (kScaled) y[i][j][4 * g + q] = fmaf(a * sa[i], s[q], b[q]);
+          else y[i][j][4 * g + q] = a + b[q];
+        }
+      });
+    });
+  });
+  const bool bf = p.d_type == TLA_BF16, v16 = p.flags & kOpD16;
+  auto pack = [&]() {
+    auto run = [&](auto kb) {
+      each_group<FM, FN>([&](auto i, auto j, auto g) {
+        *(uint2*)R::slot(region, lane, i, j, g) =
+            uint2{pack2<kb>(y[i][j][4 * g], y[i][j][4 * g + 1]),
+                  pack2<kb>(y[i][j][4 * g + 2], y[i][j][4 * g + 3])};
+      });
+    };
+    if (bf) run(std::true_type{});
+    else run(std::false_type{});
+  };
+  auto map = [&](auto f) {
+    each_group<FM, FN>([&](auto i, auto j, auto g) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) y[i][j][4 * g + q] = f(y[i][j][4 * g + q]);
+    });
+  };
+  if (p.z_mode == TLA_Z_GRAD) {
+    R::load(p.Z + ((int64_t)row * p.ldz + col) * 2, p.ldz, region, lane, rows, cols);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    auto run = [&](auto kb, auto slope) {
+      each_group<FM, FN>([&](auto i, auto j, auto g) {
+        const uint2 u = *(const uint2*)R::slot(region, lane, i, j, g);
+        y[i][j][4 * g] *= slope(widen_lo<kb>(u.x));
+        y[i][j][4 * g + 1] *= slope(widen_hi<kb>(u.x));
+        y[i][j][4 * g + 2] *= slope(widen_lo<kb>(u.y));
+        y[i][j][4 * g + 3] *= slope(widen_hi<kb>(u.y));
+      });
+    };
+    auto relu_s = [](float z) { return z > 0.f ? 1.f : 0.f; };
+    auto gelu_s = [](float z) { return gelu_slope(z); };
+    if (p.act == TLA_ACT_RELU) {
+      if (bf) run(std::true_type{}, relu_s);
+      else run(std::false_type{}, relu_s);
+    } else if (p.act == TLA_ACT_GELU) {
+      if (bf) run(std::true_type{}, gelu_s);
+      else run(std::false_type{}, gelu_s);
+    }
+  } else {
+    if (p.z_mode == TLA_Z_STORE) {
+      pack();
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      R::store(p.Z + ((int64_t)row * p.ldz + col) * 2, p.ldz, region, lane, rows, cols, v16);
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
+    if (p.act == TLA_ACT_RELU) map([](float v) { return relu_nan(v); });
+    else if (p.act == TLA_ACT_GELU) map([](float v) { return gelu_nan(v); });
+  }
+  pack();
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  R::store(p.D + ((int64_t)row * p.ldd + col) * 2, p.ldd, region, lane, rows, cols, v16);
+}
+
+// The weight gradient's epilogue: D_e rows m .., columns n .. of M x N, row
+// major, in fp32 or rounded once to 16 bits.
+template <int FM, int FN>
+__device__ __forceinline__ void wgrad_epilogue(const GroupedParams& p, int e, int m, int n,
+                                               int lane, const f32x16 (&acc)[FM][FN],
+                                               uint8_t* region) {
+  using R = WaveRegion<FM, FN>;
+  const int rows = min(32 * FM, p.M - m), cols = min(32 * FN, p.N - n);
+  if (rows <= 0 || cols <= 0) return;
+  const int64_t at = (int64_t)e * p.stride_d + (int64_t)m * p.ldd + n;
+  const bool v16 = p.flags & kOpD16;
+  if (p.d_type == TLA_F32) {
+    float* D = (float*)p.D + at;
+    each_group<FM, FN>([&](auto i, auto j, auto g) {
+      const int r = 32 * i + (lane & 31), c = 32 * j + 8 * g + 4 * (lane >> 5);
+      if (r < rows) {
+        float* d = D + (int64_t)r * p.ldd + c;
+        if (v16 && c + 3 < cols) {
+          *(f32x4*)d = f32x4{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2],
+                             acc[i][j][4 * g + 3]};
+        } else {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (c + q < cols) d[q] = acc[i][j][4 * g + q];
+        }
+      }
+    });
+    return;
+  }
+  auto run = [&](auto kb) {
+    each_group<FM, FN>([&](auto i, auto j, auto g) {
+      *(uint2*)R::slot(region, lane, i, j, g) =
+          uint2{pack2<kb>(acc[i][j][4 * g], acc[i][j][4 * g + 1]),
+                pack2<kb>(acc[i][j][4 * g + 2], acc[i][j][4 * g + 3])};
+    });
+  };
+  if (p.d_type == TLA_BF16) run(std::true_type{});
+  else run(std::false_type{});
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  R::store(p.D + at * 2, p.ldd, region, lane, rows, cols, v16);
+}
+
+// Workgroup `bid`'s tile of the weight gradient: expert e, tile (tm, tn) of
+// its D_e; an XCD's run of tiles stays within one expert, whose rows its L2
+// then serves to all of them.
+__device__ __forceinline__ void wgrad_tile(const GroupedParams& p, int bid, int total, int& e,
+                                           int& tm, int& tn) {
+  const int per = total / 8, rest = total % 8, xcd = bid & 7;
+  const int id = xcd * per + min(xcd, rest) + (bid >> 3);
+  const int tiles = p.tiles_m * p.tiles_n;
+  e = id / tiles;
+  const int in_e = id - e * tiles;
+  const int per_group = 4 * p.tiles_n;
+  const int first = (in_e / per_group) * 4;
+  const int gm = min(p.tiles_m - first, 4);
+  const int in = in_e % per_group;
+  tm = first + in % gm;
+  tn = in / gm;
+}
+
+}  // namespace
+}  // namespace tla

@@ -1,0 +1,58 @@
+// operators.hpp -- internal launch interface of the expert-grouped and 8-bit
+// integer products and of the token quantizer (declarations and contracts:
+// include/tla.h).  Every function assumes arguments validated by
+// operators_api.cpp and returns a TLA_* status.
+#pragma once
+
+#include "kernels.hpp"
+
+namespace tla {
+
+constexpr int kI8 = TLA_I8;
+
+// Bytes of an element of any type code of the public header.
+constexpr int type_bytes(int code) {
+  return code == TLA_F32 ? 4 : (code == TLA_E4M3 || code == TLA_I8 ? 1 : 2);
+}
+
+// One problem: rows r of A, grouped by expert (rows offsets[e] .. offsets[e +
+// 1] - 1 belong to expert e; offsets == nullptr: one expert with every row).
+//   product            D[r, n] = epilogue(sum_k A[r, k] B_e(k, n))
+//   weight gradient    D_e(m, n) = sum over e's rows r of A[r, m] B[r, n]
+// For the weight gradient M x N is D_e's extent, B holds `rows` rows of N,
+// and the sum runs over the expert's rows.  Leading dimensions and strides
+// are in elements.
+struct GroupedParams {
+  const int32_t* offsets;
+  const uint8_t* A;
+  const uint8_t* B;
+  uint8_t* D;
+  uint8_t* Z;
+  const float* sa;       // per row, or null
+  const float* sb;       // groups x N, or null
+  const uint8_t* bias;   // groups x N, or null
+  float* dbias;          // groups x (extent of the gradient's dY side), or null
+  int64_t lda, ldb, stride_b, ldd, stride_d, ldz;
+  int groups, rows, M, N, K;
+  int d_type, bias_type, act, z_mode;
+  int tiles_m, tiles_n;  // weight gradient: tiles of one D_e; product: tiles_n only
+  int flags;
+};
+enum : int {
+  kOpD16 = 1,    // D (and Z) rows are 16-byte aligned
+  kOpVec4 = 2,   // sb and bias rows allow aligned 4-element vectors
+};
+
+// The register-staged kernel: any order, pitch, alignment (b_kc: B is
+// K-contiguous).
+int launch_grouped_general(const GroupedParams& p, int type, bool b_kc, hipStream_t stream);
+int launch_wgrad_general(const GroupedParams& p, int type, hipStream_t stream);
+
+// dbias[e, n] = sum over e's rows of Y[r, n]
+int launch_group_colsum(const GroupedParams& p, const uint8_t* Y, int64_t ldy, int type, int N,
+                        hipStream_t stream);
+
+int launch_quantize_rows(int64_t M, int64_t K, const void* X, int type, int64_t ldx, int8_t* Q,
+                         int64_t ldq, float* scale, hipStream_t stream);
+
+}  // namespace tla

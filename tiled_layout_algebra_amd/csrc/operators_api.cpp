@@ -1,0 +1,213 @@
+// operators_api.cpp -- the C entry points of the expert-grouped and 8-bit
+// integer products and of the token quantizer: argument validation, status
+// codes and the choice of kernel.  Contracts: include/tla.h.
+#include <string.h>
+
+#include "operators.hpp"
+
+using namespace tla;
+
+namespace {
+
+constexpr int64_t kLimit = int64_t(1) << 31;
+// products of int8 values sum exactly in 32 bits while K * 128 * 128 < 2^31
+constexpr int64_t kMaxKI8 = 131071;
+
+bool out16(int t) { return t == TLA_F16 || t == TLA_BF16; }
+bool aux_type(int t) { return out16(t) || t == TLA_F32; }
+
+bool aligned_to(const void* p, int64_t bytes) { return (uintptr_t)p % (uintptr_t)bytes == 0; }
+
+// what a validated call runs
+enum Kernel { kNoop, kGeneral };
+const char* const kNames[] = {"noop", "grouped_general_128x128"};
+
+struct Plan {
+  GroupedParams p;
+  int type;
+  bool b_kc;
+  Kernel kernel;
+};
+
+int plan_product(const tla_grouped_gemm_args* a, Plan* out) {
+  if (!a) return TLA_ERR_INVALID_ARG;
+  if (a->groups < 0 || a->rows < 0 || a->N < 0 || a->K < 0) return TLA_ERR_INVALID_ARG;
+  if (a->b_order != TLA_ROW_MAJOR && a->b_order != TLA_COL_MAJOR) return TLA_ERR_INVALID_ARG;
+  if (a->act < TLA_ACT_NONE || a->act > TLA_ACT_GELU) return TLA_ERR_INVALID_ARG;
+  if (a->z_mode < TLA_Z_NONE || a->z_mode > TLA_Z_GRAD) return TLA_ERR_INVALID_ARG;
+  const bool eight = a->type == TLA_E4M3 || a->type == TLA_I8;
+  if (!eight && !out16(a->type)) return TLA_ERR_UNSUPPORTED;
+  if (!out16(a->d_type)) return TLA_ERR_UNSUPPORTED;
+  if (a->bias && !aux_type(a->bias_type)) return TLA_ERR_UNSUPPORTED;
+  if (!eight && (a->scale_a || a->scale_b)) return TLA_ERR_UNSUPPORTED;
+  if (a->groups >= kLimit || a->rows >= kLimit || a->N >= kLimit || a->K >= kLimit)
+    return TLA_ERR_UNSUPPORTED;
+  if (a->type == TLA_I8 && a->K > kMaxKI8) return TLA_ERR_UNSUPPORTED;
+  *out = Plan{};
+  out->kernel = kNoop;
+  if (a->groups == 0 || a->rows == 0 || a->N == 0) return TLA_OK;
+  if (!a->offsets && a->groups != 1) return TLA_ERR_INVALID_ARG;
+  if (!a->D || a->ldd < a->N) return TLA_ERR_INVALID_ARG;
+  const bool b_kc = a->b_order == TLA_COL_MAJOR;
+  if (a->K > 0) {
+    if (!a->A || !a->B || a->lda < a->K || a->ldb < (b_kc ? a->K : a->N) || a->stride_b < 0)
+      return TLA_ERR_INVALID_ARG;
+  }
+  // without an activation its derivative is 1 and Z is not needed
+  const int z_mode = a->z_mode == TLA_Z_GRAD && a->act == TLA_ACT_NONE ? TLA_Z_NONE : a->z_mode;
+  if (z_mode != TLA_Z_NONE && (!a->Z || a->ldz < a->N || a->Z == a->D))
+    return TLA_ERR_INVALID_ARG;
+  const int eb = type_bytes(a->type), bb = type_bytes(a->bias_type);
+  if (!aligned_to(a->offsets, 4) || !aligned_to(a->A, eb) || !aligned_to(a->B, eb) ||
+      !aligned_to(a->D, 2) || (z_mode != TLA_Z_NONE && !aligned_to(a->Z, 2)) ||
+      !aligned_to(a->scale_a, 4) || !aligned_to(a->scale_b, 4) ||
+      (a->bias && !aligned_to(a->bias, bb)))
+    return TLA_ERR_INVALID_ARG;
+  GroupedParams& p = out->p;
+  p.offsets = a->offsets;
+  p.A = (const uint8_t*)a->A;
+  p.B = (const uint8_t*)a->B;
+  p.D = (uint8_t*)a->D;
+  p.Z = z_mode == TLA_Z_NONE ? nullptr : (uint8_t*)a->Z;
+  p.sa = a->scale_a;
+  p.sb = a->scale_b;
+  p.bias = (const uint8_t*)a->bias;
+  p.lda = a->lda;
+  p.ldb = a->ldb;
+  p.stride_b = a->stride_b;
+  p.ldd = a->ldd;
+  p.ldz = a->ldz;
+  p.groups = (int)a->groups;
+  p.rows = (int)a->rows;
+  p.N = (int)a->N;
+  p.K = (int)a->K;
+  p.d_type = a->d_type;
+  p.bias_type = a->bias_type;
+  p.act = a->act;
+  p.z_mode = z_mode;
+  if (a->ldd % 8 == 0 && aligned_to(a->D, 16) && (!p.Z || (a->ldz % 8 == 0 && aligned_to(p.Z, 16))))
+    p.flags |= kOpD16;
+  if ((a->N % 4 == 0 || a->groups == 1) && aligned_to(a->scale_b, 16) &&
+      (!a->bias || aligned_to(a->bias, 4 * bb)))
+    p.flags |= kOpVec4;
+  out->type = a->type;
+  out->b_kc = b_kc;
+  out->kernel = kGeneral;
+  return TLA_OK;
+}
+
+int run_product(const tla_grouped_gemm_args* a, hipStream_t stream) {
+  Plan plan;
+  const int rc = plan_product(a, &plan);
+  if (rc) return rc;
+  switch (plan.kernel) {
+    case kNoop: return TLA_OK;
+    case kGeneral: return launch_grouped_general(plan.p, plan.type, plan.b_kc, stream);
+  }
+  return TLA_ERR_UNSUPPORTED;
+}
+
+}  // namespace
+
+extern "C" {
+
+int tla_grouped_gemm(const tla_grouped_gemm_args* args, void* stream) {
+  return run_product(args, (hipStream_t)stream);
+}
+
+int tla_grouped_gemm_variant(const tla_grouped_gemm_args* args, char* buf, int32_t cap) {
+  if (!buf || cap < 1) return TLA_ERR_INVALID_ARG;
+  Plan plan;
+  const int rc = plan_product(args, &plan);
+  if (rc) return rc;
+  strncpy(buf, kNames[plan.kernel], (size_t)cap - 1);
+  buf[cap - 1] = '\0';
+  return TLA_OK;
+}
+
+int tla_gemm_i8(const tla_gemm_i8_args* a, void* stream) {
+  if (!a) return TLA_ERR_INVALID_ARG;
+  tla_grouped_gemm_args g{};
+  g.groups = 1;
+  g.rows = a->M;
+  g.N = a->N;
+  g.K = a->K;
+  g.A = a->A;
+  g.type = TLA_I8;
+  g.lda = a->lda;
+  g.B = a->B;
+  g.b_order = a->b_order;
+  g.ldb = a->ldb;
+  g.D = a->D;
+  g.d_type = a->d_type;
+  g.ldd = a->ldd;
+  g.scale_a = a->scale_a;
+  g.scale_b = a->scale_b;
+  g.bias = a->bias;
+  g.bias_type = a->bias_type;
+  g.act = a->act;
+  return run_product(&g, (hipStream_t)stream);
+}
+
+int tla_grouped_gemm_wgrad(const tla_grouped_wgrad_args* a, void* stream) {
+  if (!a) return TLA_ERR_INVALID_ARG;
+  if (a->groups < 0 || a->rows < 0 || a->N < 0 || a->K < 0) return TLA_ERR_INVALID_ARG;
+  if (a->d_order != TLA_ROW_MAJOR && a->d_order != TLA_COL_MAJOR) return TLA_ERR_INVALID_ARG;
+  if (!out16(a->type) || !aux_type(a->d_type)) return TLA_ERR_UNSUPPORTED;
+  if (a->groups >= kLimit || a->rows >= kLimit || a->N >= kLimit || a->K >= kLimit)
+    return TLA_ERR_UNSUPPORTED;
+  const bool has_d = a->K > 0 && a->N > 0, has_bias = a->dbias && a->N > 0;
+  if (a->groups == 0 || (!has_d && !has_bias)) return TLA_OK;
+  if (a->groups > 65535 && has_bias) return TLA_ERR_UNSUPPORTED;
+  if (!a->offsets && a->groups != 1) return TLA_ERR_INVALID_ARG;
+  if (a->rows > 0 && (!a->Y || a->ldy < a->N)) return TLA_ERR_INVALID_ARG;
+  const bool row = a->d_order == TLA_ROW_MAJOR;
+  if (has_d) {
+    const int64_t outer = row ? a->K : a->N, inner = row ? a->N : a->K;
+    if (!a->D || a->ldd < inner) return TLA_ERR_INVALID_ARG;
+    if (a->rows > 0 && (!a->A || a->lda < a->K)) return TLA_ERR_INVALID_ARG;
+    // the experts' matrices must not overlap
+    if (a->groups > 1 && a->stride_d < (outer - 1) * a->ldd + inner) return TLA_ERR_INVALID_ARG;
+  }
+  const int db = type_bytes(a->d_type);
+  if (!aligned_to(a->offsets, 4) || !aligned_to(a->A, 2) || !aligned_to(a->Y, 2) ||
+      !aligned_to(a->D, db) || !aligned_to(a->dbias, 4))
+    return TLA_ERR_INVALID_ARG;
+  GroupedParams p{};
+  p.offsets = a->offsets;
+  p.groups = (int)a->groups;
+  p.rows = (int)a->rows;
+  p.dbias = a->dbias;
+  p.D = (uint8_t*)a->D;
+  p.d_type = a->d_type;
+  p.ldd = a->ldd;
+  p.stride_d = a->stride_d;
+  // a column-major D_e is the row-major product of the operands swapped
+  p.A = (const uint8_t*)(row ? a->A : a->Y);
+  p.B = (const uint8_t*)(row ? a->Y : a->A);
+  p.lda = row ? a->lda : a->ldy;
+  p.ldb = row ? a->ldy : a->lda;
+  p.M = (int)(row ? a->K : a->N);
+  p.N = (int)(row ? a->N : a->K);
+  const int per16 = 16 / db;
+  if (a->ldd % per16 == 0 && a->stride_d % per16 == 0 && aligned_to(a->D, 16)) p.flags |= kOpD16;
+  if (has_bias) {
+    const int rc = launch_group_colsum(p, (const uint8_t*)a->Y, a->ldy, a->type, (int)a->N,
+                                       (hipStream_t)stream);
+    if (rc) return rc;
+  }
+  return has_d ? launch_wgrad_general(p, a->type, (hipStream_t)stream) : TLA_OK;
+}
+
+int tla_quantize_rows(int64_t M, int64_t K, const void* X, int32_t x_type, int64_t ldx, void* Q,
+                      int64_t ldq, float* scale, void* stream) {
+  if (M < 0 || K < 0) return TLA_ERR_INVALID_ARG;
+  if (!aux_type(x_type)) return TLA_ERR_UNSUPPORTED;
+  if (M == 0) return TLA_OK;
+  if (!scale || !aligned_to(scale, 4)) return TLA_ERR_INVALID_ARG;
+  if (K > 0 && (!X || !Q || ldx < K || ldq < K || !aligned_to(X, type_bytes(x_type))))
+    return TLA_ERR_INVALID_ARG;
+  return launch_quantize_rows(M, K, X, x_type, ldx, (int8_t*)Q, ldq, scale, (hipStream_t)stream);
+}
+
+}  // extern "C"
