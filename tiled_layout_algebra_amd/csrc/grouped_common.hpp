@@ -249,16 +249,92 @@ __device__ __forceinline__ void each_group(F&& f) {
   });
 }
 
-// Four values of sb or bias (fp32 or 16-bit) at columns n .. n + 3 of a row
-// of N, clamped to the last column.
-__device__ __forceinline__ void load_cols(const uint8_t* base, int type, int n, int N, bool vec,
-                                          float (&x)[4]) {
-  if (vec && n + 3 < N) {
-    load4(base, type, n, x);
-  } else {
-#pragma unroll
-    for (int q = 0; q < 4; ++q) x[q] = load_elem(base, type, min(n + q, N - 1));
+// Scale and bias of a lane's four column groups of fragment j: columns
+// n + 8 g .. + 3 of a row of N, clamped to the last column.
+struct ColumnTerms {
+  f32x4 s[4], b[4];
+};
+template <bool kScaled>
+__device__ __forceinline__ void load_columns(const GroupedParams& p, int e, int n, ColumnTerms& t) {
+  const bool vec = (p.flags & kOpVec4) && n + 27 < p.N;
+  static_for<4>([&](auto g) {
+    t.s[g] = f32x4{1.f, 1.f, 1.f, 1.f};
+    t.b[g] = f32x4{0.f, 0.f, 0.f, 0.f};
+  });
+  auto fetch = [&](const uint8_t* base, int type, f32x4 (&x)[4]) {
+    if (vec && type == TLA_F32) {
+      static_for<4>([&](auto g) { x[g] = *(const f32x4*)((const float*)base + n + 8 * g); });
+    } else if (vec) {
+      uint2 u[4];
+      static_for<4>([&](auto g) { u[g] = *(const uint2*)((const uint16_t*)base + n + 8 * g); });
+      static_for<4>([&](auto g) {
+        x[g] = type == TLA_BF16
+                   ? f32x4{widen_lo<true>(u[g].x), widen_hi<true>(u[g].x), widen_lo<true>(u[g].y),
+                           widen_hi<true>(u[g].y)}
+                   : f32x4{widen_lo<false>(u[g].x), widen_hi<false>(u[g].x),
+                           widen_lo<false>(u[g].y), widen_hi<false>(u[g].y)};
+      });
+    } else {
+      static_for<4>([&](auto g) {
+        static_for<4>([&](auto q) { x[g][(int)q] = load_elem(base, type, min(n + 8 * g + q, p.N - 1)); });
+      });
+    }
+  };
+  if (p.bias) fetch(p.bias + (int64_t)e * p.N * type_bytes(p.bias_type), p.bias_type, t.b);
+  if constexpr (kScaled) {
+    if (p.sb) fetch((const uint8_t*)(p.sb + (int64_t)e * p.N), TLA_F32, t.s);
   }
+}
+
+// What the epilogue makes of y: itself, its activation, or y times the
+// activation's derivative at a stored z.
+enum EpiOp : int { kSame, kRelu, kGelu, kReluGrad, kGeluGrad };
+template <int kOp>
+__device__ __forceinline__ float epi_op(float y, float z) {
+  if constexpr (kOp == kRelu) return relu_nan(y);
+  if constexpr (kOp == kGelu) return gelu_nan(y);
+  if constexpr (kOp == kReluGrad) return y * (z > 0.f ? 1.f : 0.f);
+  if constexpr (kOp == kGeluGrad) return y * gelu_slope(z);
+  return y;
+}
+
+// One pass over a wave's accumulators into its region: op(sa s acc + b), four
+// columns at a time, in the MFMA layout; the derivatives read their z from
+// the slot they write.  A fragment's column terms are loaded while the one
+// before it is worked on.
+template <int kCode, int kOp, bool kBf, int FM, int FN>
+__device__ __forceinline__ void epilogue_pass(const GroupedParams& p, int e, int col, int lane,
+                                              const typename OpAtom<kCode>::Acc (&acc)[FM][FN],
+                                              const float (&sa)[FM], uint8_t* region) {
+  using R = WaveRegion<FM, FN>;
+  constexpr bool kScaled = kCode == kI8 || kCode == kE4M3;
+  constexpr bool kSlope = kOp == kReluGrad || kOp == kGeluGrad;
+  const int n0 = col + 4 * (lane >> 5);
+  ColumnTerms t[2];
+  load_columns<kScaled>(p, e, n0, t[0]);
+  static_for<FN>([&](auto j) {
+    if constexpr (j + 1 < FN) load_columns<kScaled>(p, e, n0 + 32 * (j + 1), t[(j + 1) & 1]);
+    const ColumnTerms& c = t[j & 1];
+    static_for<4>([&](auto g) {
+      static_for<FM>([&](auto i) {
+        uint8_t* slot = R::slot(region, lane, i, j, g);
+        float z[4] = {0.f, 0.f, 0.f, 0.f}, y[4];
+        if constexpr (kSlope) {
+          const uint2 u = *(const uint2*)slot;
+          z[0] = widen_lo<kBf>(u.x);
+          z[1] = widen_hi<kBf>(u.x);
+          z[2] = widen_lo<kBf>(u.y);
+          z[3] = widen_hi<kBf>(u.y);
+        }
+        static_for<4>([&](auto q) {
+          const float a = (float)acc[i][j][4 * g + q];
+          const float v = kScaled ? fmaf(a * sa[i], c.s[g][(int)q], c.b[g][(int)q]) : a + c.b[g][(int)q];
+          y[q] = epi_op<kOp>(v, z[q]);
+        });
+        *(uint2*)slot = uint2{pack2<kBf>(y[0], y[1]), pack2<kBf>(y[2], y[3])};
+      });
+    });
+  });
 }
 
 // The grouped product's epilogue for one wave's accumulators: rows row ..,
@@ -272,90 +348,34 @@ __device__ __forceinline__ void grouped_epilogue(const GroupedParams& p, int e, 
                                                  const typename OpAtom<kCode>::Acc (&acc)[FM][FN],
                                                  uint8_t* region) {
   using R = WaveRegion<FM, FN>;
-  constexpr bool kScaled = kCode == kI8 || kCode == kE4M3;
   const int rows = min(32 * FM, r1 - row), cols = min(32 * FN, p.N - col);
   if (rows <= 0 || cols <= 0) return;
-  const int half = lane >> 5;
-  const bool vec = p.flags & kOpVec4;
-  f32x16 y[FM][FN];
-  float sa[FM];
-  if constexpr (kScaled) {
-    static_for<FM>([&](auto i) {
-      const int r = 32 * i + (lane & 31);
-      sa[i] = p.sa ? p.sa[row + min(r, rows - 1)] : 1.f;
-    });
-  }
-  static_for<FN>([&](auto j) {
-    static_for<4>([&](auto g) {
-      float b[4] = {0.f, 0.f, 0.f, 0.f}, s[4] = {1.f, 1.f, 1.f, 1.f};
-      const int n = col + 32 * j + 8 * g + 4 * half;
-      if (p.bias)
-        load_cols(p.bias + (int64_t)e * p.N * type_bytes(p.bias_type), p.bias_type, n, p.N, vec, b);
-      if constexpr (kScaled) {
-        if (p.sb) load_cols((const uint8_t*)(p.sb + (int64_t)e * p.N), TLA_F32, n, p.N, vec, s);
-      }
-      static_for<FM>([&](auto i) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const float a = (float)acc[i][j][4 * g + q];
-          if constexpr (kScaled) y[i][j][4 * g + q] = fmaf(a * sa[i], s[q], b[q]);
-          else y[i][j][4 * g + q] = a + b[q];
-        }
-      });
-    });
-  });
   const bool bf = p.d_type == TLA_BF16, v16 = p.flags & kOpD16;
-  auto pack = [&]() {
-    auto run = [&](auto kb) {
-      each_group<FM, FN>([&](auto i, auto j, auto g) {
-        *(uint2*)R::slot(region, lane, i, j, g) =
-            uint2{pack2<kb>(y[i][j][4 * g], y[i][j][4 * g + 1]),
-                  pack2<kb>(y[i][j][4 * g + 2], y[i][j][4 * g + 3])};
-      });
-    };
-    if (bf) run(std::true_type{});
-    else run(std::false_type{});
-  };
-  auto map = [&](auto f) {
-    each_group<FM, FN>([&](auto i, auto j, auto g) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q) y[i][j][4 * g + q] = f(y[i][j][4 * g + q]);
-    });
+  float sa[FM];
+  static_for<FM>([&](auto i) {
+    sa[i] = p.sa ? p.sa[row + min(32 * (int)i + (lane & 31), rows - 1)] : 1.f;
+  });
+  auto fence = [&]() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); };
+  auto pass = [&](auto op, uint8_t* out, int64_t ld) {
+    if (bf) epilogue_pass<kCode, op, true, FM, FN>(p, e, col, lane, acc, sa, region);
+    else epilogue_pass<kCode, op, false, FM, FN>(p, e, col, lane, acc, sa, region);
+    fence();
+    R::store(out + ((int64_t)row * ld + col) * 2, ld, region, lane, rows, cols, v16);
   };
   if (p.z_mode == TLA_Z_GRAD) {
     R::load(p.Z + ((int64_t)row * p.ldz + col) * 2, p.ldz, region, lane, rows, cols);
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    auto run = [&](auto kb, auto slope) {
-      each_group<FM, FN>([&](auto i, auto j, auto g) {
-        const uint2 u = *(const uint2*)R::slot(region, lane, i, j, g);
-        y[i][j][4 * g] *= slope(widen_lo<kb>(u.x));
-        y[i][j][4 * g + 1] *= slope(widen_hi<kb>(u.x));
-        y[i][j][4 * g + 2] *= slope(widen_lo<kb>(u.y));
-        y[i][j][4 * g + 3] *= slope(widen_hi<kb>(u.y));
-      });
-    };
-    auto relu_s = [](float z) { return z > 0.f ? 1.f : 0.f; };
-    auto gelu_s = [](float z) { return gelu_slope(z); };
-    if (p.act == TLA_ACT_RELU) {
-      if (bf) run(std::true_type{}, relu_s);
-      else run(std::false_type{}, relu_s);
-    } else if (p.act == TLA_ACT_GELU) {
-      if (bf) run(std::true_type{}, gelu_s);
-      else run(std::false_type{}, gelu_s);
-    }
-  } else {
-    if (p.z_mode == TLA_Z_STORE) {
-      pack();
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      R::store(p.Z + ((int64_t)row * p.ldz + col) * 2, p.ldz, region, lane, rows, cols, v16);
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    }
-    if (p.act == TLA_ACT_RELU) map([](float v) { return relu_nan(v); });
-    else if (p.act == TLA_ACT_GELU) map([](float v) { return gelu_nan(v); });
+    fence();
+    if (p.act == TLA_ACT_RELU) pass(std::integral_constant<int, kReluGrad>{}, p.D, p.ldd);
+    else pass(std::integral_constant<int, kGeluGrad>{}, p.D, p.ldd);
+    return;
   }
-  pack();
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  R::store(p.D + ((int64_t)row * p.ldd + col) * 2, p.ldd, region, lane, rows, cols, v16);
+  if (p.z_mode == TLA_Z_STORE) {
+    pass(std::integral_constant<int, kSame>{}, p.Z, p.ldz);
+    fence();
+  }
+  if (p.act == TLA_ACT_RELU) pass(std::integral_constant<int, kRelu>{}, p.D, p.ldd);
+  else if (p.act == TLA_ACT_GELU) pass(std::integral_constant<int, kGelu>{}, p.D, p.ldd);
+  else pass(std::integral_constant<int, kSame>{}, p.D, p.ldd);
 }
 
 // The weight gradient's epilogue: D_e rows m .., columns n .. of M x N, row

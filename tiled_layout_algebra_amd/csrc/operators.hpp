@@ -48,6 +48,18 @@ enum : int {
 int launch_grouped_general(const GroupedParams& p, int type, bool b_kc, hipStream_t stream);
 int launch_wgrad_general(const GroupedParams& p, int type, hipStream_t stream);
 
+// The 256 x 256 direct-copy kernel (grouped_two_group.hip).  Product: A and,
+// with b_kc, B have 16-byte aligned rows of a multiple of 16 bytes of K below
+// 64 MiB each; otherwise B is 16-bit with 16-byte aligned rows, N a multiple
+// of 8, a matrix below 2 GiB.  Gradient: both operands have such rows, M and
+// N multiples of 8, each operand below 2 GiB.
+int launch_grouped_two_group(const GroupedParams& p, int type, bool b_kc, hipStream_t stream);
+int launch_wgrad_two_group(const GroupedParams& p, int type, hipStream_t stream);
+
+// The kernel for few rows an expert (grouped_few_rows.hip): B K-contiguous,
+// any pitch and alignment; blocks of 16 mt rows, mt 1, 2 or 4.
+int launch_grouped_few_rows(const GroupedParams& p, int type, int mt, hipStream_t stream);
+
 // dbias[e, n] = sum over e's rows of Y[r, n]
 int launch_group_colsum(const GroupedParams& p, const uint8_t* Y, int64_t ldy, int type, int N,
                         hipStream_t stream);
