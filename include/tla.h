@@ -233,6 +233,30 @@ int tla_grouped_gemm(const tla_grouped_gemm_args *args, void *stream);
 int tla_grouped_gemm_variant(const tla_grouped_gemm_args *args, char *buf, int32_t cap);
 
 /*
+ * The kernels, for comparison and testing:
+ *   0 "grouped_general_128x128"          any order, pitch, alignment
+ *   1 "grouped_two_group_256x256"        direct copies: 16-byte aligned rows
+ *                                        less than 8 MiB apart, K a multiple
+ *                                        of 16 bytes; b_order TLA_ROW_MAJOR:
+ *                                        16-bit, N a multiple of 8, each B_e
+ *                                        below 2 GiB
+ *   2 "grouped_direct_128x128"           the same
+ *   3 "grouped_direct_64x128"            the same, TLA_COL_MAJOR only
+ *   4 "grouped_few_rows_64"              blocks of 64, 32 and 16 rows, weights
+ *   5 "grouped_few_rows_32"              straight to registers; any alignment,
+ *   6 "grouped_few_rows_16"              K > 0, TLA_COL_MAJOR only
+ *   7 "grouped_two_group_shift_256x256"  variant 1 for any alignment, K > 0,
+ *                                        TLA_COL_MAJOR only
+ * (1, 2, 3 and 7 take e4m3 with K >= 512 only.)  tla_grouped_gemm takes the
+ * one with the smallest estimated time; tla_grouped_gemm_run_variant runs the
+ * one asked for, with the same semantics, or returns TLA_ERR_UNSUPPORTED when
+ * the problem does not meet its conditions.  Ids outside
+ * [0, TLA_GROUPED_VARIANTS) are TLA_ERR_INVALID_ARG.
+ */
+#define TLA_GROUPED_VARIANTS 8
+int tla_grouped_gemm_run_variant(const tla_grouped_gemm_args *args, int32_t variant, void *stream);
+
+/*
  * The weight and bias gradients of a grouped product:
  *   D_e[k, n] = sum over e's rows r of A[r, k] Y[r, n]     (K x N)
  *   dbias[e, n] = sum over e's rows r of Y[r, n]           (fp32, or NULL)

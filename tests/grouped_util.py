@@ -97,7 +97,7 @@ class Product:
                      if bias else None)
         self.Z = torch.randn(self.rows, N, generator=gen).to(TORCH[self.d_type])
 
-    def call(self, stream=None, variant_only=False):
+    def call(self, stream=None, variant=None):
         pad, sh = self.pad, self.shift
         A, _ = pitched(self.A[None], self.K + pad, self.kind)
         kn = self.B if self.order == tla.ROW_MAJOR else self.B.view(
@@ -117,9 +117,7 @@ class Product:
                 shifted(B, sh), self.order, ldb, stride_b, self.D, self.d_type, ldd)
         kw = dict(scale_a=up(self.sa), scale_b=up(self.sb, sh), bias=up(self.bias, sh),
                   bias_type=self.bias_type, Z=self.Zd, ldz=ldd, z_mode=self.z, act=self.act)
-        if variant_only:
-            return tla.grouped_gemm_variant(*args, **kw)
-        tla.grouped_gemm(*args, stream=stream, **kw)
+        tla.grouped_gemm(*args, stream=stream, variant=variant, **kw)
         self.keep = (args, kw)
         return self
 

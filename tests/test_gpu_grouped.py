@@ -292,3 +292,52 @@ def test_gradient_order_is_fixed():
                                tla.ROW_MAJOR, 128, 256 * 128, dbias=db)
         outs.append((D, db))
     assert all(torch.equal(a, b) for o in outs[1:] for a, b in zip(outs[0], o))
+
+
+def _takes(variant, kind, order, N, K, pad, shift):
+    """The conditions include/tla.h names."""
+    eb = 1 if kind in (tla.E4M3, tla.I8) else 2
+    nk = order == tla.COL_MAJOR
+    if variant == 0:
+        return True
+    if variant in (4, 5, 6):
+        return nk
+    if kind == tla.E4M3 and K < 512:
+        return False
+    if variant == 7:
+        return nk
+    ldb = (K if nk else N) + pad
+    aligned = all(x * eb % 16 == 0 for x in (K, K + pad, ldb, shift, pad))
+    if variant == 3 and not nk:
+        return False
+    return aligned and (nk or (eb == 2 and N % 8 == 0))
+
+
+@pytest.mark.parametrize("variant", range(tla.GROUPED_VARIANTS))
+@pytest.mark.parametrize("kind", TYPES, ids=IDS.get)
+@pytest.mark.parametrize("order", [tla.COL_MAJOR, tla.ROW_MAJOR], ids=["nk", "kn"])
+@pytest.mark.parametrize("N,K,pad,shift", [
+    (40, 16, 0, 0), (300, 96, 0, 0), (264, 576, 0, 0), (136, 1040, 16, 16), (7, 47, 0, 0),
+    (300, 97, 1, 1), (129, 511, 2, 3), (280, 1055, 3, 0), (257, 600, 5, 2)], ids=str)
+def test_every_kernel(variant, kind, order, N, K, pad, shift):
+    """Each kernel on tiles it fills and tiles it does not, K from less than a
+    step to several k-tiles, and at any byte address where it takes that: the
+    padding and the next row's bytes are poison."""
+    p = Product([300, 0, 5, 129, 1], N, K, kind, order=order, bias=True, act=tla.ACT_RELU, pad=pad,
+                shift=shift, seed=K)
+    if _takes(variant, kind, order, N, K, pad, shift):
+        p.call(variant=variant).verify()
+    else:
+        with pytest.raises(tla.TlaError) as err:
+            p.call(variant=variant)
+        assert err.value.status == tla.ERR_UNSUPPORTED
+        torch.cuda.synchronize()
+        assert (p.D == 7.0).all()
+
+
+@pytest.mark.parametrize("variant", [0, 1, 2, 3, 4, 5, 6, 7])
+def test_every_kernel_keeps_and_differentiates(variant):
+    for kind in (tla.F16, tla.I8):
+        for z in (tla.Z_STORE, tla.Z_GRAD):
+            Product([150, 3, 0, 70], 200, 512, kind, z=z, act=tla.ACT_GELU,
+                    seed=z).call(variant=variant).verify()

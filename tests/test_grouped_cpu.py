@@ -75,6 +75,47 @@ def _variant(**kw):
     return buf.value.decode()
 
 
+@pytest.mark.parametrize("kw,kernel", [
+    (dict(rows=1, groups=1), "grouped_few_rows_16"),
+    (dict(rows=4, N=4096, K=4096, lda=4096, ldb=4096, ldd=4096, stride_b=1 << 24), "grouped_few_rows_16"),
+    (dict(rows=16384, groups=8, N=4096, K=4096, lda=4096, ldb=4096, ldd=4096, stride_b=1 << 24),
+     "grouped_two_group_256x256"),
+    (dict(rows=16384, groups=8, N=4096, K=4096, lda=4096, ldb=4096, ldd=4096, stride_b=1 << 24,
+          b_order=tla.ROW_MAJOR), "grouped_two_group_256x256"),
+    (dict(rows=16384, groups=8, N=4096, K=4095, lda=4095, ldb=4095, ldd=4096, stride_b=4095 * 4096),
+     "grouped_two_group_shift_256x256"),
+    (dict(rows=16384, groups=8, N=4095, K=4096, lda=4096, ldb=4095, ldd=4095, stride_b=4095 * 4096,
+          b_order=tla.ROW_MAJOR), "grouped_general_128x128"),
+    (dict(rows=500, N=1024, K=1024, lda=1024, ldb=1024, ldd=1024, stride_b=1 << 20,
+          b_order=tla.ROW_MAJOR), "grouped_direct_128x128"),
+    (dict(rows=2048, groups=32, N=2048, K=4096, lda=4096, ldb=4096, ldd=2048, stride_b=1 << 23),
+     "grouped_direct_64x128"),
+    (dict(rows=4096, type=tla.I8, N=1024, K=1024, lda=1024, ldb=1024, ldd=1024, stride_b=1 << 20,
+          b_order=tla.ROW_MAJOR), "grouped_general_128x128"),
+    (dict(rows=4096, type=tla.E4M3, K=256, lda=256, ldb=256, N=1024, ldd=1024, stride_b=1 << 18),
+     "grouped_general_128x128"),
+    (dict(K=0, A=None, B=None), "grouped_general_128x128"),
+])
+def test_kernel_choice(kw, kernel):
+    assert _variant(**kw) == kernel
+
+
+def test_run_variant_refusals():
+    f = tla.lib().tla_grouped_gemm_run_variant
+    for v in (-1, tla.GROUPED_VARIANTS):
+        assert f(ctypes.byref(_product()), v, None) == tla.ERR_INVALID_ARG
+    assert f(ctypes.byref(_product(rows=-1)), 0, None) == tla.ERR_INVALID_ARG
+    assert f(ctypes.byref(_product(rows=0)), 3, None) == tla.OK
+    kn, odd = dict(b_order=tla.ROW_MAJOR), dict(K=63, lda=63, ldb=63)
+    wide = dict(lda=1 << 22, ldb=1 << 22)  # rows 8 MiB apart
+    e4m3 = dict(type=tla.E4M3)
+    for v, bad in ((1, [odd, wide, e4m3, dict(K=0), dict(A=FAKE + 2), dict(stride_b=4097)]),
+                   (2, [odd, dict(kn, N=63), dict(kn, type=tla.I8)]), (3, [kn, odd, dict(B=FAKE + 8)]),
+                   (4, [kn, dict(K=0)]), (5, [kn]), (6, [kn]), (7, [kn, wide, e4m3, dict(K=0)])):
+        for kw in bad:
+            assert f(ctypes.byref(_product(**kw)), v, None) == tla.ERR_UNSUPPORTED, (v, kw)
+
+
 def test_noops_and_small_buffers():
     L = tla.lib()
     for kw in (dict(rows=0), dict(N=0), dict(groups=0)):

@@ -32,8 +32,8 @@ EXPORTED = [
     "tla_thread_map_eval", "tla_logical_product", "tla_coalesce", "tla_composition",
     "tla_logical_divide_modes", "tla_thread_map_ex", "tla_thread_map_eval_ex",
     "tla_status_string", "tla_version",
-    "tla_grouped_gemm", "tla_grouped_gemm_variant", "tla_grouped_gemm_wgrad", "tla_gemm_i8",
-    "tla_quantize_rows",
+    "tla_grouped_gemm", "tla_grouped_gemm_variant", "tla_grouped_gemm_run_variant",
+    "tla_grouped_gemm_wgrad", "tla_gemm_i8", "tla_quantize_rows",
 ]
 
 
@@ -107,6 +107,7 @@ def lib() -> ctypes.CDLL:
         L.tla_grouped_gemm.argtypes = [ctypes.POINTER(GroupedGemmArgs), P]
         L.tla_grouped_gemm_variant.argtypes = [ctypes.POINTER(GroupedGemmArgs), ctypes.c_char_p,
                                                I32]
+        L.tla_grouped_gemm_run_variant.argtypes = [ctypes.POINTER(GroupedGemmArgs), I32, P]
         L.tla_grouped_gemm_wgrad.argtypes = [ctypes.POINTER(GroupedWgradArgs), P]
         L.tla_gemm_i8.argtypes = [ctypes.POINTER(GemmI8Args), P]
         L.tla_quantize_rows.argtypes = [I64, I64, P, I32, I64, P, I64, P, P]
@@ -142,12 +143,25 @@ def _dev(t, what):
     return t.data_ptr()
 
 
+_raw_stream = None
+
+
 def _stream(stream, *tensors):
+    """The given stream's address, or that of torch's current stream on the
+    first tensor's device."""
     if stream is not None:
         return int(stream)
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        # the address without a Stream object around it (2 us a call less)
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda index: torch.cuda.current_stream(index).cuda_stream)
+    for t in tensors:
+        if t is not None:
+            return _raw_stream(t.get_device())
     import torch
-    dev = next((t.device for t in tensors if t is not None), None)
-    return torch.cuda.current_stream(dev).cuda_stream
+    return _raw_stream(torch.cuda.current_device())
 
 
 # ------------------------------------------------------------------- GEMM
@@ -305,6 +319,9 @@ class GemmI8Args(ctypes.Structure):
     ]
 
 
+GROUPED_VARIANTS = 8
+
+
 def _dev32(t, kind, what):
     """_dev for a buffer whose element type the library fixes ("int32" or
     "float32"): another dtype would be misread, so it is refused."""
@@ -326,14 +343,20 @@ def _grouped_gemm_args(groups, rows, N, K, offsets, A, type, lda, B, b_order, ld
 
 def grouped_gemm(groups, rows, N, K, offsets, A, type, lda, B, b_order, ldb, stride_b, D, d_type,
                  ldd, scale_a=None, scale_b=None, bias=None, bias_type=None, Z=None, ldz=0,
-                 z_mode=Z_NONE, act=ACT_NONE, stream=None):
+                 z_mode=Z_NONE, act=ACT_NONE, stream=None, variant=None):
     """Rows grouped by expert times their expert's matrix (tla_grouped_gemm):
     z = scale_a scale_b A.B_e + bias; D = act(z), with Z = z for Z_STORE, or
     D = z act'(Z) for Z_GRAD.  offsets: int32 CUDA tensor of groups + 1
-    values (None: one expert)."""
+    values (None: one expert).  With `variant` (0 .. GROUPED_VARIANTS - 1) that
+    kernel is run (tla_grouped_gemm_run_variant)."""
     a = _grouped_gemm_args(groups, rows, N, K, offsets, A, type, lda, B, b_order, ldb, stride_b, D,
                            d_type, ldd, scale_a, scale_b, bias, bias_type, Z, ldz, z_mode, act)
-    _check(lib().tla_grouped_gemm(ctypes.byref(a), _stream(stream, A, B, D)), "tla_grouped_gemm")
+    s = _stream(stream, A, B, D)
+    if variant is None:
+        _check(lib().tla_grouped_gemm(ctypes.byref(a), s), "tla_grouped_gemm")
+    else:
+        _check(lib().tla_grouped_gemm_run_variant(ctypes.byref(a), variant, s),
+               "tla_grouped_gemm_run_variant")
 
 
 def grouped_gemm_variant(*args, **kw) -> str:

@@ -56,6 +56,20 @@ struct E4m3AsF16 {
     for (int q = 0; q < 4; ++q) MfmaAtom<kF16>::mma(acc, widen(a, q), widen(b, q));
   }
 };
+// e4m3 sixteen bytes a lane at a time, like the other types: two of the
+// unscaled 8-bit instructions.
+struct E4m3Bytes {
+  static constexpr int kK = 32;
+  static constexpr int kLaneBytes = 16;
+  typedef i32x4 Frag;
+  typedef f32x16 Acc;
+  static __device__ __forceinline__ void mma(f32x16& acc, const Frag& a, const Frag& b) {
+    typedef long i64x2 __attribute__((ext_vector_type(2)));
+    const i64x2 x = __builtin_bit_cast(i64x2, a), y = __builtin_bit_cast(i64x2, b);
+    acc = __builtin_amdgcn_mfma_f32_32x32x16_fp8_fp8(x[0], y[0], acc, 0, 0, 0);
+    acc = __builtin_amdgcn_mfma_f32_32x32x16_fp8_fp8(x[1], y[1], acc, 0, 0, 0);
+  }
+};
 // load_frag's geometry depends only on the bytes of a K step and of a lane's
 // share of it, which int8 shares with the 16-bit types.
 template <int kCode>
@@ -136,13 +150,6 @@ __device__ __forceinline__ bool row_tile(const GroupedParams& p, int bid, RowTil
     before += __builtin_amdgcn_readlane(incl, 63);
   }
   return false;
-}
-
-// Blocks of BM rows that `rows` rows in `groups` groups can need: every
-// non-empty group's last block may hold a single row.
-int64_t row_tiles_bound(int64_t rows, int64_t groups, int64_t BM) {
-  const int64_t live = rows < groups ? rows : groups;
-  return (rows + live * (BM - 1)) / BM;
 }
 
 // ---------------------------------------------------------------- epilogue

@@ -157,11 +157,15 @@ int launch(const GroupedParams& p0, hipStream_t stream) {
   return hipGetLastError() == hipSuccess ? TLA_OK : TLA_ERR_HIP;
 }
 
+// 32 columns and four waves a workgroup, or, where that would leave compute
+// units without one, 16 columns and eight waves.
 template <int kCode>
 int pick(const GroupedParams& p, int mt, hipStream_t s) {
+  const int64_t wide = (p.rows < p.groups ? p.rows : p.groups) * (int64_t)((p.N + 31) / 32);
+  if (mt == 1 && wide <= 512) return launch<kCode, 1, 1, 8>(p, s);
   if (mt == 1) return launch<kCode, 1, 2, 4>(p, s);
-  if (mt == 2) return launch<kCode, 2, 2, 4>(p, s);
-  return launch<kCode, 4, 2, 4>(p, s);
+  if (mt == 2) return wide <= 512 ? launch<kCode, 2, 1, 8>(p, s) : launch<kCode, 2, 2, 4>(p, s);
+  return wide <= 512 ? launch<kCode, 4, 1, 8>(p, s) : launch<kCode, 4, 2, 4>(p, s);
 }
 
 }  // namespace

@@ -1,396 +1,12 @@
-// grouped_two_group.hip -- the 256 x 256 kernel of the expert-grouped
-// products, for tiles enough to fill the card.
-//
-// The tile program is the two-group one of gemm_pingpong.hip: eight
-// wavefronts in two groups of four, one wave of each group on a SIMD; a group
-// alternates between a memory phase (a k-tile's fragments from LDS, the
-// direct global -> LDS copies of a later one in between) and a compute phase
-// (the k-tile's 32 MFMAs, nothing else), half a period apart from the other
-// group, so that one multiplies while the other moves data.  LDS holds two A
-// slabs and three B slabs of 128 bytes of K: all 160 KiB.  What differs:
-//   tiles     come from the ragged lookup, so the last block of an expert's
-//             rows ends inside the tile; copies past it read zeros through
-//             the buffer range check, and waves without a row skip their
-//             MFMAs
-//   kNK, kKN  the product with B K-contiguous ([N, K] weights) or
-//             N-contiguous (16-bit [K, N] weights: a slab of k rows, read
-//             back by transposing LDS reads)
-//   kGrad     the weight gradient: the sum runs over the expert's rows, both
-//             operands are slabs of k rows, and the rows past the expert's
-//             last lie past the copies' record counts, so any number of rows
-//             works
-//   int8      the 16-bit geometry with 32 K a step and integer sums
-#include "grouped_common.hpp"
+// grouped_two_group.hip -- launches of the two-group kernel
+// (grouped_two_group.hpp): the product of 16-bit operands
+// with B K-contiguous.
+#include "grouped_two_group.hpp"
 
 namespace tla {
-namespace {
 
-enum Form : int { kNK = 0, kKN = 1, kGrad = 2 };
-
-template <int kCode, int kForm>
-__global__ __launch_bounds__(512) void grouped_two_group_kernel(const GroupedParams p) {
-  using Atom = OpAtom<kCode>;
-  using Frag = typename Atom::Frag;
-  constexpr int kRowBytes = 128;
-  using Swz = typename Slab<kRowBytes>::Swz;
-  constexpr int kChunks = Slab<kRowBytes>::kChunks;
-  constexpr int EB = type_bytes(kCode);
-  constexpr bool kBT = kForm != kNK, kAT = kForm == kGrad;
-  constexpr int BK = kRowBytes / EB;            // K elements per k-tile
-  constexpr int BM = 256, BN = 256;
-  constexpr int WM = 64, WN = 128;              // wave tile
-  constexpr int FM = WM / 32, FN = WN / 32;     // MFMA tiles per wave
-  constexpr int KSTEPS = BK / Atom::kK;         // MFMA k-steps per k-tile
-  constexpr int kSub = Atom::kLaneBytes / 16;   // 16-byte reads per fragment
-  constexpr int kStepBytes = Atom::kK * EB;
-  constexpr int SLAB = BM * kRowBytes;          // 32 KiB: one operand, one k-tile
-  constexpr int B_BASE = 2 * SLAB;              // LDS: [A0 A1 | B0 B1 B2]
-  constexpr int kCopies = SLAB / (256 * 16);    // 16-byte copies per thread per slab
-  static_assert(BK % Atom::kK == 0 && kCopies == 8, "k-tile geometry");
-  static_assert((1 << Slab<kRowBytes>::kRowShift) * kChunks <= 32,
-                "the swizzle repeats within 32 rows");
-  static_assert(5 * SLAB <= 160 * 1024, "LDS budget");
-  static_assert(!kBT || EB == 2, "slabs of k rows: 16-bit operands");
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[5 * SLAB];
-
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int grp = wave >> 2;                    // 0: waves 0-3, 1: waves 4-7
-  const int t = tid & 255;                      // thread index inside the group
-  // The tile: the operands' first rows and what is left of them from there.
-  // Product: rows m0 .. m_end - 1 of A are the expert's.  Gradient: the
-  // expert's rows are the K of both operands, m0 and n0 columns of them.
-  int e, m0, m_end, n0, K;
-  const uint8_t *A = p.A, *B = p.B;
-  if constexpr (kForm == kGrad) {
-    int tm, tn, lo, hi;
-    wgrad_tile(p, blockIdx.x, gridDim.x, e, tm, tn);
-    expert_rows(p, e, lo, hi);
-    m0 = tm * BM;
-    m_end = p.M;
-    n0 = tn * BN;
-    K = hi - lo;
-    A += (int64_t)lo * p.lda * EB;
-    B += (int64_t)lo * p.ldb * EB;
-  } else {
-    RowTile rt;
-    if (!row_tile<BM>(p, blockIdx.x, rt)) return;
-    e = rt.e;
-    m0 = rt.r0;
-    m_end = rt.r1;
-    n0 = rt.tn * BN;
-    K = p.K;
-    B += (int64_t)e * p.stride_b * EB;
-  }
-  const int wm0 = 128 * grp + WM * (wave & 1), wn0 = WN * ((wave >> 1) & 1);
-  const bool busy = kForm == kGrad || m0 + wm0 < m_end;  // a wave without a row multiplies nothing
-  const int KT = (K + BK - 1) / BK;
-  const int KTf = K / BK;  // whole k-tiles; tile KTf, if K ends inside it, is ragged
-
-  // ---- copies: group 0 moves A (two LDS slots), group 1 moves B (three
-  // slots), 8 instructions per slab.  Thread t fills slot byte 16 (t + 256q)
-  // (lane-linear), i.e. row r0 + 32q, physical chunk t % 8, and fetches the
-  // logical chunk the swizzle puts there; rows 32q.. of the tile start the
-  // buffer resource of copy q, whose record count ends at the last real row.
-  const int r0 = t / kChunks;
-  const int64_t rb = (grp == 0 ? p.lda : p.ldb) * EB;   // row pitch in bytes
-  const uint8_t* op = (grp == 0 ? A + m0 * rb : B + n0 * rb);  // the tile's first row
-  const int rows_left = (grp == 0 ? m_end - m0 : p.N - n0); // real rows from there on
-  uint32_t voff = (uint32_t)(r0 * rb + Swz::chunk(r0, t % kChunks) * 16);
-  const int lds_op = grp == 0 ? 0 : B_BASE;
-  int recs[kCopies];
-  static_for<kCopies>([&](auto q) {
-    recs[q] = (int)(min(max(rows_left - 32 * (int)q, 0), 32) * rb);
-  });
-  // per group: the byte step of a k-tile, and (N-contiguous B) of a copy
-  uint32_t kt_bytes = kRowBytes, q_bytes = 0;
-  const uint8_t* qbase = op;
-  int64_t q_stride = 32 * rb;
-  if constexpr (kBT) {
-    if (grp == 1) {
-      // slab chunk t + 256 q: row r0 = t / 32 (+ 8 q), stored chunk t % 32
-      // holding columns n0 + 8 ((t % 32) ^ 4 (r0 % 4)) .. + 7
-      const int64_t ldb = p.ldb;
-      const int rt = t >> 5;
-      const int n = min(n0 + 8 * ((t & 31) ^ (4 * (rt & 3))), p.N - 8);
-      voff = (uint32_t)((rt * ldb + n) * EB);
-      kt_bytes = (uint32_t)(BK * ldb * EB);
-      q_bytes = (uint32_t)(8 * ldb * EB);
-      qbase = B;
-      q_stride = 0;
-      const int64_t whole = (int64_t)K * ldb * EB;
-      static_for<kCopies>([&](auto q) { recs[q] = (int)min(whole, (int64_t)0x7FFFFFFF); });
-    }
-  }
-  if constexpr (kAT) {
-    if (grp == 0) {
-      // the same for an M-contiguous A (column-major M x K, pitch lda):
-      // row rt (+ 8 q) of k, stored chunk t % 32 holding columns
-      // m0 + 8 ((t % 32) ^ 4 (rt % 4)) .. + 7, clamped to the last chunk of M
-      const int64_t lda = p.lda;
-      const int rt = t >> 5;
-      const int m = min(m0 + 8 * ((t & 31) ^ (4 * (rt & 3))), p.M - 8);
-      voff = (uint32_t)((rt * lda + m) * EB);
-      kt_bytes = (uint32_t)(BK * lda * EB);
-      q_bytes = (uint32_t)(8 * lda * EB);
-      qbase = A;
-      q_stride = 0;
-      const int64_t whole = (int64_t)K * lda * EB;
-      static_for<kCopies>([&](auto q) { recs[q] = (int)min(whole, (int64_t)0x7FFFFFFF); });
-    }
-  }
-  // The ragged last k-tile (K a multiple of the 16-byte chunk): a lane whose
-  // K-contiguous chunk lies past K reads from past every record, so the
-  // range check returns zeros; the rows past K of a k-rows slab (an M- or
-  // N-contiguous operand) are past its records already.
-  uint32_t voff_tail = voff;
-  if ((grp == 0 && !kAT) || (grp == 1 && !kBT)) {
-    if (Swz::chunk(r0, t % kChunks) * 16 >= (K - KTf * BK) * EB) voff_tail = 0x80000000u;
-  }
-  // Copy q of k-tile kt into `slot`.  A copy past the last k-tile still runs
-  // (so the instruction stream and the wait counts never change) but with no
-  // records: it writes zeros into a slot nobody reads any more.
-  auto copy_one = [&](int kt, int slot, bool live, auto q) {
-    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
-        (void*)(qbase + (int64_t)q * q_stride), 0, recs[q] & -(int)live, 0x00020000);
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(
-        r, (__attribute__((address_space(3))) void*)(smem + lds_op + slot * SLAB + q * 4096 +
-                                                     (wave & 3) * 1024),
-        16, kt == KTf ? voff_tail : voff, (uint32_t)kt * kt_bytes + (uint32_t)q * q_bytes, 0, 0);
-  };
-  auto copy_slab = [&](int kt, int slot, bool live) {
-    static_for<kCopies>([&](auto q) { copy_one(kt, slot, live, q); });
-  };
-
-  // ---- fragments: one base register per k-step; the A slot and the 32-row
-  // fragment are immediates, the B slot (three of them: immediates would
-  // pass 64 KiB) is added into the B bases as they move from slot to slot.
-  // A 32-byte (e4m3) fragment is logical chunks 2u, 2u+1 of the row: the
-  // swizzle XORs the chunk index, so the second chunk sits at the first
-  // one's address XOR 16 (every other term of the address is a multiple of
-  // 128), formed in the loop rather than held.
-  static_assert(kSub == 1 || (Atom::kLaneBytes == 32 && kStepBytes % 32 == 0), "chunk pairs");
-  uint32_t fa[kAT ? 1 : KSTEPS], fb[kBT ? 1 : KSTEPS];
-  static_for<KSTEPS>([&](auto ks) {
-    const int c = (ks * kStepBytes + (lane >> 5) * Atom::kLaneBytes) / 16;
-    const int ra = wm0 + (lane & 31), rbw = wn0 + (lane & 31);
-    if constexpr (!kAT) fa[ks] = (uint32_t)(ra * kRowBytes + Swz::chunk(ra, c) * 16);
-    if constexpr (!kBT)
-      fb[ks] = (uint32_t)(B_BASE + rbw * kRowBytes + Swz::chunk(rbw, c) * 16);  // B slot 0
-  });
-  if constexpr (kAT) {
-    // as for an N-contiguous B below, with rows m = wm0 + ... of A slot 0
-    // (wm0 is a multiple of 64, so fragment i is again XOR 64 i)
-    const int qw = lane >> 4, a4 = lane & 15;
-    const int k = 8 * (qw >> 1) + (a4 >> 2);
-    const int m = wm0 + 16 * (qw & 1) + 4 * (a4 & 3);
-    fa[0] = (uint32_t)(k * 512 + (((m >> 3) ^ (4 * (k & 3))) * 16) + (m & 7) * 2);
-  }
-  if constexpr (kBT) {
-    // transpose read h of k-step ks for lane a of quarter-wave qw: row
-    // k = 16 ks + 8 (qw / 2) + 4 h + a / 4, columns n = wn0 + 16 (qw % 2) +
-    // 4 (a % 4) of the first 32-column fragment, stored chunk
-    // (n / 8) ^ 4 (k % 4).  k % 4 = a / 4 whatever ks and h, so one base
-    // (ks = h = 0) serves all: + 8192 ks + 2048 h, and XOR 64 j for
-    // fragment j
-    const int qw = lane >> 4, a4 = lane & 15;
-    const int k = 8 * (qw >> 1) + (a4 >> 2);
-    const int n = wn0 + 16 * (qw & 1) + 4 * (a4 & 3);
-    fb[0] = (uint32_t)(B_BASE + k * 512 + (((n >> 3) ^ (4 * (k & 3))) * 16) + (n & 7) * 2);
-  }
-  Frag a[KSTEPS][FM], b[KSTEPS][FN];
-  auto lds_frag = [&](uint32_t base, int imm) -> Frag {
-    if constexpr (kSub == 1) {
-      return *(const i32x4*)(smem + base + imm);
-    } else {
-      uint32_t base_hi = base ^ 16u;
-      asm volatile("" : "+v"(base_hi));  // keep the XOR in the loop
-      const i32x4 lo = *(const i32x4*)(smem + base + imm);
-      const i32x4 hi = *(const i32x4*)(smem + base_hi + imm);
-      return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-    }
-  };
-  // k-tile kt: A slot kt % 2 (immediate), B slot kt % 3 (in fb); afterwards
-  // fb moves on to B slot (kt + 1) % 3
-  auto lds_frag_t = [&](uint32_t addr) -> Frag {
-    typedef int s32x2 __attribute__((ext_vector_type(2)));
-    const s16x4 lo = ds_read_tr16(smem + addr);
-    const s16x4 hi = ds_read_tr16(smem + addr + 2048);
-    const s32x2 l2 = __builtin_bit_cast(s32x2, lo), h2 = __builtin_bit_cast(s32x2, hi);
-    return Frag{l2[0], l2[1], h2[0], h2[1]};
-  };
-  auto read_frag = [&](int kt, auto r) {
-    constexpr int ks = r / (FM + FN), f = r % (FM + FN);
-    if constexpr (f < FM && kAT)
-      a[ks][f] = lds_frag_t((fa[0] ^ (64u * f)) + 8192 * ks + (kt & 1) * SLAB);
-    else if constexpr (f < FM)
-      a[ks][f] = lds_frag(fa[ks], (kt & 1) * SLAB + f * 32 * kRowBytes);
-    else if constexpr (kBT)
-      b[ks][f - FM] = lds_frag_t((fb[0] ^ (64u * (f - FM))) + 8192 * ks);
-    else
-      b[ks][f - FM] = lds_frag(fb[ks], (f - FM) * 32 * kRowBytes);
-  };
-  auto advance_b = [&](int kt) {
-    const int step = (kt % 3 == 2) ? -2 * SLAB : SLAB;
-    static_for<kBT ? 1 : KSTEPS>([&](auto ks) { fb[ks] += step; });
-  };
-  // A memory phase: read k-tile kt's fragments and copy k-tile ct into
-  // `slot`.  Under load the copy path accepts a direct-to-LDS copy only every
-  // few dozen cycles, and a wave issues in order, so the copies go out
-  // between the LDS reads (kReads / kCopies fragments after each copy, the
-  // remainder spread over the first copies): the TA and the LDS then work
-  // side by side instead of one after the other.  Measured per k-tile of
-  // 256 x 256 x 128 bytes: 2508 cycles interleaved against 2590 with the
-  // copies after the reads (16-bit), 3728 against 3952 (reads first) and
-  // 4276 (copies first) for e4m3.
-  constexpr int kReads = KSTEPS * (FM + FN);  // fragments per k-tile
-  constexpr int kPer = kReads / kCopies, kRem = kReads % kCopies;
-  // LDS read instructions of fragments [first, first + n)
-  auto read_insts = [](int first, int n) constexpr {
-    int c = 0;
-    for (int r = first; r < first + n; ++r)
-      c += (r % (FM + FN) < FM) ? (kAT ? 2 : kSub) : (kBT ? 2 : kSub);
-    return c;
-  };
-  auto memory_phase = [&](int kt, int ct, int slot, bool live) {
-    __builtin_amdgcn_sched_barrier(0);
-    static_for<kCopies>([&](auto q) {
-      copy_one(ct, slot, live, q);
-      constexpr int first = kPer * q + (q < kRem ? q : kRem);
-      constexpr int n = kPer + (q < kRem ? 1 : 0);
-      static_for<n>([&](auto u) { read_frag(kt, std::integral_constant<int, first + u>{}); });
-    });
-    static_for<kCopies>([&](auto q) {
-      constexpr int first = kPer * q + (q < kRem ? q : kRem);
-      constexpr int n = kPer + (q < kRem ? 1 : 0);
-      __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(0x100, read_insts(first, n), 0);
-    });
-    advance_b(kt);
-    __builtin_amdgcn_sched_barrier(0);
-  };
-  typename Atom::Acc acc[FM][FN];
-  static_for<FM>([&](auto i) { static_for<FN>([&](auto j) { acc[i][j] = typename Atom::Acc{}; }); });
-  // one k-tile of MFMAs, fenced off from the scheduler on both sides so that
-  // no wait or memory instruction of a neighbouring phase moves into it
-  auto compute = [&]() {
-    __builtin_amdgcn_sched_barrier(0);
-    if (busy) {
-      static_for<KSTEPS * FM * FN>([&](auto idx) {
-        constexpr int ks = idx / (FM * FN), i = (idx / FN) % FM, j = idx % FN;
-        Atom::mma(acc[i][j], b[ks][j], a[ks][i]);
-      });
-    }
-    __builtin_amdgcn_sched_barrier(0);
-  };
-  auto wait_lgkmcnt0 = [&]() { __builtin_amdgcn_s_waitcnt(0xC07F); };
-  auto barrier = [&]() {
-    __builtin_amdgcn_sched_barrier(0);
-    stage_barrier();
-    __builtin_amdgcn_sched_barrier(0);
-  };
-
-  // Each group runs its own program with exactly one MFMA sequence; copies
-  // are issued only between LDS reads.  Period kt ends at barrier 2kt+1:
-  //   group 0: read k-tile kt's fragments and copy A of kt+1 into A slot
-  //     (kt+1)%2 (it held kt-1, read by both groups in period kt-1), then
-  //     multiply kt and wait for its copies;
-  //   group 1: multiply kt-1 (fragments read in period kt-1), then read
-  //     kt's fragments and copy B of kt+2 into B slot (kt+2)%3 (it held
-  //     kt-1), then wait for B of kt+1 (copied in period kt-1); in period
-  //     0 it only reads.
-  // Every slab is thus complete one barrier before its first reader.  A
-  // second barrier splits each period between its halves: group 0 reads
-  // while group 1 multiplies, then the other way round.  An MFMA holds its
-  // wave's issue for its whole run, so without the split group 0 starts
-  // multiplying before group 1 is done, both share the matrix core and the
-  // period grows (16-bit: 3084 cycles per k-tile against 2508; the e4m3
-  // 8192^3 GEMM with GELU: 440 us with one barrier per period, 396 us with
-  // two).
-  //
-  // Group 1's second barrier is skipped after the last k-tile, and the
-  // compiler is free to sink the MFMAs, plain register arithmetic, past
-  // such a conditional barrier into the next period (it does so for e4m3,
-  // which then measured 3664 cycles per k-tile): an empty asm reading every
-  // accumulator keeps them in front of it.
-  if (KT > 0) {
-    if (grp == 0) {
-      copy_slab(0, 0, true);
-      wait_vmcnt<0>();
-      barrier();
-      for (int kt = 0; kt < KT; ++kt) {
-        memory_phase(kt, kt + 1, (kt + 1) & 1, kt + 1 < KT);
-        wait_lgkmcnt0();
-        barrier();
-        compute();
-        wait_vmcnt<0>();                             // A of kt+1 landed
-        barrier();
-      }
-    } else {
-      copy_slab(0, 0, true);
-      copy_slab(1, 1, KT > 1);
-      wait_vmcnt<kCopies>();
-      barrier();
-      barrier();
-      // one iteration reads k-tile kt (end of period kt) and multiplies it
-      // (start of period kt+1): the fragments never live across iterations
-      for (int kt = 0; kt < KT; ++kt) {
-        memory_phase(kt, kt + 2, (kt + 2) % 3, kt + 2 < KT);
-        wait_lgkmcnt0();
-        wait_vmcnt<kCopies>();                       // B of kt+1 landed
-        barrier();
-        compute();
-#pragma unroll
-        for (int i = 0; i < FM; ++i)
-#pragma unroll
-          for (int j = 0; j < FN; ++j) {
-#if defined(__HIP_DEVICE_COMPILE__)  // a type of the template: the host pass has no such register
-            asm volatile("" ::"v"(acc[i][j]));
-#endif
-          }
-        if (kt + 1 < KT) barrier();
-      }
-      wait_vmcnt<0>();  // the last (record-less) copies
-    }
-  }
-  // Every LDS read of the main loop finished before the last barrier and no
-  // copy is in flight, so the slots are free for the epilogue: group 0
-  // starts while group 1 still multiplies the last k-tile.
-  uint8_t* region = smem + wave * (32 * FM) * (64 * FN);
-  if constexpr (kForm == kGrad)
-    wgrad_epilogue<FM, FN>(p, e, m0 + wm0, n0 + wn0, lane, acc, region);
-  else
-    grouped_epilogue<kCode, FM, FN>(p, e, m_end, m0 + wm0, n0 + wn0, lane, acc, region);
-}
-
-template <int kCode, int kForm>
-int launch(const GroupedParams& p0, hipStream_t stream) {
-  GroupedParams p = p0;
-  p.tiles_n = (p.N + 255) / 256;
-  p.tiles_m = (p.M + 255) / 256;
-  const int64_t grid = kForm == kGrad ? (int64_t)p.groups * p.tiles_m * p.tiles_n
-                                      : row_tiles_bound(p.rows, p.groups, 256) * p.tiles_n;
-  if (grid <= 0) return TLA_OK;
-  if (grid > 0x7FFFFFFF) return TLA_ERR_UNSUPPORTED;
-  hipLaunchKernelGGL((grouped_two_group_kernel<kCode, kForm>), dim3((unsigned)grid), dim3(512), 0,
-                     stream, p);
-  return hipGetLastError() == hipSuccess ? TLA_OK : TLA_ERR_HIP;
-}
-
-}  // namespace
-
-int launch_grouped_two_group(const GroupedParams& p, int type, bool b_kc, hipStream_t s) {
-  switch (type) {
-    case TLA_BF16: return b_kc ? launch<kBF16, kNK>(p, s) : launch<kBF16, kKN>(p, s);
-    case TLA_F16: return b_kc ? launch<kF16, kNK>(p, s) : launch<kF16, kKN>(p, s);
-    case TLA_E4M3: return b_kc ? launch<kE4M3, kNK>(p, s) : TLA_ERR_UNSUPPORTED;
-    case TLA_I8: return b_kc ? launch<kI8, kNK>(p, s) : TLA_ERR_UNSUPPORTED;
-    default: return TLA_ERR_UNSUPPORTED;
-  }
-}
-
-int launch_wgrad_two_group(const GroupedParams& p, int type, hipStream_t s) {
-  return type == TLA_BF16 ? launch<kBF16, kGrad>(p, s) : launch<kF16, kGrad>(p, s);
+int launch_two_group_nk16(const GroupedParams& p, int type, hipStream_t s) {
+  return type == TLA_BF16 ? launch<kBF16, kNK>(p, s) : launch<kF16, kNK>(p, s);
 }
 
 }  // namespace tla

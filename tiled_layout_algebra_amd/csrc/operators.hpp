@@ -43,18 +43,35 @@ enum : int {
   kOpVec4 = 2,   // sb and bias rows allow aligned 4-element vectors
 };
 
+// Blocks of BM rows that `rows` rows in `groups` groups can need: every
+// non-empty group's last block may hold a single row.
+inline int64_t row_tiles_bound(int64_t rows, int64_t groups, int64_t BM) {
+  const int64_t live = rows < groups ? rows : groups;
+  return (rows + live * (BM - 1)) / BM;
+}
+
 // The register-staged kernel: any order, pitch, alignment (b_kc: B is
 // K-contiguous).
 int launch_grouped_general(const GroupedParams& p, int type, bool b_kc, hipStream_t stream);
 int launch_wgrad_general(const GroupedParams& p, int type, hipStream_t stream);
 
-// The 256 x 256 direct-copy kernel (grouped_two_group.hip).  Product: A and,
-// with b_kc, B have 16-byte aligned rows of a multiple of 16 bytes of K below
-// 64 MiB each; otherwise B is 16-bit with 16-byte aligned rows, N a multiple
-// of 8, a matrix below 2 GiB.  Gradient: both operands have such rows, M and
-// N multiples of 8, each operand below 2 GiB.
-int launch_grouped_two_group(const GroupedParams& p, int type, bool b_kc, hipStream_t stream);
+// The direct-copy kernels.  Product: A's rows and, for nk, B's are 16-byte
+// aligned, a multiple of 16 bytes of K long and less than 8 MiB apart; kn: B
+// is 16-bit with 16-byte aligned rows, N a multiple of 8, a matrix below
+// 2 GiB.  Gradient: both operands have 16-byte aligned rows, M and N are
+// multiples of 8, each operand is below 2 GiB.
+// 256 x 256 tiles (grouped_two_group.hpp)
+int launch_two_group_nk16(const GroupedParams& p, int type, hipStream_t stream);
+int launch_two_group_nk8(const GroupedParams& p, int type, hipStream_t stream);
+int launch_two_group_kn(const GroupedParams& p, int type, hipStream_t stream);
+// any alignment, B K-contiguous, rows less than 8 MiB apart
+int launch_two_group_shift(const GroupedParams& p, int type, hipStream_t stream);
 int launch_wgrad_two_group(const GroupedParams& p, int type, hipStream_t stream);
+// 64 or 128 x 128 tiles, two or three LDS stages (grouped_direct.hpp)
+enum DirectShape : int { kDirect64x3, kDirect128x2, kDirect128x3 };
+int launch_grouped_direct(const GroupedParams& p, int type, int shape, hipStream_t stream);
+int launch_grouped_direct_kn(const GroupedParams& p, int type, int shape, hipStream_t stream);
+int launch_wgrad_direct(const GroupedParams& p, int type, int shape, hipStream_t stream);
 
 // The kernel for few rows an expert (grouped_few_rows.hip): B K-contiguous,
 // any pitch and alignment; blocks of 16 mt rows, mt 1, 2 or 4.

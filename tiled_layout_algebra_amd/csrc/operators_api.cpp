@@ -23,11 +23,15 @@ bool aux_type(int t) { return out16(t) || t == TLA_F32; }
 
 bool aligned_to(const void* p, int64_t bytes) { return (uintptr_t)p % (uintptr_t)bytes == 0; }
 
-// what a validated call runs
-enum Kernel { kNoop, kGeneral, kTwoGroup, kFewRows1, kFewRows2, kFewRows4 };
-const char* const kNames[] = {"noop", "grouped_general_128x128", "grouped_two_group_256x256",
-                              "grouped_few_rows_16x32", "grouped_few_rows_32x32",
-                              "grouped_few_rows_64x32"};
+// what a validated call runs: the variant ids of the public header, or nothing
+enum Kernel {
+  kNoop = -1, kGeneral, kTwoGroup, kDirect128, kDirect64, kFewRows4, kFewRows2, kFewRows1,
+  kTwoGroupShift
+};
+const char* const kNames[TLA_GROUPED_VARIANTS] = {
+    "grouped_general_128x128", "grouped_two_group_256x256", "grouped_direct_128x128",
+    "grouped_direct_64x128", "grouped_few_rows_64", "grouped_few_rows_32", "grouped_few_rows_16",
+    "grouped_two_group_shift_256x256"};
 
 struct Plan {
   GroupedParams p;
@@ -39,27 +43,80 @@ struct Plan {
 // Rows of `ld` elements of eb bytes at p start on 16-byte boundaries.
 bool rows16(const void* p, int64_t ld, int eb) { return aligned_to(p, 16) && ld * eb % 16 == 0; }
 
-// The direct copies' layout (operators.hpp, launch_grouped_two_group).
-bool direct_copies(const tla_grouped_gemm_args* a, int eb, bool b_kc) {
-  if (a->K == 0 || a->K * eb % 16 != 0 || !rows16(a->A, a->lda, eb) || !rows16(a->B, a->ldb, eb) ||
-      (a->groups > 1 && a->stride_b * eb % 16 != 0) || a->lda * eb >= (kLimit >> 5))
+// Whether a kernel takes the problem.
+bool takes(Kernel k, const tla_grouped_gemm_args* a, int eb, bool b_kc) {
+  if (k == kGeneral) return true;
+  if (a->K == 0) return false;
+  if (k == kFewRows1 || k == kFewRows2 || k == kFewRows4) return b_kc;
+  if (a->type == TLA_E4M3 && a->K < kMinKE4m3) return false;
+  // 32-bit offsets within a tile's rows
+  if (a->lda * eb >= (kLimit >> 8) || (b_kc && a->ldb * eb >= (kLimit >> 8))) return false;
+  if (k == kTwoGroupShift) return b_kc;
+  if (k == kDirect64 && !b_kc) return false;
+  if (a->K * eb % 16 != 0 || !rows16(a->A, a->lda, eb) || !rows16(a->B, a->ldb, eb) ||
+      (a->groups > 1 && a->stride_b * eb % 16 != 0))
     return false;
-  if (b_kc) return a->ldb * eb < (kLimit >> 5);
-  return eb == 2 && a->N % 8 == 0 && a->K * a->ldb * eb < kLimit;
+  return b_kc || (eb == 2 && a->N % 8 == 0 && a->K * a->ldb * eb < kLimit);
 }
 
+// Blocks of bm rows the experts need, about: a block at least for each that
+// has any, otherwise its rows' share and three quarters of a block for its
+// ragged end (a half when the experts are even, more when they are not).
+double row_blocks(const tla_grouped_gemm_args* a, double bm) {
+  const double live = (double)(a->rows < a->groups ? a->rows : a->groups);
+  const double blocks = (double)a->rows / live / bm + (a->groups > 1 ? 0.75 : 0.0);
+  return live * (blocks > 1.0 ? blocks : 1.0);
+}
+
+// The kernel with the smallest estimated time (us).  No kernel reads the
+// weights faster than 5.0 TB/s.  Measured with [N, K] weights of 4096 x 4096
+// int8 (32 k-tiles of 128 bytes), one expert, M rows:
+//      M     few 16   few 32   few 64   64x128   128x128   256x256
+//      1       6.7      6.9      8.1     13.6      15.9      30.4
+//     32      11.0      9.4     10.8     14.3      16.1      30.7
+//     64      19.2     14.4     13.3     14.8      16.4      31.2
+//    512       125       90       75     17.2      18.7      39.6
+//   2048                                 50.0      46.5      43.8
+//   3001                                 74.6      68.0      54.0
+// and in bf16 for 32 experts of 2048 x 4096: 128 rows 107 (few 16), 111
+// (64x128), 4096 rows 178 (64x128), 151 (128x128), 192 (256x256); for 8
+// experts of 4096 x 4096 with 2000 rows 136, 127, 96.
 Kernel choose(const tla_grouped_gemm_args* a, int eb, bool b_kc) {
-  const int64_t tiles_n = (a->N + 255) / 256, each = a->rows / a->groups;
-  const bool direct = direct_copies(a, eb, b_kc);
-  if (b_kc && a->K > 0) {
-    if (each <= 12) return kFewRows1;
-    if (each <= 28) return kFewRows2;
-    if (each <= 64) return kFewRows4;
-  }
-  if (direct && each >= 128 && (a->rows + 255) / 256 * tiles_n >= 128 &&
-      (a->type != TLA_E4M3 || a->K >= kMinKE4m3))
-    return kTwoGroup;
-  return kGeneral;
+  const double live = (double)(a->rows < a->groups ? a->rows : a->groups);
+  const double matrix = (double)a->N * (double)a->K * eb * 1e-6;  // MB
+  const double weights = live * matrix / 5.0;
+  const double kt = (double)((a->K * eb + 127) / 128);
+  Kernel best = kGeneral;
+  double best_us = 1e30;
+  auto consider = [&](Kernel k, double us) {
+    if (!takes(k, a, eb, b_kc)) return;
+    us = us > weights + 4.0 ? us : weights + 4.0;
+    if (us < best_us) {
+      best = k;
+      best_us = us;
+    }
+  };
+  auto tiles = [&](double bm, double bn) {
+    return row_blocks(a, bm) * (double)((a->N + (int64_t)bn - 1) / (int64_t)bn);
+  };
+  // rounds of workgroups, one a compute unit
+  auto rounds = [](double t) { return (double)(int64_t)((t + 255.0) / 256.0); };
+  // each block of rows reads the weights again, at the rate the matrix
+  // instructions and A's rows leave
+  consider(kFewRows1, 4.0 + row_blocks(a, 16) * matrix / 5.0);
+  consider(kFewRows2, 4.3 + row_blocks(a, 32) * matrix / 3.3);
+  consider(kFewRows4, 5.0 + row_blocks(a, 64) * matrix / 2.2);
+  const double t64 = 0.0016 * tiles(64, 128), t128 = tiles(128, 128), t256 = tiles(256, 256);
+  consider(kDirect64, 4.2 + kt * (t64 > 0.3 ? t64 : 0.3));
+  consider(kDirect128, 4.5 + kt * (t128 <= 128.0 ? 0.4 : 0.66 * rounds(t128)));
+  consider(kTwoGroup, 5.0 + kt * (t256 <= 128.0 ? 1.25 : 1.6 * rounds(t256)));
+  // any alignment: 16384 bf16 rows on 8 experts of 4096 x 4095 725 us for the
+  // shifting kernel against 1095 for the general one, 3001 int8 rows 4096 x
+  // 4095 71 against 118; 2000 f16 rows on 8 experts of 2047 x 1023 46 against 43
+  consider(kTwoGroupShift,
+           6.0 + (double)(a->K * eb / 96 + 1) * (t256 <= 128.0 ? 1.5 : 1.65 * rounds(t256)));
+  consider(kGeneral, 4.5 + kt * 1.8 * rounds(t128 / 2.0));
+  return best;
 }
 
 int plan_product(const tla_grouped_gemm_args* a, Plan* out) {
@@ -129,17 +186,37 @@ int plan_product(const tla_grouped_gemm_args* a, Plan* out) {
   return TLA_OK;
 }
 
-int run_product(const tla_grouped_gemm_args* a, hipStream_t stream) {
+// forced: a variant id, or -1 for the estimate's choice
+int run_product(const tla_grouped_gemm_args* a, hipStream_t stream, int forced = -1) {
   Plan plan;
   const int rc = plan_product(a, &plan);
   if (rc) return rc;
+  if (forced >= 0 && plan.kernel != kNoop) {
+    if (!takes((Kernel)forced, a, type_bytes(a->type), plan.b_kc)) return TLA_ERR_UNSUPPORTED;
+    plan.kernel = (Kernel)forced;
+  }
+  const GroupedParams& p = plan.p;
+  const int t = plan.type;
   switch (plan.kernel) {
     case kNoop: return TLA_OK;
-    case kTwoGroup: return launch_grouped_two_group(plan.p, plan.type, plan.b_kc, stream);
-    case kFewRows1: return launch_grouped_few_rows(plan.p, plan.type, 1, stream);
-    case kFewRows2: return launch_grouped_few_rows(plan.p, plan.type, 2, stream);
-    case kFewRows4: return launch_grouped_few_rows(plan.p, plan.type, 4, stream);
-    case kGeneral: return launch_grouped_general(plan.p, plan.type, plan.b_kc, stream);
+    case kTwoGroup:
+      if (!plan.b_kc) return launch_two_group_kn(p, t, stream);
+      return type_bytes(t) == 1 ? launch_two_group_nk8(p, t, stream)
+                                : launch_two_group_nk16(p, t, stream);
+    case kTwoGroupShift: return launch_two_group_shift(p, t, stream);
+    case kDirect64: return launch_grouped_direct(p, t, kDirect64x3, stream);
+    case kDirect128: {
+      if (plan.b_kc) return launch_grouped_direct(p, t, kDirect128x3, stream);
+      // three stages while every workgroup has a compute unit of its own (500
+      // rows on 4 experts of 1024 x 1024: 10.6 us against 15.9 with two), two
+      // stages and two workgroups a unit beyond (16000 rows: 49 against 57)
+      const int64_t blocks = row_tiles_bound(p.rows, p.groups, 128) * ((p.N + 127) / 128);
+      return launch_grouped_direct_kn(p, t, blocks <= 256 ? kDirect128x3 : kDirect128x2, stream);
+    }
+    case kFewRows1: return launch_grouped_few_rows(p, t, 1, stream);
+    case kFewRows2: return launch_grouped_few_rows(p, t, 2, stream);
+    case kFewRows4: return launch_grouped_few_rows(p, t, 4, stream);
+    case kGeneral: return launch_grouped_general(p, t, plan.b_kc, stream);
   }
   return TLA_ERR_UNSUPPORTED;
 }
@@ -157,9 +234,15 @@ int tla_grouped_gemm_variant(const tla_grouped_gemm_args* args, char* buf, int32
   Plan plan;
   const int rc = plan_product(args, &plan);
   if (rc) return rc;
-  strncpy(buf, kNames[plan.kernel], (size_t)cap - 1);
+  strncpy(buf, plan.kernel == kNoop ? "noop" : kNames[plan.kernel], (size_t)cap - 1);
   buf[cap - 1] = '\0';
   return TLA_OK;
+}
+
+int tla_grouped_gemm_run_variant(const tla_grouped_gemm_args* args, int32_t variant,
+                                 void* stream) {
+  if (variant < 0 || variant >= TLA_GROUPED_VARIANTS) return TLA_ERR_INVALID_ARG;
+  return run_product(args, (hipStream_t)stream, variant);
 }
 
 int tla_gemm_i8(const tla_gemm_i8_args* a, void* stream) {
@@ -237,8 +320,17 @@ int tla_grouped_gemm_wgrad(const tla_grouped_wgrad_args* a, void* stream) {
   // the direct copies' layout (operators.hpp, launch_wgrad_two_group)
   const bool direct = rows16(a->A, a->lda, 2) && rows16(a->Y, a->ldy, 2) && a->K % 8 == 0 &&
                       a->N % 8 == 0 && a->rows * a->lda * 2 < kLimit && a->rows * a->ldy * 2 < kLimit;
+  // 256 x 256 tiles when they give every compute unit one (8000 rows on 16
+  // experts of 2048 x 2048: 82 us against 101 for 128 x 128); below, 128 x 128
+  // with two stages (777 rows, 16 experts of 512 x 1024: 17.2 us against 22.6
+  // and 18.5 with three), three stages when they all fit at once (1000 rows, 2
+  // experts of 1024 x 1024: 8.1 against 9.5)
   const int64_t tiles = a->groups * ((a->K + 255) / 256) * ((a->N + 255) / 256);
-  if (direct && tiles >= 128) return launch_wgrad_two_group(p, a->type, (hipStream_t)stream);
+  const int64_t tiles128 = a->groups * ((a->K + 127) / 128) * ((a->N + 127) / 128);
+  if (direct && tiles >= 256) return launch_wgrad_two_group(p, a->type, (hipStream_t)stream);
+  if (direct)
+    return launch_wgrad_direct(p, a->type, tiles128 <= 256 ? kDirect128x3 : kDirect128x2,
+                               (hipStream_t)stream);
   return launch_wgrad_general(p, a->type, (hipStream_t)stream);
 }
 
