@@ -245,15 +245,16 @@ int tla_grouped_gemm_variant(const tla_grouped_gemm_args *args, char *buf, int32
  *   4 "grouped_few_rows_64"              blocks of 64, 32 and 16 rows, weights
  *   5 "grouped_few_rows_32"              straight to registers; any alignment,
  *   6 "grouped_few_rows_16"              K > 0, TLA_COL_MAJOR only
- *   7 "grouped_two_group_shift_256x256"  variant 1 for any alignment, K > 0,
- *                                        TLA_COL_MAJOR only
- * (1, 2, 3 and 7 take e4m3 with K >= 512 only.)  tla_grouped_gemm takes the
+ *   7 "grouped_two_group_shift_256x256"  variants 1, 2 and 3 for any
+ *   8 "grouped_direct_shift_128x128"     alignment, K > 0, TLA_COL_MAJOR only
+ *   9 "grouped_direct_shift_64x128"
+ * (1, 2, 3, 7, 8 and 9 take e4m3 with K >= 512 only.)  tla_grouped_gemm takes the
  * one with the smallest estimated time; tla_grouped_gemm_run_variant runs the
  * one asked for, with the same semantics, or returns TLA_ERR_UNSUPPORTED when
  * the problem does not meet its conditions.  Ids outside
  * [0, TLA_GROUPED_VARIANTS) are TLA_ERR_INVALID_ARG.
  */
-#define TLA_GROUPED_VARIANTS 8
+#define TLA_GROUPED_VARIANTS 10
 int tla_grouped_gemm_run_variant(const tla_grouped_gemm_args *args, int32_t variant, void *stream);
 
 /*

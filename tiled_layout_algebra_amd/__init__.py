@@ -319,7 +319,7 @@ class GemmI8Args(ctypes.Structure):
     ]
 
 
-GROUPED_VARIANTS = 8
+GROUPED_VARIANTS = 10
 
 
 def _dev32(t, kind, what):

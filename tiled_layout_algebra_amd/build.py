@@ -19,8 +19,8 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libtla.so")
 SOURCES = ["api.cpp", "algebra.cpp", "gemm.hip", "gemm_general.hip", "gemm_pingpong.hip",
            "conv_slab.hip", "transpose.hip", "layout_eval.hip", "operators_api.cpp",
-           "grouped_direct.hip", "grouped_direct_rows.hip", "grouped_few_rows.hip",
-           "grouped_general.hip", "grouped_two_group.hip", "grouped_two_group_8bit.hip",
+           "grouped_direct.hip", "grouped_direct_rows.hip", "grouped_direct_shift.hip",
+           "grouped_few_rows.hip", "grouped_general.hip", "grouped_two_group.hip", "grouped_two_group_8bit.hip",
            "grouped_two_group_rows.hip", "grouped_two_group_shift.hip", "quantize.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

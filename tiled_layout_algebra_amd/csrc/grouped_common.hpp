@@ -402,8 +402,10 @@ __device__ __forceinline__ void wgrad_epilogue(const GroupedParams& p, int e, in
       const int r = 32 * i + (lane & 31), c = 32 * j + 8 * g + 4 * (lane >> 5);
       if (r < rows) {
         float* d = D + (int64_t)r * p.ldd + c;
-        if (v16 && c + 3 < cols) {
-          *(f32x4*)d = f32x4{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2],
+        if (c + 3 < cols) {
+          // vector stores need the element's alignment only
+          typedef float f32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
+          *(f32x4_a4*)d = f32x4_a4{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2],
                              acc[i][j][4 * g + 3]};
         } else {
 #pragma unroll

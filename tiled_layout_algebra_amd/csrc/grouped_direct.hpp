@@ -7,7 +7,8 @@
 // LDS holds kStages A slabs and kStages B slabs of 128 bytes of K.  With two
 // stages two workgroups share a compute unit, so one's prologue and epilogue
 // run under the other's loop.  Forms and tile lookup as in
-// grouped_two_group.hip.
+// grouped_two_group.hpp, but the rows of kNKShift bring the dword after their
+// window with them, so a k-tile is the whole window.
 #pragma once
 
 #include "grouped_common.hpp"
@@ -15,13 +16,24 @@
 namespace tla {
 namespace {
 
-enum Form : int { kNK = 0, kKN = 1, kGrad = 2 };
+enum Form : int { kNK = 0, kKN = 1, kGrad = 2, kNKShift = 3 };
+
+// dma16_buf for a dword a lane
+__device__ __forceinline__ void dma4_buf(const uint8_t* base, uint32_t voffset, uint32_t soffset,
+                                         uint8_t* lds, int records) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, records, 0x00020000);
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 4, voffset,
+                                           soffset, 0, 0);
+#endif
+}
 
 template <int kCode, int kForm, int BM, int BN, int kStages, int kFront, int kWM, int kWN>
 __global__ __launch_bounds__(64 * kWM * kWN) void grouped_direct_kernel(const GroupedParams p) {
-  using Atom = OpAtom<kCode>;
+  constexpr bool kShift = kForm == kNKShift;
+  using Atom = std::conditional_t<kShift && kCode == kE4M3, E4m3Bytes, OpAtom<kCode>>;
   constexpr int kRowBytes = 128;
-  constexpr bool kBT = kForm != kNK, kAT = kForm == kGrad;
+  constexpr bool kBT = kForm == kKN || kForm == kGrad, kAT = kForm == kGrad;
   using Frag = typename Atom::Frag;
   using Swz = typename Slab<kRowBytes>::Swz;
   constexpr int NT = 64 * kWM * kWN;  // kWM x kWN wavefronts
@@ -47,9 +59,13 @@ __global__ __launch_bounds__(64 * kWM * kWN) void grouped_direct_kernel(const Gr
   static_assert((1 << Slab<kRowBytes>::kRowShift) * kChunks <= 32, "swizzle period divides 32 rows");
   constexpr int IA = BM * kChunks / NT, IB = BN * kChunks / NT;
   static_assert(IA * NT == BM * kChunks && IB * NT == BN * kChunks, "whole copy instructions");
-  constexpr int kLoads = IA + IB;                  // copies per thread per tile
+  // copies per thread per tile; kShift: the last one a dword a row
+  constexpr int kLoads = IA + IB + (kShift ? 1 : 0);
+  constexpr int TAIL_BASE = kStages * (SLAB_A + SLAB_B), kTail = kShift ? 4 * NT : 0;
+  static_assert(!kShift || (kWM * kWN * 64 >= BM + BN && BM % 64 == 0), "a wave's rows are A's or B's");
   constexpr int kSub = Atom::kLaneBytes / 16;      // 16-byte reads per fragment
-  constexpr int kReads = (kAT ? 2 * FM : FM * kSub) + (kBT ? 2 * FN : FN * kSub);
+  constexpr int kReads =
+      kShift ? 2 * (FM + FN) : (kAT ? 2 * FM : FM * kSub) + (kBT ? 2 * FN : FN * kSub);
   constexpr int kMfmas = FM * FN;
   constexpr int kStepBytes = Atom::kK * EB;
   // Copies per full step, the rest go into the first half of the last step.
@@ -59,7 +75,7 @@ __global__ __launch_bounds__(64 * kWM * kWN) void grouped_direct_kernel(const Gr
   constexpr int kFull = kPerStep * (KSTEPS - 1) < kLoads ? kPerStep * (KSTEPS - 1) : kLoads;
   constexpr int kLast = kLoads - kFull;
   constexpr int kWait = (kStages - 2) * kLoads;  // copies allowed in flight past the next tile
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[kStages * (SLAB_A + SLAB_B)];
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[TAIL_BASE + kStages * kTail];
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -91,6 +107,22 @@ __global__ __launch_bounds__(64 * kWM * kWN) void grouped_direct_kernel(const Gr
   const int KT = (K + BK - 1) / BK;
   const int KTf = K / BK;  // whole k-tiles; tile KTf, if K ends inside it, is ragged
 
+  // kShift: rows begin at any byte.  Copies start at each row's dword, so its
+  // bytes land `row_shift` late and the window's last ones in a dword of its
+  // own (tail), a row a lane; records end with the tile's last row's last dword.
+  const uint32_t a_rb = (uint32_t)(p.lda * EB), b_rb = (uint32_t)(p.ldb * EB);
+  const uint32_t a_off = (uint32_t)(uintptr_t)A & 3u, b_off = (uint32_t)(uintptr_t)B & 3u;
+  auto row_shift = [&](bool is_a, int r) {
+    return ((is_a ? a_off : b_off) + (uint32_t)r * (is_a ? a_rb : b_rb)) & 3u;
+  };
+  const int a_last = m_end - 1 - m0, b_last = p.N - 1 - n0;
+  int a_bytes = 0x7FFFFFFF, b_bytes = 0x7FFFFFFF;
+  if constexpr (kShift) {
+    A -= a_off;
+    B -= b_off;
+    a_bytes = (int)((min(a_last, BM - 1) * a_rb + K * EB + a_off + 3) & ~3u);
+    b_bytes = (int)((min(b_last, BN - 1) * b_rb + K * EB + b_off + 3) & ~3u);
+  }
   // Copy q (A for q < IA, else B): slab row r = tid/kChunks + (NT/kChunks)*q',
   // landing at slab slot wave*64 + NT*q' (lane-linear); the lane fetches the
   // global chunk the swizzle assigns to that slot, from row r clamped to the
@@ -99,7 +131,14 @@ __global__ __launch_bounds__(64 * kWM * kWN) void grouped_direct_kernel(const Gr
   static_for<kLoads>([&](auto q) {
     constexpr bool kA = q < IA;
     constexpr int qq = kA ? q : q - IA;
-    if constexpr (kA && kAT) {
+    if constexpr (q == IA + IB) {
+      const int r = tid < BM ? tid : tid - BM;
+      const bool is_a = tid < BM;
+      const int row = min(r, is_a ? a_last : b_last);
+      off[q] = tid < BM + BN ? ((uint32_t)row * (is_a ? a_rb : b_rb) + (is_a ? a_off : b_off)) / 4 * 4 +
+                                   kRowBytes
+                             : 0x80000000u;
+    } else if constexpr (kA && kAT) {
       // as for an N-contiguous B: k row r, stored chunk pc holding columns
       // m0 + 8 (pc ^ 4 (r % 4)) .. + 7, clamped to the last chunk of M
       const int sc = tid + NT * qq, r = sc / kChAT, pc = sc % kChAT;
@@ -117,6 +156,9 @@ __global__ __launch_bounds__(64 * kWM * kWN) void grouped_direct_kernel(const Gr
       const int64_t row = kA ? min(r, m_end - 1 - m0) : min(r, p.N - 1 - n0);
       const int64_t rb = (kA ? p.lda : p.ldb) * EB;
       off[q] = (uint32_t)(row * rb + Swz::chunk(r, tid % kChunks) * 16);
+      if constexpr (kShift)
+        off[q] = (uint32_t)(row * rb + (kA ? a_off : b_off)) / 4 * 4 +
+                 Swz::chunk(r, tid % kChunks) * 16;
     }
   });
   // The ragged last k-tile (K a multiple of the 16-byte chunk): bit q is set
@@ -124,7 +166,7 @@ __global__ __launch_bounds__(64 * kWM * kWN) void grouped_direct_kernel(const Gr
   // past every record and the range check returns zeros.  An N-contiguous B
   // slab's rows past K lie past its record count (K rows).
   uint32_t tail_past = 0;
-  static_for<kLoads>([&](auto q) {
+  static_for<kShift ? 0 : kLoads>([&](auto q) {
     constexpr bool kA = q < IA;
     constexpr int qq = kA ? q : q - IA;
     if constexpr (kA ? !kAT : !kBT) {
@@ -178,6 +220,27 @@ __global__ __launch_bounds__(64 * kWM * kWN) void grouped_direct_kernel(const Gr
     });
   }
 
+  // kShift: the dword after the fragment of step ks is dword 0 of the next
+  // chunk, or the row's tail dword after chunk 7 (the last step's upper lanes):
+  // its address, the distance between slots and between 32-row fragments
+  uint32_t na[kShift ? KSTEPS : 1], nb[kShift ? KSTEPS : 1], sh_a = 0, sh_b = 0;
+  uint32_t step_a = SLAB_A, step_b = SLAB_B, frag32 = 32 * kRowBytes;
+  if constexpr (kShift) {
+    const int ra = wm0 + (lane & 31), rb = wn0 + (lane & 31), half = lane >> 5;
+    sh_a = row_shift(true, ra);
+    sh_b = row_shift(false, rb);
+    static_for<KSTEPS>([&](auto ks) {
+      const int c = 2 * ks + half + 1;
+      na[ks] = c < 8 ? ra * kRowBytes + Swz::chunk(ra, c & 7) * 16 : TAIL_BASE + 4 * ra;
+      nb[ks] = c < 8 ? B_BASE + rb * kRowBytes + Swz::chunk(rb, c & 7) * 16
+                     : TAIL_BASE + 4 * (BM + rb);
+    });
+    if (half) {  // of the last step
+      step_a = step_b = kTail;
+      frag32 = 32 * 4;
+    }
+  }
+  uint32_t xa[kShift ? 2 : 1][FM], xb[kShift ? 2 : 1][FN];
   typename Atom::Acc acc[FM][FN];
   static_for<FM>([&](auto i) { static_for<FN>([&](auto j) { acc[i][j] = typename Atom::Acc{}; }); });
   Frag a[2][FM], b[2][FN];
@@ -206,6 +269,52 @@ __global__ __launch_bounds__(64 * kWM * kWN) void grouped_direct_kernel(const Gr
       static_for<FN>([&](auto j) { b[buf][j] = lds_frag_t(fbt[ks][j], slot * SLAB_B); });
     else
       static_for<FN>([&](auto j) { b[buf][j] = lds_frag(fb[ks], slot * SLAB_B + j * 32 * kRowBytes); });
+    if constexpr (kShift) {
+      static_for<FM>([&](auto i) {
+        const uint32_t at = ks + 1 < KSTEPS ? na[ks] + slot * SLAB_A + i * 32 * kRowBytes
+                                            : na[ks] + slot * step_a + i * frag32;
+        xa[buf][i] = *(const uint32_t*)(smem + at);
+      });
+      static_for<FN>([&](auto j) {
+        const uint32_t at = ks + 1 < KSTEPS ? nb[ks] + slot * SLAB_B + j * 32 * kRowBytes
+                                            : nb[ks] + slot * step_b + j * frag32;
+        xb[buf][j] = *(const uint32_t*)(smem + at);
+      });
+    }
+  };
+  // kShift: a step's fragments moved into place before its MFMAs
+  auto place = [&](auto buf) {
+    if constexpr (kShift) {
+      auto shift = [](Frag& w, uint32_t x, uint32_t sh) {
+        const uint32_t w0 = w[0], w1 = w[1], w2 = w[2], w3 = w[3];
+        w[0] = (int)__builtin_amdgcn_alignbyte(w1, w0, sh);
+        w[1] = (int)__builtin_amdgcn_alignbyte(w2, w1, sh);
+        w[2] = (int)__builtin_amdgcn_alignbyte(w3, w2, sh);
+        w[3] = (int)__builtin_amdgcn_alignbyte(x, w3, sh);
+      };
+      static_for<FM>([&](auto i) { shift(a[buf][i], xa[buf][i], sh_a); });
+      static_for<FN>([&](auto j) { shift(b[buf][j], xb[buf][j], sh_b); });
+    }
+  };
+  // kShift: clears what a ragged last k-tile in slot S holds past K (the next
+  // row's bytes), a thread a row, between its landing and its first reader
+  auto clear_tail = [&](int kt, auto S) {
+    if constexpr (kShift) {
+      if (kt != KTf) return;
+      if (tid < BM + BN) {
+        const bool is_a = tid < BM;
+        const int r = is_a ? tid : tid - BM;
+        uint8_t* row = smem + (is_a ? S * SLAB_A : B_BASE + S * SLAB_B) + r * kRowBytes;
+        const int first = (int)row_shift(is_a, min(r, is_a ? a_last : b_last)) + (K - KTf * BK) * EB;
+        for (int d = first >> 2; d < 33; ++d) {
+          uint32_t* w = d < 32 ? (uint32_t*)(row + Swz::chunk(r, d >> 2) * 16 + (d & 3) * 4)
+                               : (uint32_t*)(smem + TAIL_BASE + S * kTail + 4 * tid);
+          *w = d == first >> 2 ? *w & ((1u << (8 * (first & 3))) - 1u) : 0u;
+        }
+      }
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
+      stage_barrier();
+    }
   };
   auto mma = [&](auto buf, auto idx) {
     Atom::mma(acc[idx / FN][idx % FN], b[buf][idx % FN], a[buf][idx / FN]);
@@ -215,16 +324,21 @@ __global__ __launch_bounds__(64 * kWM * kWN) void grouped_direct_kernel(const Gr
     const int tt = min(t, KT - 1);
     const uint32_t kb = (uint32_t)tt * kRowBytes;
     const uint32_t o = (tt == KTf && ((tail_past >> q) & 1)) ? 0x80000000u : off[q];
-    if constexpr (q < IA && kAT)
+    if constexpr (q == IA + IB) {
+      const bool is_a = wave * 64 < BM;
+      dma4_buf(is_a ? A : B, off[q], kb, smem + TAIL_BASE + slot * kTail + wave * 256,
+               is_a ? a_bytes : b_bytes);
+    } else if constexpr (q < IA && kAT)
       dma16_buf(A, off[q], (uint32_t)(tt * BK) * (uint32_t)(p.lda * EB),
                 smem + slot * SLAB_A + (wave * 64 + NT * q) * 16, a_records);
     else if constexpr (q < IA)
-      dma16_buf(A, o, kb, smem + slot * SLAB_A + (wave * 64 + NT * q) * 16);
+      dma16_buf(A, o, kb, smem + slot * SLAB_A + (wave * 64 + NT * q) * 16, a_bytes);
     else if constexpr (kBT)
       dma16_buf(B, off[q], (uint32_t)(tt * BK) * (uint32_t)(p.ldb * EB),
                 smem + B_BASE + slot * SLAB_B + (wave * 64 + NT * (q - IA)) * 16, b_records);
     else
-      dma16_buf(B, o, kb, smem + B_BASE + slot * SLAB_B + (wave * 64 + NT * (q - IA)) * 16);
+      dma16_buf(B, o, kb, smem + B_BASE + slot * SLAB_B + (wave * 64 + NT * (q - IA)) * 16,
+                b_bytes);
   };
   // MFMAs [lo, hi) of a step with copies [q0, q0 + nq) of tile t spread
   // evenly between them: after MFMA k come copies [k*nq/n, (k+1)*nq/n).
@@ -248,6 +362,7 @@ __global__ __launch_bounds__(64 * kWM * kWN) void grouped_direct_kernel(const Gr
     const int ct = kt + kStages - 1;  // tile whose copies are issued now
     static_for<KSTEPS>([&](auto ks) {
       constexpr int cur = ks & 1;
+      place(std::integral_constant<int, cur>{});
       if constexpr (ks + 1 < KSTEPS) {
         read_frags(std::integral_constant<int, cur ^ 1>{}, S, std::integral_constant<int, ks + 1>{});
         __builtin_amdgcn_sched_group_barrier(0x100, kReads, 0);
@@ -263,6 +378,7 @@ __global__ __launch_bounds__(64 * kWM * kWN) void grouped_direct_kernel(const Gr
         if (kt + 1 < KT) {
           wait_vmcnt<kWait>();  // tile kt+1 landed (this thread's copies)
           stage_barrier();      // ... everyone's; tile kt-1's slot is free
+          clear_tail(kt + 1, Next{});
           read_frags(std::integral_constant<int, cur ^ 1>{}, Next{}, std::integral_constant<int, 0>{});
         }
         static_for<kMfmas - kMfmas / 2>([&](auto k) {
@@ -278,6 +394,7 @@ __global__ __launch_bounds__(64 * kWM * kWN) void grouped_direct_kernel(const Gr
     });
     wait_vmcnt<kWait>();
     stage_barrier();
+    clear_tail(0, std::integral_constant<int, 0>{});
     read_frags(std::integral_constant<int, 0>{}, std::integral_constant<int, 0>{},
                std::integral_constant<int, 0>{});
     for (int kt = 0; kt < KT; kt += kStages) {

@@ -6,8 +6,7 @@
 // registers.  A weight is used by one wave only, so nothing is staged: lane l
 // of a step loads 16 bytes of K of column l % 16 (and of row l % 16 of A, from
 // the caches) straight into the operands of the 16x16 matrix instruction --
-// any assignment of K to lanes is right while both operands share it, and the
-// loads need no alignment.  kU steps are loaded before the first is used.
+// any assignment of K to lanes is right while both operands share it.  kU steps are loaded before the first is used.
 // The waves' partial sums meet in LDS in a fixed order, and the epilogue runs
 // element by element, consecutive lanes along a row of D.
 //
@@ -48,12 +47,26 @@ struct Step16<kE4M3> {
   }
 };
 
-__device__ __forceinline__ i32x4 load16_any(const uint8_t* p) {
-  typedef int i32x4_a1 __attribute__((ext_vector_type(4), aligned(1)));
-  return *(const i32x4_a1*)p;
-}
+// Sixteen bytes of a row.  kDword: rows start on dwords, one load.  Otherwise
+// the dword-aligned sixteen bytes and the dword after them, shifted into place
+// when they are used: loads at other addresses take twice as long (128 bf16
+// rows on 32 experts of 2048 x 4095: 243 us unaligned).
+template <bool kDword>
+struct Chunk {
+  i32x4 v;
+  uint32_t hi;
+  __device__ __forceinline__ void load(const uint8_t* p) {
+    typedef int i32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
+    if constexpr (kDword) v = *(const i32x4_a4*)p;
+    else load16_split(p, v, hi);
+  }
+  __device__ __forceinline__ i32x4 get(uint32_t sh) const {
+    if constexpr (kDword) return v;
+    else return realign16(v, hi, sh);
+  }
+};
 
-template <int kCode, int MT, int NT, int kWaves>
+template <int kCode, int MT, int NT, int kWaves, bool kDword>
 __global__ __launch_bounds__(64 * kWaves) void grouped_few_rows_kernel(const GroupedParams p) {
   using S = Step16<kCode>;
   typedef typename S::Acc Acc;
@@ -79,20 +92,25 @@ __global__ __launch_bounds__(64 * kWaves) void grouped_few_rows_kernel(const Gro
     const int n = n0 + min(16 * (int)j + (lane & 15), cols - 1);
     pb[j] = p.B + ((int64_t)t.e * p.stride_b + (int64_t)n * p.ldb) * EB + 16 * (lane >> 4);
   });
+  // rows 16 apart share a byte shift
+  const uint32_t sa = (uint32_t)(uintptr_t)pa[0] & 3u, sb = (uint32_t)(uintptr_t)pb[0] & 3u;
   Acc acc[MT][NT];
   static_for<MT>([&](auto i) { static_for<NT>([&](auto j) { acc[i][j] = Acc{}; }); });
 
   const int whole = min(s1, kbytes / 64);  // steps inside K
   int s = s0;
   for (; s + kU <= whole; s += kU) {
-    i32x4 a[kU][MT], b[kU][NT];
+    Chunk<kDword> a[kU][MT], b[kU][NT];
     static_for<kU>([&](auto u) {
-      static_for<NT>([&](auto j) { b[u][j] = load16_any(pb[j] + (int64_t)(s + u) * 64); });
-      static_for<MT>([&](auto i) { a[u][i] = load16_any(pa[i] + (int64_t)(s + u) * 64); });
+      static_for<NT>([&](auto j) { b[u][j].load(pb[j] + (int64_t)(s + u) * 64); });
+      static_for<MT>([&](auto i) { a[u][i].load(pa[i] + (int64_t)(s + u) * 64); });
     });
     static_for<kU>([&](auto u) {
+      i32x4 bb[NT];
+      static_for<NT>([&](auto j) { bb[j] = b[u][j].get(sb); });
       static_for<MT>([&](auto i) {
-        static_for<NT>([&](auto j) { S::mma(acc[i][j], b[u][j], a[u][i]); });
+        const i32x4 aa = a[u][i].get(sa);
+        static_for<NT>([&](auto j) { S::mma(acc[i][j], bb[j], aa); });
       });
     });
   }
@@ -102,8 +120,12 @@ __global__ __launch_bounds__(64 * kWaves) void grouped_few_rows_kernel(const Gro
     const int left = kbytes - (s * 64 + 16 * (lane >> 4));
     auto get = [&](const uint8_t* base) {
       const uint8_t* q = base + (int64_t)s * 64;
-      if (left >= 16) return load16_any(q);
       i32x4 x = {0, 0, 0, 0};
+      if (left >= 16) {
+        Chunk<false> c;
+        c.load(q);
+        return c.get((uint32_t)(uintptr_t)q & 3u);
+      }
       if (left > 0) x = gather16<EB>(q, EB, 0, left / EB, left / EB - 1);
       return x;
     };
@@ -147,13 +169,20 @@ __global__ __launch_bounds__(64 * kWaves) void grouped_few_rows_kernel(const Gro
 
 template <int kCode, int MT, int NT, int kWaves>
 int launch(const GroupedParams& p0, hipStream_t stream) {
+  constexpr int EB = type_bytes(kCode);
   GroupedParams p = p0;
   p.tiles_n = (p.N + 16 * NT - 1) / (16 * NT);
   const int64_t grid = row_tiles_bound(p.rows, p.groups, 16 * MT) * p.tiles_n;
   if (grid <= 0) return TLA_OK;
   if (grid > 0x7FFFFFFF) return TLA_ERR_UNSUPPORTED;
-  hipLaunchKernelGGL((grouped_few_rows_kernel<kCode, MT, NT, kWaves>), dim3((unsigned)grid),
-                     dim3(64 * kWaves), 0, stream, p);
+  const bool dword = aligned(p.A, 4) && aligned(p.B, 4) && p.lda * EB % 4 == 0 &&
+                     p.ldb * EB % 4 == 0 && (p.groups == 1 || p.stride_b * EB % 4 == 0);
+  if (dword)
+    hipLaunchKernelGGL((grouped_few_rows_kernel<kCode, MT, NT, kWaves, true>), dim3((unsigned)grid),
+                       dim3(64 * kWaves), 0, stream, p);
+  else
+    hipLaunchKernelGGL((grouped_few_rows_kernel<kCode, MT, NT, kWaves, false>),
+                       dim3((unsigned)grid), dim3(64 * kWaves), 0, stream, p);
   return hipGetLastError() == hipSuccess ? TLA_OK : TLA_ERR_HIP;
 }
 

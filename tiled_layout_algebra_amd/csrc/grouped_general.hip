@@ -3,14 +3,18 @@
 //
 // A workgroup of four wavefronts owns 128 x 128 of D, each wave 64 x 64 of
 // it, two LDS stages of 128 bytes of K.  Product: tiles come from the ragged
-// lookup (row_tile), A and B are read through gemm_common.hpp's
-// register-staged loaders (16-byte chunks at any byte address, shifted into
-// place on the way to LDS), B K-contiguous, 16-bit N-contiguous (its slab as
-// k rows of n, read back transposed) or 8-bit N-contiguous (element by
-// element).  Weight gradient: the sum runs over an expert's rows, so both
-// operands are k-row slabs.  Tile kt + 1 is loaded into registers before the
-// MFMAs of tile kt and written to the other stage after them; whole and
-// ragged k-tiles have loops of their own.
+// lookup (row_tile), B K-contiguous, 16-bit N-contiguous (its slab as k rows
+// of n, read back transposed) or 8-bit N-contiguous.  Weight gradient: the sum
+// runs over an expert's rows, so both operands are k-row slabs.
+//
+// Chunks of sixteen bytes are loaded through dword-aligned addresses and
+// shifted into place on the way to LDS.  A chunk that would pass the end of
+// its line starts early enough to end with it and is shifted down by the
+// difference, which puts zeros past the end: no load is predicated, none
+// leaves the matrix, and every k-tile runs the same code, two tiles ahead of
+// the MFMAs in two register sets.  (One loop for whole and another, chunk by
+// chunk, for ragged k-tiles: 555 rows' gradient 277 x 1688 took 29 us.)  Lines
+// shorter than a chunk and 8-bit N-contiguous weights go element by element.
 #include "grouped_common.hpp"
 
 namespace tla {
@@ -18,7 +22,65 @@ namespace {
 
 enum : int { kBKc = 0, kBElem = 1, kBRows = 2 };
 
-template <int kCode, int kBView, bool kWgrad>
+// Sixteen bytes shifted down by n bytes, zeros coming in; 16 and more: zeros.
+__device__ __forceinline__ i32x4 shift_down(const i32x4& v, int n) {
+  const bool one = n & 4, two = n & 8, out = n >= 16;
+  const uint32_t v0 = v[0], v1 = v[1], v2 = v[2], v3 = v[3], sh = (uint32_t)n & 3u;
+  const uint32_t a0 = one ? v1 : v0, a1 = one ? v2 : v1, a2 = one ? v3 : v2, a3 = one ? 0u : v3;
+  const uint32_t b0 = two ? a2 : a0, b1 = two ? a3 : a1, b2 = two ? 0u : a2, b3 = two ? 0u : a3;
+  return i32x4{out ? 0 : (int)__builtin_amdgcn_alignbyte(b1, b0, sh),
+               out ? 0 : (int)__builtin_amdgcn_alignbyte(b2, b1, sh),
+               out ? 0 : (int)__builtin_amdgcn_alignbyte(b3, b2, sh),
+               out ? 0 : (int)__builtin_amdgcn_alignbyte(0u, b3, sh)};
+}
+
+// One operand's slab of a k-tile in registers: 1024 chunks, four a thread.
+// kRows: 64 rows of k, each 128 columns (16-bit; chunk c of row r stored at
+// c ^ 4 (r % 4), as load_frag_nt reads it); otherwise 128 rows of 128 bytes of
+// K (load_frag's swizzle).  Lines hold at least one chunk.
+template <int EB, bool kRows>
+struct LooseSlab {
+  static constexpr int kCE = 16 / EB, kI = 4;
+  i32x4 v[kI];
+  uint32_t hi[kI];
+  uint32_t shifts;
+
+  static __device__ __forceinline__ int row(int tid, int it) {
+    return (tid + 256 * it) / (kRows ? 16 : 8);
+  }
+  static __device__ __forceinline__ int col(int tid, int it) {
+    return (tid + 256 * it) % (kRows ? 16 : 8) * kCE;
+  }
+  // lines first + row (clamped to the last one), elements at + col
+  __device__ __forceinline__ void load(const uint8_t* __restrict__ base, int64_t ld, int first,
+                                       int lines, int at, int len, int tid) {
+    shifts = 0;
+#pragma unroll
+    for (int it = 0; it < kI; ++it) {
+      const int r = min(first + row(tid, it), lines - 1), c = min(at + col(tid, it), len - kCE);
+      shifts |= load16_split(base + ((int64_t)r * ld + c) * EB, v[it], hi[it]) << (4 * it);
+    }
+  }
+  // cut: the tile passes the lines' end; gone: (kRows) passes the last line
+  __device__ __forceinline__ void store(uint8_t* slab, int first, int lines, int at, int len,
+                                        int tid) const {
+    const bool cut = at + (kRows ? 128 : 128 / EB) > len;
+    const bool gone = kRows && first + 64 > lines;
+#pragma unroll
+    for (int it = 0; it < kI; ++it) {
+      i32x4 x = realign16(v[it], hi[it], shifts >> (4 * it));
+      const int r = row(tid, it), c = col(tid, it);
+      if (cut) x = shift_down(x, max(at + c - (len - kCE), 0) * EB);
+      if (gone && first + r >= lines) x = i32x4{0, 0, 0, 0};
+      if constexpr (kRows)
+        *(i32x4*)(slab + r * 256 + ((c / 8) ^ (4 * (r & 3))) * 16) = x;
+      else
+        *(i32x4*)(slab + r * 128 + Slab<128>::Swz::chunk(r, c / kCE) * 16) = x;
+    }
+  }
+};
+
+template <int kCode, int kBView, bool kWgrad, bool kLoose>
 __global__ __launch_bounds__(kThreads, kBView == kBElem ? 1 : 2) void grouped_general_kernel(
     const GroupedParams p) {
   using Atom = std::conditional_t<kCode == kE4M3, E4m3AsF16, OpAtom<kCode>>;
@@ -86,49 +148,78 @@ __global__ __launch_bounds__(kThreads, kBView == kBElem ? 1 : 2) void grouped_ge
     });
   };
 
-  using RA = std::conditional_t<kAT, RegSlabNT<BM, BK>, RegSlab<BM, EB, kRowBytes, true>>;
-  using RB = std::conditional_t<kNT, RegSlabNT<BN, BK>, RegSlab<BN, EB, kRowBytes, kBView == kBKc>>;
-  RA ra;
-  RB rb;
   const int KT = (K + BK - 1) / BK;
-  // Whole tiles: inside K; where a k-rows slab's tile crosses its matrix's
-  // edge also before the tile that holds row K - 1 (whole chunks there read
-  // on into the next row).
-  const bool m_edge = kAT && m0 + BM > m_end, n_edge = kNT && n0 + BN > N;
-  const int KTw = kBView == kBElem ? 0
-                  : (m_edge || n_edge)
-                      ? ((m_edge && m_end < 8) || (n_edge && N < 8) ? 0 : (K - 1) / BK)
-                      : K / BK;
-  auto load = [&](int k0, auto whole) {
-    if constexpr (whole) {
-      ra.load_whole(A, p.lda, m0, m_end, k0, tid);
-      if constexpr (kBView != kBElem) rb.load_whole(B, p.ldb, n0, N, k0, tid);
-    } else {
+  if constexpr (kLoose) {
+    LooseSlab<EB, kAT> ra[2];
+    LooseSlab<EB, kNT> rb[2];
+    auto load = [&](int kt, auto set) {
+      const int k0 = min(kt, KT - 1) * BK;
+      if constexpr (kAT) ra[set].load(A, p.lda, k0, K, m0, m_end, tid);
+      else ra[set].load(A, p.lda, m0, m_end, k0, K, tid);
+      if constexpr (kNT) rb[set].load(B, p.ldb, k0, K, n0, N, tid);
+      else rb[set].load(B, p.ldb, n0, N, k0, K, tid);
+    };
+    auto store = [&](int kt, auto set) {
+      uint8_t* st = smem + (kt & 1) * STAGE;
+      const int k0 = kt * BK;
+      if constexpr (kAT) ra[set].store(st, k0, K, m0, m_end, tid);
+      else ra[set].store(st, m0, m_end, k0, K, tid);
+      if constexpr (kNT) rb[set].store(st + SLAB_A, k0, K, n0, N, tid);
+      else rb[set].store(st + SLAB_A, n0, N, k0, K, tid);
+    };
+    using S0 = std::integral_constant<int, 0>;
+    using S1 = std::integral_constant<int, 1>;
+    auto fenced_compute = [&](int kt) {
+      __builtin_amdgcn_sched_barrier(0);
+      compute(smem + (kt & 1) * STAGE);
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    // tile kt in LDS, tile kt + 1 in set S ^ 1: load tile kt + 2 into set S,
+    // multiply, hand tile kt + 1 on.  No branch in the loop, so the waits for
+    // loads count exactly.
+    auto step = [&](int kt, auto S) {
+      load(kt + 2, S);
+      fenced_compute(kt);
+      store(kt + 1, std::integral_constant<int, S ^ 1>{});
+      __syncthreads();
+    };
+    if (KT > 0) {
+      load(0, S0{});
+      load(1, S1{});  // (past the end: the last tile again)
+      store(0, S0{});
+      __syncthreads();
+      int kt = 0;
+      for (; kt + 2 < KT; kt += 2) {
+        step(kt, S0{});
+        step(kt + 1, S1{});
+      }
+      if (kt + 1 < KT) {
+        fenced_compute(kt);
+        store(kt + 1, S1{});
+        __syncthreads();
+        ++kt;
+      }
+      compute(smem + (kt & 1) * STAGE);
+    }
+  } else {
+    using RA = std::conditional_t<kAT, RegSlabNT<BM, BK>, RegSlab<BM, EB, kRowBytes, true>>;
+    using RB =
+        std::conditional_t<kNT, RegSlabNT<BN, BK>, RegSlab<BN, EB, kRowBytes, kBView == kBKc>>;
+    RA ra;
+    RB rb;
+    auto load = [&](int k0) {
       ra.load_edge(A, p.lda, m0, m_end, k0, K, tid);
       rb.load_edge(B, p.ldb, n0, N, k0, K, tid);
+    };
+    if (KT > 0) load(0);
+    for (int kt = 0; kt < KT; ++kt) {
+      ra.store(smem, tid);
+      rb.store(smem + SLAB_A, tid);
+      __syncthreads();
+      if (kt + 1 < KT) load((kt + 1) * BK);
+      compute(smem);
+      __syncthreads();
     }
-  };
-  auto store = [&](uint8_t* st) {
-    ra.store(st, tid);
-    rb.store(st + SLAB_A, tid);
-  };
-  auto step = [&](int kt, auto whole) {  // load tile kt + 1, multiply tile kt
-    load((kt + 1) * BK, whole);
-    __builtin_amdgcn_sched_barrier(0);
-    compute(smem + (kt & 1) * STAGE);
-    __builtin_amdgcn_sched_barrier(0);
-    store(smem + ((kt + 1) & 1) * STAGE);
-    __syncthreads();
-  };
-  if (KT > 0) {
-    if (KTw > 0) load(0, std::true_type{});
-    else load(0, std::false_type{});
-    store(smem);
-    __syncthreads();
-    int kt = 0;
-    for (; kt + 1 < KTw; ++kt) step(kt, std::true_type{});
-    for (; kt + 1 < KT; ++kt) step(kt, std::false_type{});
-    compute(smem + (kt & 1) * STAGE);
   }
   __syncthreads();  // the stages become the waves' epilogue regions
   uint8_t* region = smem + wave * WM * 64 * FN;
@@ -138,8 +229,8 @@ __global__ __launch_bounds__(kThreads, kBView == kBElem ? 1 : 2) void grouped_ge
     grouped_epilogue<kCode, FM, FN>(p, e, m_end, m0 + wm0, n0 + wn0, lane, acc, region);
 }
 
-template <int kCode, int kBView, bool kWgrad>
-int launch(const GroupedParams& p0, hipStream_t stream) {
+template <int kCode, int kBView, bool kWgrad, bool kLoose>
+int launch_form(const GroupedParams& p0, hipStream_t stream) {
   GroupedParams p = p0;
   p.tiles_n = (p.N + 127) / 128;
   p.tiles_m = (p.M + 127) / 128;
@@ -147,9 +238,21 @@ int launch(const GroupedParams& p0, hipStream_t stream) {
                               : row_tiles_bound(p.rows, p.groups, 128) * p.tiles_n;
   if (grid <= 0) return TLA_OK;
   if (grid > 0x7FFFFFFF) return TLA_ERR_UNSUPPORTED;
-  hipLaunchKernelGGL((grouped_general_kernel<kCode, kBView, kWgrad>), dim3((unsigned)grid),
+  hipLaunchKernelGGL((grouped_general_kernel<kCode, kBView, kWgrad, kLoose>), dim3((unsigned)grid),
                      dim3(kThreads), 0, stream, p);
   return hipGetLastError() == hipSuccess ? TLA_OK : TLA_ERR_HIP;
+}
+
+template <int kCode, int kBView, bool kWgrad>
+int launch(const GroupedParams& p, hipStream_t stream) {
+  if constexpr (kBView != kBElem) {
+    constexpr int kCE = 16 / type_bytes(kCode);
+    // the lines: of K (A, or both), of N, of both extents of the gradient
+    const bool a_long = kWgrad ? p.M >= kCE : p.K >= kCE;
+    const bool b_long = kBView == kBKc ? p.K >= kCE : p.N >= kCE;
+    if (a_long && b_long) return launch_form<kCode, kBView, kWgrad, true>(p, stream);
+  }
+  return launch_form<kCode, kBView, kWgrad, false>(p, stream);
 }
 
 // Column sums of each expert's rows of Y, 64 columns a workgroup: 8 lanes

@@ -71,6 +71,7 @@ int launch_wgrad_two_group(const GroupedParams& p, int type, hipStream_t stream)
 enum DirectShape : int { kDirect64x3, kDirect128x2, kDirect128x3 };
 int launch_grouped_direct(const GroupedParams& p, int type, int shape, hipStream_t stream);
 int launch_grouped_direct_kn(const GroupedParams& p, int type, int shape, hipStream_t stream);
+int launch_grouped_direct_shift(const GroupedParams& p, int type, int shape, hipStream_t stream);
 int launch_wgrad_direct(const GroupedParams& p, int type, int shape, hipStream_t stream);
 
 // The kernel for few rows an expert (grouped_few_rows.hip): B K-contiguous,

@@ -26,12 +26,12 @@ bool aligned_to(const void* p, int64_t bytes) { return (uintptr_t)p % (uintptr_t
 // what a validated call runs: the variant ids of the public header, or nothing
 enum Kernel {
   kNoop = -1, kGeneral, kTwoGroup, kDirect128, kDirect64, kFewRows4, kFewRows2, kFewRows1,
-  kTwoGroupShift
+  kTwoGroupShift, kDirect128Shift, kDirect64Shift
 };
 const char* const kNames[TLA_GROUPED_VARIANTS] = {
     "grouped_general_128x128", "grouped_two_group_256x256", "grouped_direct_128x128",
     "grouped_direct_64x128", "grouped_few_rows_64", "grouped_few_rows_32", "grouped_few_rows_16",
-    "grouped_two_group_shift_256x256"};
+    "grouped_two_group_shift_256x256", "grouped_direct_shift_128x128", "grouped_direct_shift_64x128"};
 
 struct Plan {
   GroupedParams p;
@@ -51,7 +51,7 @@ bool takes(Kernel k, const tla_grouped_gemm_args* a, int eb, bool b_kc) {
   if (a->type == TLA_E4M3 && a->K < kMinKE4m3) return false;
   // 32-bit offsets within a tile's rows
   if (a->lda * eb >= (kLimit >> 8) || (b_kc && a->ldb * eb >= (kLimit >> 8))) return false;
-  if (k == kTwoGroupShift) return b_kc;
+  if (k >= kTwoGroupShift) return b_kc;
   if (k == kDirect64 && !b_kc) return false;
   if (a->K * eb % 16 != 0 || !rows16(a->A, a->lda, eb) || !rows16(a->B, a->ldb, eb) ||
       (a->groups > 1 && a->stride_b * eb % 16 != 0))
@@ -106,16 +106,19 @@ Kernel choose(const tla_grouped_gemm_args* a, int eb, bool b_kc) {
   consider(kFewRows1, 4.0 + row_blocks(a, 16) * matrix / 5.0);
   consider(kFewRows2, 4.3 + row_blocks(a, 32) * matrix / 3.3);
   consider(kFewRows4, 5.0 + row_blocks(a, 64) * matrix / 2.2);
-  const double t64 = 0.0016 * tiles(64, 128), t128 = tiles(128, 128), t256 = tiles(256, 256);
-  consider(kDirect64, 4.2 + kt * (t64 > 0.3 ? t64 : 0.3));
-  consider(kDirect128, 4.5 + kt * (t128 <= 128.0 ? 0.4 : 0.66 * rounds(t128)));
-  consider(kTwoGroup, 5.0 + kt * (t256 <= 128.0 ? 1.25 : 1.6 * rounds(t256)));
-  // any alignment: 16384 bf16 rows on 8 experts of 4096 x 4095 725 us for the
-  // shifting kernel against 1095 for the general one, 3001 int8 rows 4096 x
-  // 4095 71 against 118; 2000 f16 rows on 8 experts of 2047 x 1023 46 against 43
-  consider(kTwoGroupShift,
-           6.0 + (double)(a->K * eb / 96 + 1) * (t256 <= 128.0 ? 1.5 : 1.65 * rounds(t256)));
-  consider(kGeneral, 4.5 + kt * 1.8 * rounds(t128 / 2.0));
+  const double t64 = tiles(64, 128), t128 = tiles(128, 128), t256 = tiles(256, 256);
+  auto at_least = [](double least, double us) { return us > least ? us : least; };
+  consider(kDirect64, 4.2 + kt * at_least(0.3, (eb == 1 ? 0.0015 : 0.0019) * t64));
+  consider(kDirect128, 4.5 + kt * (t128 <= 128.0 ? 0.4 : t128 <= 256.0 ? 0.54 : 0.62 * rounds(t128)));
+  consider(kTwoGroup, at_least(4.0 + 1.2 * weights, 5.0 + kt * (t256 <= 64.0 ? 1.0 : t256 <= 128.0 ? 1.25 : 1.6 * rounds(t256))));
+  // any alignment: with B 4096 x 4095 int8, 3001 rows: 121 us (64 rows), 99
+  // (128), 68 (256), 115 (general); with 988 x 2371, 400 rows 18, 23, 40, 33;
+  // bf16, 4096 rows on 32 experts of 2048 x 4095: 305, 247, 285, 269
+  const double kt96 = (double)(a->K * eb / 96 + 1);
+  consider(kDirect64Shift, 4.5 + kt * at_least(0.6, (eb == 1 ? 0.0024 : 0.0032) * t64));
+  consider(kDirect128Shift, 4.8 + kt * 0.96 * rounds(t128));
+  consider(kTwoGroupShift, 6.0 + kt96 * (t256 <= 128.0 ? 1.3 : 1.6 * rounds(t256)));
+  consider(kGeneral, 4.5 + kt * at_least(1.5, 2.05 * rounds(t128 / 2.0)));
   return best;
 }
 
@@ -203,6 +206,8 @@ int run_product(const tla_grouped_gemm_args* a, hipStream_t stream, int forced =
       if (!plan.b_kc) return launch_two_group_kn(p, t, stream);
       return type_bytes(t) == 1 ? launch_two_group_nk8(p, t, stream)
                                 : launch_two_group_nk16(p, t, stream);
+    case kDirect128Shift: return launch_grouped_direct_shift(p, t, kDirect128x3, stream);
+    case kDirect64Shift: return launch_grouped_direct_shift(p, t, kDirect64x3, stream);
     case kTwoGroupShift: return launch_two_group_shift(p, t, stream);
     case kDirect64: return launch_grouped_direct(p, t, kDirect64x3, stream);
     case kDirect128: {
