@@ -266,7 +266,8 @@ int tla_grouped_gemm_run_variant(const tla_grouped_gemm_args *args, int32_t vari
  * (TLA_ROW_MAJOR: [K, N] weights, ldd >= N; TLA_COL_MAJOR: [N, K] weights,
  * ldd >= K).  Sums are fp32, rounded once at the end, in an order that does
  * not change from call to call.  An expert without rows gets zeros; D is
- * overwritten.  offsets as for tla_grouped_gemm.  K or N == 0 writes no D.
+ * overwritten.  offsets as for tla_grouped_gemm.  groups, K or N == 0 is a
+ * no-op.
  */
 typedef struct {
   int64_t groups, rows, N, K;

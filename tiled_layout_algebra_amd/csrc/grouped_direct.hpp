@@ -80,11 +80,14 @@ __global__ __launch_bounds__(64 * kWM * kWN) void grouped_direct_kernel(const Gr
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   int e, m0, m_end, n0, K;
+  bool sum_a = false, sum_b = false;  // gradient: this wave sums dY's lines
   const uint8_t *A = p.A, *B = p.B;
   if constexpr (kForm == kGrad) {
     int tm, tn, lo, hi;
     wgrad_tile(p, blockIdx.x, gridDim.x, e, tm, tn);
     expert_rows(p, e, lo, hi);
+    sum_a = p.dbias && (p.flags & kOpSumA) && tn == 0 && wave / kWM == 0;
+    sum_b = p.dbias && !(p.flags & kOpSumA) && tm == 0 && wave % kWM == 0;
     m0 = tm * BM;
     m_end = p.M;
     n0 = tn * BN;
@@ -243,6 +246,8 @@ __global__ __launch_bounds__(64 * kWM * kWN) void grouped_direct_kernel(const Gr
   uint32_t xa[kShift ? 2 : 1][FM], xb[kShift ? 2 : 1][FN];
   typename Atom::Acc acc[FM][FN];
   static_for<FM>([&](auto i) { static_for<FN>([&](auto j) { acc[i][j] = typename Atom::Acc{}; }); });
+  LineSums<kCode, (FM > FN ? FM : FN)> sums;
+  if constexpr (kForm == kGrad) sums.init(lane);
   Frag a[2][FM], b[2][FN];
   auto lds_frag = [&](const uint32_t (&base)[kSub], int imm) -> Frag {
     if constexpr (kSub == 1) {
@@ -363,6 +368,10 @@ __global__ __launch_bounds__(64 * kWM * kWN) void grouped_direct_kernel(const Gr
     static_for<KSTEPS>([&](auto ks) {
       constexpr int cur = ks & 1;
       place(std::integral_constant<int, cur>{});
+      if constexpr (kForm == kGrad) {
+        if (sum_b) static_for<FN>([&](auto j) { sums.template add<j>(b[cur][j]); });
+        if (sum_a) static_for<FM>([&](auto i) { sums.template add<i>(a[cur][i]); });
+      }
       if constexpr (ks + 1 < KSTEPS) {
         read_frags(std::integral_constant<int, cur ^ 1>{}, S, std::integral_constant<int, ks + 1>{});
         __builtin_amdgcn_sched_group_barrier(0x100, kReads, 0);
@@ -410,6 +419,10 @@ __global__ __launch_bounds__(64 * kWM * kWN) void grouped_direct_kernel(const Gr
   static_assert((NT / 64) * WM * 64 * FN <= kStages * (SLAB_A + SLAB_B), "epilogue regions");
   __syncthreads();
   uint8_t* region = smem + wave * WM * 64 * FN;
+  if constexpr (kForm == kGrad) {
+    if (sum_b) sums.template write<FN>(p.dbias + (int64_t)e * p.N, n0 + wn0, p.N, lane);
+    if (sum_a) sums.template write<FM>(p.dbias + (int64_t)e * p.M, m0 + wm0, p.M, lane);
+  }
   if constexpr (kForm == kGrad)
     wgrad_epilogue<FM, FN>(p, e, m0 + wm0, n0 + wn0, lane, acc, region);
   else

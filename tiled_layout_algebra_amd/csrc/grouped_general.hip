@@ -97,11 +97,14 @@ __global__ __launch_bounds__(kThreads, kBView == kBElem ? 1 : 2) void grouped_ge
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   int e, m0, m_end, n0, K;
+  bool sum_a = false, sum_b = false;  // gradient: this wave sums dY's lines
   const uint8_t *A = p.A, *B = p.B;
   if constexpr (kWgrad) {
     int tm, tn, lo, hi;
     wgrad_tile(p, blockIdx.x, gridDim.x, e, tm, tn);
     expert_rows(p, e, lo, hi);
+    sum_a = p.dbias && (p.flags & kOpSumA) && tn == 0 && !(wave >> 1);
+    sum_b = p.dbias && !(p.flags & kOpSumA) && tm == 0 && !(wave & 1);
     m0 = tm * BM;
     n0 = tn * BN;
     m_end = p.M;
@@ -123,6 +126,8 @@ __global__ __launch_bounds__(kThreads, kBView == kBElem ? 1 : 2) void grouped_ge
 
   typename Atom::Acc acc[FM][FN];
   static_for<FM>([&](auto i) { static_for<FN>([&](auto j) { acc[i][j] = typename Atom::Acc{}; }); });
+  LineSums<kCode, FM> sums;
+  if constexpr (kWgrad) sums.init(lane);
   Frag a[2][FM], b[2][FN];
   auto read_frags = [&](auto buf, const uint8_t* stage, auto ks) {
     static_for<FM>([&](auto i) {
@@ -145,6 +150,10 @@ __global__ __launch_bounds__(kThreads, kBView == kBElem ? 1 : 2) void grouped_ge
       static_for<FM * FN>([&](auto q) {
         Atom::mma(acc[q / FN][q % FN], b[cur][q % FN], a[cur][q / FN]);
       });
+      if constexpr (kWgrad) {
+        if (sum_b) static_for<FN>([&](auto j) { sums.template add<j>(b[cur][j]); });
+        if (sum_a) static_for<FM>([&](auto i) { sums.template add<i>(a[cur][i]); });
+      }
     });
   };
 
@@ -223,6 +232,10 @@ __global__ __launch_bounds__(kThreads, kBView == kBElem ? 1 : 2) void grouped_ge
   }
   __syncthreads();  // the stages become the waves' epilogue regions
   uint8_t* region = smem + wave * WM * 64 * FN;
+  if constexpr (kWgrad) {
+    if (sum_b) sums.template write<FN>(p.dbias + (int64_t)e * p.N, n0 + wn0, p.N, lane);
+    if (sum_a) sums.template write<FM>(p.dbias + (int64_t)e * p.M, m0 + wm0, p.M, lane);
+  }
   if constexpr (kWgrad)
     wgrad_epilogue<FM, FN>(p, e, m0 + wm0, n0 + wn0, lane, acc, region);
   else
@@ -255,50 +268,6 @@ int launch(const GroupedParams& p, hipStream_t stream) {
   return launch_form<kCode, kBView, kWgrad, false>(p, stream);
 }
 
-// Column sums of each expert's rows of Y, 64 columns a workgroup: 8 lanes
-// cover a row's 128 bytes, 32 rows at a time; the 32 partial sums of a column
-// are joined in LDS in a fixed order.
-template <int kCode>
-__global__ __launch_bounds__(256) void group_colsum_kernel(const GroupedParams p, const uint8_t* Y,
-                                                           int64_t ldy, int N) {
-  __shared__ float part[32][65];
-  const int e = blockIdx.y, c0 = blockIdx.x * 64, tid = threadIdx.x;
-  const int c = c0 + 8 * (tid & 7), r0 = tid >> 3;
-  int lo, hi;
-  expert_rows(p, e, lo, hi);
-  float s[8] = {};
-  auto add = [&](const i32x4& v) {
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      s[2 * w] += widen_lo<kCode == kBF16>((uint32_t)v[w]);
-      s[2 * w + 1] += widen_hi<kCode == kBF16>((uint32_t)v[w]);
-    }
-  };
-  if (c + 8 <= N) {
-    int r = lo + r0;
-    for (; r + 7 * 32 < hi; r += 8 * 32) {
-      i32x4 v[8];
-#pragma unroll
-      for (int u = 0; u < 8; ++u) v[u] = load16_even(Y + ((int64_t)(r + 32 * u) * ldy + c) * 2);
-#pragma unroll
-      for (int u = 0; u < 8; ++u) add(v[u]);
-    }
-    for (; r < hi; r += 32) add(load16_even(Y + ((int64_t)r * ldy + c) * 2));
-  } else if (c < N) {
-    for (int r = lo + r0; r < hi; r += 32)
-      add(gather16<2>(Y + (int64_t)r * ldy * 2, 2, c, N, N - 1));
-  }
-#pragma unroll
-  for (int q = 0; q < 8; ++q) part[r0][8 * (tid & 7) + q] = s[q];
-  __syncthreads();
-  if (tid < 64 && c0 + tid < N) {
-    float t = 0.f;
-#pragma unroll
-    for (int r = 0; r < 32; ++r) t += part[r][tid];
-    p.dbias[(int64_t)e * N + c0 + tid] = t;
-  }
-}
-
 }  // namespace
 
 int launch_grouped_general(const GroupedParams& p, int type, bool b_kc, hipStream_t s) {
@@ -321,16 +290,6 @@ int launch_wgrad_general(const GroupedParams& p, int type, hipStream_t s) {
     case TLA_F16: return launch<kF16, kBRows, true>(p, s);
     default: return TLA_ERR_UNSUPPORTED;
   }
-}
-
-int launch_group_colsum(const GroupedParams& p, const uint8_t* Y, int64_t ldy, int type, int N,
-                        hipStream_t s) {
-  const dim3 grid((unsigned)((N + 63) / 64), (unsigned)p.groups);
-  if (type == TLA_BF16)
-    hipLaunchKernelGGL(group_colsum_kernel<kBF16>, grid, dim3(256), 0, s, p, Y, ldy, N);
-  else
-    hipLaunchKernelGGL(group_colsum_kernel<kF16>, grid, dim3(256), 0, s, p, Y, ldy, N);
-  return hipGetLastError() == hipSuccess ? TLA_OK : TLA_ERR_HIP;
 }
 
 }  // namespace tla

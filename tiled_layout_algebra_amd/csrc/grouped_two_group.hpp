@@ -73,11 +73,14 @@ __global__ __launch_bounds__(512) void grouped_two_group_kernel(const GroupedPar
   // Product: rows m0 .. m_end - 1 of A are the expert's.  Gradient: the
   // expert's rows are the K of both operands, m0 and n0 columns of them.
   int e, m0, m_end, n0, K;
+  bool sum_a = false, sum_b = false;  // gradient: this wave sums dY's lines
   const uint8_t *A = p.A, *B = p.B;
   if constexpr (kForm == kGrad) {
     int tm, tn, lo, hi;
     wgrad_tile(p, blockIdx.x, gridDim.x, e, tm, tn);
     expert_rows(p, e, lo, hi);
+    sum_a = p.dbias && (p.flags & kOpSumA) && tn == 0 && !((wave >> 1) & 1);
+    sum_b = p.dbias && !(p.flags & kOpSumA) && tm == 0 && grp == 0 && !(wave & 1);
     m0 = tm * BM;
     m_end = p.M;
     n0 = tn * BN;
@@ -349,6 +352,8 @@ __global__ __launch_bounds__(512) void grouped_two_group_kernel(const GroupedPar
   };
   typename Atom::Acc acc[FM][FN];
   static_for<FM>([&](auto i) { static_for<FN>([&](auto j) { acc[i][j] = typename Atom::Acc{}; }); });
+  LineSums<kCode, FN> sums;
+  if constexpr (kForm == kGrad) sums.init(lane);
   // one k-tile of MFMAs, fenced off from the scheduler on both sides so that
   // no wait or memory instruction of a neighbouring phase moves into it
   auto compute = [&]() {
@@ -357,6 +362,12 @@ __global__ __launch_bounds__(512) void grouped_two_group_kernel(const GroupedPar
       static_for<KSTEPS * FM * FN>([&](auto idx) {
         constexpr int ks = idx / (FM * FN), i = (idx / FN) % FM, j = idx % FN;
         Atom::mma(acc[i][j], b[ks][j], a[ks][i]);
+      });
+    }
+    if constexpr (kForm == kGrad) {
+      static_for<KSTEPS>([&](auto ks) {
+        if (sum_b) static_for<FN>([&](auto j) { sums.template add<j>(b[ks][j]); });
+        if (sum_a) static_for<FM>([&](auto i) { sums.template add<i>(a[ks][i]); });
       });
     }
     __builtin_amdgcn_sched_barrier(0);
@@ -457,6 +468,10 @@ __global__ __launch_bounds__(512) void grouped_two_group_kernel(const GroupedPar
   // copy is in flight, so the slots are free for the epilogue: group 0
   // starts while group 1 still multiplies the last k-tile.
   uint8_t* region = smem + wave * (32 * FM) * (64 * FN);
+  if constexpr (kForm == kGrad) {
+    if (sum_b) sums.template write<FN>(p.dbias + (int64_t)e * p.N, n0 + wn0, p.N, lane);
+    if (sum_a) sums.template write<FM>(p.dbias + (int64_t)e * p.M, m0 + wm0, p.M, lane);
+  }
   if constexpr (kForm == kGrad)
     wgrad_epilogue<FM, FN>(p, e, m0 + wm0, n0 + wn0, lane, acc, region);
   else

@@ -41,6 +41,7 @@ struct GroupedParams {
 enum : int {
   kOpD16 = 1,    // D (and Z) rows are 16-byte aligned
   kOpVec4 = 2,   // sb and bias rows allow aligned 4-element vectors
+  kOpSumA = 4,   // gradient: dY is operand A (column-major D), else B
 };
 
 // Blocks of BM rows that `rows` rows in `groups` groups can need: every
@@ -77,10 +78,6 @@ int launch_wgrad_direct(const GroupedParams& p, int type, int shape, hipStream_t
 // The kernel for few rows an expert (grouped_few_rows.hip): B K-contiguous,
 // any pitch and alignment; blocks of 16 mt rows, mt 1, 2 or 4.
 int launch_grouped_few_rows(const GroupedParams& p, int type, int mt, hipStream_t stream);
-
-// dbias[e, n] = sum over e's rows of Y[r, n]
-int launch_group_colsum(const GroupedParams& p, const uint8_t* Y, int64_t ldy, int type, int N,
-                        hipStream_t stream);
 
 int launch_quantize_rows(int64_t M, int64_t K, const void* X, int type, int64_t ldx, int8_t* Q,
                          int64_t ldq, float* scale, hipStream_t stream);

@@ -281,19 +281,15 @@ int tla_grouped_gemm_wgrad(const tla_grouped_wgrad_args* a, void* stream) {
   if (!out16(a->type) || !aux_type(a->d_type)) return TLA_ERR_UNSUPPORTED;
   if (a->groups >= kLimit || a->rows >= kLimit || a->N >= kLimit || a->K >= kLimit)
     return TLA_ERR_UNSUPPORTED;
-  const bool has_d = a->K > 0 && a->N > 0, has_bias = a->dbias && a->N > 0;
-  if (a->groups == 0 || (!has_d && !has_bias)) return TLA_OK;
-  if (a->groups > 65535 && has_bias) return TLA_ERR_UNSUPPORTED;
+  if (a->groups == 0 || a->K == 0 || a->N == 0) return TLA_OK;
   if (!a->offsets && a->groups != 1) return TLA_ERR_INVALID_ARG;
   if (a->rows > 0 && (!a->Y || a->ldy < a->N)) return TLA_ERR_INVALID_ARG;
   const bool row = a->d_order == TLA_ROW_MAJOR;
-  if (has_d) {
-    const int64_t outer = row ? a->K : a->N, inner = row ? a->N : a->K;
-    if (!a->D || a->ldd < inner) return TLA_ERR_INVALID_ARG;
-    if (a->rows > 0 && (!a->A || a->lda < a->K)) return TLA_ERR_INVALID_ARG;
-    // the experts' matrices must not overlap
-    if (a->groups > 1 && a->stride_d < (outer - 1) * a->ldd + inner) return TLA_ERR_INVALID_ARG;
-  }
+  const int64_t outer = row ? a->K : a->N, inner = row ? a->N : a->K;
+  if (!a->D || a->ldd < inner) return TLA_ERR_INVALID_ARG;
+  if (a->rows > 0 && (!a->A || a->lda < a->K)) return TLA_ERR_INVALID_ARG;
+  // the experts' matrices must not overlap
+  if (a->groups > 1 && a->stride_d < (outer - 1) * a->ldd + inner) return TLA_ERR_INVALID_ARG;
   const int db = type_bytes(a->d_type);
   if (!aligned_to(a->offsets, 4) || !aligned_to(a->A, 2) || !aligned_to(a->Y, 2) ||
       !aligned_to(a->D, db) || !aligned_to(a->dbias, 4))
@@ -316,12 +312,7 @@ int tla_grouped_gemm_wgrad(const tla_grouped_wgrad_args* a, void* stream) {
   p.N = (int)(row ? a->N : a->K);
   const int per16 = 16 / db;
   if (a->ldd % per16 == 0 && a->stride_d % per16 == 0 && aligned_to(a->D, 16)) p.flags |= kOpD16;
-  if (has_bias) {
-    const int rc = launch_group_colsum(p, (const uint8_t*)a->Y, a->ldy, a->type, (int)a->N,
-                                       (hipStream_t)stream);
-    if (rc) return rc;
-  }
-  if (!has_d) return TLA_OK;
+  if (!row) p.flags |= kOpSumA;
   // the direct copies' layout (operators.hpp, launch_wgrad_two_group)
   const bool direct = rows16(a->A, a->lda, 2) && rows16(a->Y, a->ldy, 2) && a->K % 8 == 0 &&
                       a->N % 8 == 0 && a->rows * a->lda * 2 < kLimit && a->rows * a->ldy * 2 < kLimit;
