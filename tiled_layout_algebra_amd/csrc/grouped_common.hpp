@@ -145,7 +145,9 @@ __device__ __forceinline__ bool row_tile(const GroupedParams& p, int bid, RowTil
       expert_rows(p, t.e, lo, hi);
       t.r0 = __builtin_amdgcn_readfirstlane(lo + (tm - before - excl) * BM);
       t.r1 = __builtin_amdgcn_readfirstlane(hi);
-      return true;
+      lo = __builtin_amdgcn_readfirstlane(lo);
+      // (wrong offsets could have overflowed the sums)
+      return t.r0 >= lo && t.r0 < t.r1 && (unsigned)t.tn < (unsigned)p.tiles_n;
     }
     before += __builtin_amdgcn_readlane(incl, 63);
   }

@@ -36,8 +36,25 @@ namespace {
 
 enum Form : int { kNK = 0, kKN = 1, kGrad = 2, kNKShift = 3 };
 
-template <int kCode, int kForm>
-__global__ __launch_bounds__(512) void grouped_two_group_kernel(const GroupedParams p) {
+// LDS bytes of the workgroup
+constexpr int kTwoGroupLds = 5 * 256 * 128;
+
+// Where a workgroup's tile lies: rows m0 .. of the expert, which end at m_end;
+// columns n0 ..; the operands' bases, and the length of the sum.  Product: rows
+// of A and of D.  Gradient: the expert's rows are the K of both operands, m0
+// and n0 columns of them; sum_a / sum_b: this wave sums dY's lines.
+struct TileSpan {
+  int e, m0, m_end, n0, K;
+  const uint8_t *A, *B;
+  bool sum_a, sum_b;
+};
+
+// The tile program.  kHalf: 128 x 256 instead of 256 x 256, for blocks of at
+// most 128 rows: both groups share the rows and take half the columns each, so
+// every wave multiplies 64 x 64 (16 MFMAs a k-tile, not 32) and none idles.
+template <int kCode, int kForm, bool kHalf>
+__device__ __forceinline__ void two_group_tile(const GroupedParams& p, const TileSpan& ts,
+                                               uint8_t* smem) {
   constexpr bool kShift = kForm == kNKShift;
   using Atom = std::conditional_t<kShift && kCode == kE4M3, E4m3Bytes, OpAtom<kCode>>;
   using Frag = typename Atom::Frag;
@@ -48,56 +65,33 @@ __global__ __launch_bounds__(512) void grouped_two_group_kernel(const GroupedPar
   constexpr bool kBT = kForm == kKN || kForm == kGrad, kAT = kForm == kGrad;
   constexpr int kUsed = kShift ? 96 : kRowBytes;  // bytes of K in a k-tile
   constexpr int BK = kUsed / EB;                // K elements per k-tile
-  constexpr int BM = 256, BN = 256;
-  constexpr int WM = 64, WN = 128;              // wave tile
+  constexpr int BM = kHalf ? 128 : 256, BN = 256;
+  constexpr int WM = 64, WN = kHalf ? 64 : 128;  // wave tile
   constexpr int FM = WM / 32, FN = WN / 32;     // MFMA tiles per wave
   constexpr int KSTEPS = BK / Atom::kK;         // MFMA k-steps per k-tile
   constexpr int kSub = Atom::kLaneBytes / 16;   // 16-byte reads per fragment
   constexpr int kStepBytes = Atom::kK * EB;
-  constexpr int SLAB = BM * kRowBytes;          // 32 KiB: one operand, one k-tile
+  constexpr int SLAB = BN * kRowBytes;          // 32 KiB: one operand, one k-tile
   constexpr int B_BASE = 2 * SLAB;              // LDS: [A0 A1 | B0 B1 B2]
   constexpr int kCopies = SLAB / (256 * 16);    // 16-byte copies per thread per slab
+  constexpr int kCopiesA = BM * kRowBytes / (256 * 16);
   static_assert(BK % Atom::kK == 0 && kCopies == 8, "k-tile geometry");
   static_assert(!kShift || (kSub == 1 && kStepBytes == 32), "a dword follows every fragment");
   static_assert((1 << Slab<kRowBytes>::kRowShift) * kChunks <= 32,
                 "the swizzle repeats within 32 rows");
-  static_assert(5 * SLAB <= 160 * 1024, "LDS budget");
+  static_assert(5 * SLAB == kTwoGroupLds && 5 * SLAB <= 160 * 1024, "LDS budget");
+  static_assert(!kHalf || kForm != kGrad, "blocks of rows");
   static_assert(!kBT || EB == 2, "slabs of k rows: 16-bit operands");
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[5 * SLAB];
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int grp = wave >> 2;                    // 0: waves 0-3, 1: waves 4-7
   const int t = tid & 255;                      // thread index inside the group
-  // The tile: the operands' first rows and what is left of them from there.
-  // Product: rows m0 .. m_end - 1 of A are the expert's.  Gradient: the
-  // expert's rows are the K of both operands, m0 and n0 columns of them.
-  int e, m0, m_end, n0, K;
-  bool sum_a = false, sum_b = false;  // gradient: this wave sums dY's lines
-  const uint8_t *A = p.A, *B = p.B;
-  if constexpr (kForm == kGrad) {
-    int tm, tn, lo, hi;
-    wgrad_tile(p, blockIdx.x, gridDim.x, e, tm, tn);
-    expert_rows(p, e, lo, hi);
-    sum_a = p.dbias && (p.flags & kOpSumA) && tn == 0 && !((wave >> 1) & 1);
-    sum_b = p.dbias && !(p.flags & kOpSumA) && tm == 0 && grp == 0 && !(wave & 1);
-    m0 = tm * BM;
-    m_end = p.M;
-    n0 = tn * BN;
-    K = hi - lo;
-    A += (int64_t)lo * p.lda * EB;
-    B += (int64_t)lo * p.ldb * EB;
-  } else {
-    RowTile rt;
-    if (!row_tile<BM>(p, blockIdx.x, rt)) return;
-    e = rt.e;
-    m0 = rt.r0;
-    m_end = rt.r1;
-    n0 = rt.tn * BN;
-    K = p.K;
-    B += (int64_t)e * p.stride_b * EB;
-  }
-  const int wm0 = 128 * grp + WM * (wave & 1), wn0 = WN * ((wave >> 1) & 1);
+  const int e = ts.e, m0 = ts.m0, m_end = ts.m_end, n0 = ts.n0, K = ts.K;
+  const uint8_t *A = ts.A, *B = ts.B;
+  const bool sum_a = ts.sum_a, sum_b = ts.sum_b;
+  const int wm0 = kHalf ? WM * (wave & 1) : 128 * grp + WM * (wave & 1);
+  const int wn0 = WN * (kHalf ? 2 * grp + ((wave >> 1) & 1) : ((wave >> 1) & 1));
   const bool busy = kForm == kGrad || m0 + wm0 < m_end;  // a wave without a row multiplies nothing
   const int KT = (K + BK - 1) / BK;
   const int KTf = K / BK;  // whole k-tiles; tile KTf, if K ends inside it, is ragged
@@ -179,15 +173,18 @@ __global__ __launch_bounds__(512) void grouped_two_group_kernel(const GroupedPar
   // records: it writes zeros into a slot nobody reads any more.
   auto copy_one = [&](int kt, int slot, bool live, auto q) {
     const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
-        (void*)(qbase + (int64_t)q * q_stride), 0, recs[q] & -(int)live, 0x00020000);
+        (void*)(qbase + (int64_t)q * q_stride), 0,
+        __builtin_amdgcn_readfirstlane(recs[q] & -(int)live), 0x00020000);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(
         r, (__attribute__((address_space(3))) void*)(smem + lds_op + slot * SLAB + q * 4096 +
                                                      (wave & 3) * 1024),
         16, kt == KTf ? voff_tail : voff, (uint32_t)kt * kt_bytes + (uint32_t)q * q_bytes, 0, 0);
   };
-  auto copy_slab = [&](int kt, int slot, bool live) {
-    static_for<kCopies>([&](auto q) { copy_one(kt, slot, live, q); });
+  auto copy_slab = [&](int kt, int slot, bool live, auto n) {
+    static_for<n>([&](auto q) { copy_one(kt, slot, live, q); });
   };
+  using CopiesA = std::integral_constant<int, kCopiesA>;
+  using CopiesB = std::integral_constant<int, kCopies>;
 
   // ---- fragments: one base register per k-step; the A slot and the 32-row
   // fragment are immediates, the B slot (three of them: immediates would
@@ -301,6 +298,7 @@ __global__ __launch_bounds__(512) void grouped_two_group_kernel(const GroupedPar
   const bool ragged = kShift && KTf < KT;
   auto clear_tail = [&]() {
     const int kt = KT - 1, slot = grp == 0 ? (kt & 1) : kt % 3;
+    if (kHalf && grp == 0 && t >= BM) return;
     uint8_t* row = smem + lds_op + slot * SLAB + t * kRowBytes;
     const uint32_t sh = ((uint32_t)(uintptr_t)op + (uint32_t)t * (uint32_t)rb) & 3u;
     const int first = (int)sh + K * EB - KTf * kUsed;  // of the window's bytes, the first past K
@@ -324,7 +322,6 @@ __global__ __launch_bounds__(512) void grouped_two_group_kernel(const GroupedPar
   // copies after the reads (16-bit), 3728 against 3952 (reads first) and
   // 4276 (copies first) for e4m3.
   constexpr int kReads = KSTEPS * (FM + FN);  // fragments per k-tile
-  constexpr int kPer = kReads / kCopies, kRem = kReads % kCopies;
   // LDS read instructions of fragments [first, first + n)
   auto read_insts = [](int first, int n) constexpr {
     int c = 0;
@@ -332,15 +329,16 @@ __global__ __launch_bounds__(512) void grouped_two_group_kernel(const GroupedPar
       c += kShift ? 2 : (r % (FM + FN) < FM) ? (kAT ? 2 : kSub) : (kBT ? 2 : kSub);
     return c;
   };
-  auto memory_phase = [&](int kt, int ct, int slot, bool live) {
+  auto memory_phase = [&](int kt, int ct, int slot, bool live, auto copies) {
+    constexpr int kPer = kReads / copies, kRem = kReads % copies;
     __builtin_amdgcn_sched_barrier(0);
-    static_for<kCopies>([&](auto q) {
+    static_for<copies>([&](auto q) {
       copy_one(ct, slot, live, q);
       constexpr int first = kPer * q + (q < kRem ? q : kRem);
       constexpr int n = kPer + (q < kRem ? 1 : 0);
       static_for<n>([&](auto u) { read_frag(kt, std::integral_constant<int, first + u>{}); });
     });
-    static_for<kCopies>([&](auto q) {
+    static_for<copies>([&](auto q) {
       constexpr int first = kPer * q + (q < kRem ? q : kRem);
       constexpr int n = kPer + (q < kRem ? 1 : 0);
       __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
@@ -413,7 +411,7 @@ __global__ __launch_bounds__(512) void grouped_two_group_kernel(const GroupedPar
   // accumulator keeps them in front of it.
   if (KT > 0) {
     if (grp == 0) {
-      copy_slab(0, 0, true);
+      copy_slab(0, 0, true, CopiesA{});
       wait_vmcnt<0>();
       barrier();
       for (int kt = 0; kt < KT; ++kt) {
@@ -423,7 +421,7 @@ __global__ __launch_bounds__(512) void grouped_two_group_kernel(const GroupedPar
             barrier();
           }
         }
-        memory_phase(kt, kt + 1, (kt + 1) & 1, kt + 1 < KT);
+        memory_phase(kt, kt + 1, (kt + 1) & 1, kt + 1 < KT, CopiesA{});
         wait_lgkmcnt0();
         barrier();
         compute();
@@ -432,8 +430,8 @@ __global__ __launch_bounds__(512) void grouped_two_group_kernel(const GroupedPar
         barrier();
       }
     } else {
-      copy_slab(0, 0, true);
-      copy_slab(1, 1, KT > 1);
+      copy_slab(0, 0, true, CopiesB{});
+      copy_slab(1, 1, KT > 1, CopiesB{});
       wait_vmcnt<kCopies>();
       barrier();
       if constexpr (kShift) {
@@ -446,7 +444,7 @@ __global__ __launch_bounds__(512) void grouped_two_group_kernel(const GroupedPar
       // one iteration reads k-tile kt (end of period kt) and multiplies it
       // (start of period kt+1): the fragments never live across iterations
       for (int kt = 0; kt < KT; ++kt) {
-        memory_phase(kt, kt + 2, (kt + 2) % 3, kt + 2 < KT);
+        memory_phase(kt, kt + 2, (kt + 2) % 3, kt + 2 < KT, CopiesB{});
         wait_lgkmcnt0();
         wait_vmcnt<kCopies>();                       // B of kt+1 landed
         barrier();
@@ -478,13 +476,145 @@ __global__ __launch_bounds__(512) void grouped_two_group_kernel(const GroupedPar
     grouped_epilogue<kCode, FM, FN>(p, e, m_end, m0 + wm0, n0 + wn0, lane, acc, region);
 }
 
+// Which blocks of rows a workgroup may get.  Experts are cut into blocks of
+// 256 rows and, where at most 128 are left, a half block.  The whole tiles come
+// first; when the last round of them would not fill the card's compute units,
+// they are split into halves if the halves then end sooner (a half tile takes
+// about 0.55 of a whole one's time).  p.flags & kOpHalves: half blocks only.
+// As in row_tile, a segment's tiles go to the XCDs in contiguous runs, four
+// blocks of rows at a time.
+struct HalfTile {
+  int e, r0, r1, tn;
+  bool half;
+};
+__device__ __forceinline__ bool two_group_lookup(const GroupedParams& p, int bid, HalfTile& t) {
+  constexpr int kUnits = 256;  // compute units of the card, one workgroup on each
+  const int lane = threadIdx.x & 63;
+  const bool halves = p.flags & kOpHalves;
+  auto count = [&](int e, int& full, int& half) {
+    full = half = 0;
+    if (e >= p.groups) return;
+    int lo, hi;
+    expert_rows(p, e, lo, hi);
+    const int rows = hi - lo, rest = rows & 255;
+    full = halves ? 0 : (rows >> 8) + (rest > 128);
+    half = halves ? (rows >> 7) + ((rows & 127) > 0) : rest > 0 && rest <= 128;
+  };
+  int tf = 0, th = 0, fi = 0, hi_ = 0, f, h;
+  for (int g0 = 0; g0 < p.groups; g0 += 64) {
+    count(g0 + lane, f, h);
+    fi = wave_scan(f, lane);
+    hi_ = wave_scan(h, lane);
+    tf += __builtin_amdgcn_readlane(fi, 63);
+    th += __builtin_amdgcn_readlane(hi_, 63);
+  }
+  const int64_t n_full = (int64_t)tf * p.tiles_n, n_half = (int64_t)th * p.tiles_n;
+  const int over = (int)(n_full % kUnits);
+  int split = 0;
+  if (over) {
+    auto half_rounds = [](int64_t n) { return 0.55f * (float)((n + kUnits - 1) / kUnits); };
+    const int64_t room = kUnits - over;
+    const float whole = 1.f + half_rounds(n_half > room ? n_half - room : 0);
+    if (half_rounds(2 * over + n_half) < whole) split = over;
+  }
+  const int64_t whole_tiles = n_full - split, half_tiles = 2 * (int64_t)split + n_half;
+  const bool in_full = bid < whole_tiles;
+  if (!in_full && bid - whole_tiles >= half_tiles) return false;
+  const int n = (int)(in_full ? whole_tiles : half_tiles);
+  const int at = (int)(in_full ? bid : bid - whole_tiles);
+  const int per = n / 8, rest = n % 8, xcd = at & 7;
+  int id = xcd * per + min(xcd, rest) + (at >> 3);
+  int part = 0;
+  bool of_full = in_full;
+  if (!in_full) {
+    if (id < 2 * split) {
+      of_full = true;
+      part = id & 1;
+      id = (int)whole_tiles + (id >> 1);
+    } else {
+      id -= 2 * split;
+    }
+  }
+  const int total = of_full ? tf : th;
+  const int per_group = 4 * p.tiles_n, first = (id / per_group) * 4;
+  const int gm = min(total - first, 4), in = id % per_group;
+  const int block = first + in % gm;
+  t.tn = in / gm;
+  t.half = !in_full;
+  int before = 0;
+  for (int g0 = 0; g0 < p.groups; g0 += 64) {
+    if (p.groups > 64) {
+      count(g0 + lane, f, h);
+      fi = wave_scan(f, lane);
+      hi_ = wave_scan(h, lane);
+    }
+    const int incl = of_full ? fi : hi_;
+    const uint64_t mask = __ballot(block < before + incl);
+    if (mask) {
+      const int l = __builtin_ctzll(mask);
+      const int excl = l ? __builtin_amdgcn_readlane(incl, l - 1) : 0;
+      t.e = g0 + l;
+      int lo, hi, ef, eh;
+      expert_rows(p, t.e, lo, hi);
+      count(t.e, ef, eh);
+      const int local = block - before - excl;
+      const int r0 = of_full ? lo + local * 256 + part * 128 : lo + ef * 256 + local * 128;
+      t.r0 = __builtin_amdgcn_readfirstlane(r0);
+      t.r1 = __builtin_amdgcn_readfirstlane(hi);
+      lo = __builtin_amdgcn_readfirstlane(lo);
+      // (wrong offsets could have overflowed the sums)
+      return t.r0 >= lo && t.r0 < t.r1 && (unsigned)t.tn < (unsigned)p.tiles_n;
+    }
+    before += __builtin_amdgcn_readlane(incl, 63);
+  }
+  return false;
+}
+
+template <int kCode, int kForm>
+__global__ __launch_bounds__(512) void grouped_two_group_kernel(const GroupedParams p) {
+  constexpr int EB = type_bytes(kCode);
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[kTwoGroupLds];
+  TileSpan ts{};
+  if constexpr (kForm == kGrad) {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), grp = wave >> 2;
+    int tm, tn, lo, hi;
+    wgrad_tile(p, blockIdx.x, gridDim.x, ts.e, tm, tn);
+    expert_rows(p, ts.e, lo, hi);
+    ts.sum_a = p.dbias && (p.flags & kOpSumA) && tn == 0 && !((wave >> 1) & 1);
+    ts.sum_b = p.dbias && !(p.flags & kOpSumA) && tm == 0 && grp == 0 && !(wave & 1);
+    ts.m0 = tm * 256;
+    ts.m_end = p.M;
+    ts.n0 = tn * 256;
+    ts.K = hi - lo;
+    ts.A = p.A + (int64_t)lo * p.lda * EB;
+    ts.B = p.B + (int64_t)lo * p.ldb * EB;
+    two_group_tile<kCode, kForm, false>(p, ts, smem);
+  } else {
+    HalfTile t;
+    if (!two_group_lookup(p, blockIdx.x, t)) return;
+    // scalars for certain: copies whose buffer lies in vector registers loop
+    ts.e = __builtin_amdgcn_readfirstlane(t.e);
+    ts.m0 = __builtin_amdgcn_readfirstlane(t.r0);
+    ts.m_end = __builtin_amdgcn_readfirstlane(t.r1);
+    ts.n0 = __builtin_amdgcn_readfirstlane(t.tn) * 256;
+    ts.K = p.K;
+    ts.A = p.A;
+    ts.B = p.B + (int64_t)ts.e * p.stride_b * EB;
+    if (t.half) two_group_tile<kCode, kForm, true>(p, ts, smem);
+    else two_group_tile<kCode, kForm, false>(p, ts, smem);
+  }
+}
+
 template <int kCode, int kForm>
 int launch(const GroupedParams& p0, hipStream_t stream) {
   GroupedParams p = p0;
   p.tiles_n = (p.N + 255) / 256;
   p.tiles_m = (p.M + 255) / 256;
-  const int64_t grid = kForm == kGrad ? (int64_t)p.groups * p.tiles_m * p.tiles_n
-                                      : row_tiles_bound(p.rows, p.groups, 256) * p.tiles_n;
+  // a split round adds fewer than 256 tiles
+  const int64_t grid =
+      kForm == kGrad ? (int64_t)p.groups * p.tiles_m * p.tiles_n
+      : p.flags & kOpHalves ? row_tiles_bound(p.rows, p.groups, 128) * p.tiles_n
+                            : row_tiles_bound(p.rows, p.groups, 256) * p.tiles_n + 256;
   if (grid <= 0) return TLA_OK;
   if (grid > 0x7FFFFFFF) return TLA_ERR_UNSUPPORTED;
   hipLaunchKernelGGL((grouped_two_group_kernel<kCode, kForm>), dim3((unsigned)grid), dim3(512), 0,

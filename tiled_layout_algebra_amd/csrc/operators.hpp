@@ -42,6 +42,7 @@ enum : int {
   kOpD16 = 1,    // D (and Z) rows are 16-byte aligned
   kOpVec4 = 2,   // sb and bias rows allow aligned 4-element vectors
   kOpSumA = 4,   // gradient: dY is operand A (column-major D), else B
+  kOpHalves = 8, // two-group product: blocks of 128 rows throughout
 };
 
 // Blocks of BM rows that `rows` rows in `groups` groups can need: every

@@ -68,6 +68,17 @@ double row_blocks(const tla_grouped_gemm_args* a, double bm) {
   return live * (blocks > 1.0 ? blocks : 1.0);
 }
 
+// Rounds of 256 x 256 tiles (1.6 us a k-tile) the two-group kernel takes, its
+// last one in half tiles (0.9) where that is shorter, or half tiles throughout.
+double two_group_rounds(const tla_grouped_gemm_args* a, bool halves) {
+  const double tiles_n = (double)((a->N + 255) / 256);
+  auto up = [](double x) { return (double)(int64_t)((x + 255.0) / 256.0); };
+  if (halves) return 0.56 * up(row_blocks(a, 128) * tiles_n);
+  const double tiles = row_blocks(a, 256) * tiles_n, whole = (double)(int64_t)(tiles / 256.0);
+  const double last = 0.56 * up(2.0 * (tiles - 256.0 * whole));
+  return whole + (last < 1.0 ? last : 1.0);
+}
+
 // The kernel with the smallest estimated time (us).  No kernel reads the
 // weights faster than 5.0 TB/s.  Measured with [N, K] weights of 4096 x 4096
 // int8 (32 k-tiles of 128 bytes), one expert, M rows:
@@ -106,18 +117,20 @@ Kernel choose(const tla_grouped_gemm_args* a, int eb, bool b_kc) {
   consider(kFewRows1, 4.0 + row_blocks(a, 16) * matrix / 5.0);
   consider(kFewRows2, 4.3 + row_blocks(a, 32) * matrix / 3.3);
   consider(kFewRows4, 5.0 + row_blocks(a, 64) * matrix / 2.2);
-  const double t64 = tiles(64, 128), t128 = tiles(128, 128), t256 = tiles(256, 256);
+  const double t64 = tiles(64, 128), t128 = tiles(128, 128);
   auto at_least = [](double least, double us) { return us > least ? us : least; };
   consider(kDirect64, 4.2 + kt * at_least(0.3, (eb == 1 ? 0.0015 : 0.0019) * t64));
   consider(kDirect128, 4.5 + kt * (t128 <= 128.0 ? 0.4 : t128 <= 256.0 ? 0.54 : 0.62 * rounds(t128)));
-  consider(kTwoGroup, at_least(4.0 + 1.2 * weights, 5.0 + kt * (t256 <= 64.0 ? 1.0 : t256 <= 128.0 ? 1.25 : 1.6 * rounds(t256))));
+  const double mixed = two_group_rounds(a, false), halved = two_group_rounds(a, true);
+  const double two = mixed < halved ? mixed : halved;
+  consider(kTwoGroup, at_least(4.0 + 1.2 * weights, 5.0 + kt * 1.6 * two));
   // any alignment: with B 4096 x 4095 int8, 3001 rows: 121 us (64 rows), 99
   // (128), 68 (256), 115 (general); with 988 x 2371, 400 rows 18, 23, 40, 33;
   // bf16, 4096 rows on 32 experts of 2048 x 4095: 305, 247, 285, 269
   const double kt96 = (double)(a->K * eb / 96 + 1);
   consider(kDirect64Shift, 4.5 + kt * at_least(0.6, (eb == 1 ? 0.0024 : 0.0032) * t64));
   consider(kDirect128Shift, 4.8 + kt * 0.96 * rounds(t128));
-  consider(kTwoGroupShift, 6.0 + kt96 * (t256 <= 128.0 ? 1.3 : 1.6 * rounds(t256)));
+  consider(kTwoGroupShift, 6.0 + kt96 * 1.6 * two);
   consider(kGeneral, 4.5 + kt * at_least(1.5, 2.05 * rounds(t128 / 2.0)));
   return best;
 }
@@ -198,7 +211,8 @@ int run_product(const tla_grouped_gemm_args* a, hipStream_t stream, int forced =
     if (!takes((Kernel)forced, a, type_bytes(a->type), plan.b_kc)) return TLA_ERR_UNSUPPORTED;
     plan.kernel = (Kernel)forced;
   }
-  const GroupedParams& p = plan.p;
+  GroupedParams& p = plan.p;
+  if (two_group_rounds(a, true) < two_group_rounds(a, false)) p.flags |= kOpHalves;
   const int t = plan.type;
   switch (plan.kernel) {
     case kNoop: return TLA_OK;
