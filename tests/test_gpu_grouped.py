@@ -307,10 +307,11 @@ def _takes(variant, kind, order, N, K, pad, shift):
     if variant >= 7:
         return nk
     ldb = (K if nk else N) + pad
-    aligned = all(x * eb % 16 == 0 for x in (K, K + pad, ldb, shift, pad))
+    stride_b = (N if nk else K) * ldb + pad
+    aligned = all(x * eb % 4 == 0 for x in (K + pad, ldb, shift, stride_b))
     if variant == 3 and not nk:
         return False
-    return aligned and (nk or (eb == 2 and N % 8 == 0))
+    return aligned and (nk or eb == 2)
 
 
 @pytest.mark.parametrize("variant", range(tla.GROUPED_VARIANTS))
@@ -318,7 +319,8 @@ def _takes(variant, kind, order, N, K, pad, shift):
 @pytest.mark.parametrize("order", [tla.COL_MAJOR, tla.ROW_MAJOR], ids=["nk", "kn"])
 @pytest.mark.parametrize("N,K,pad,shift", [
     (40, 16, 0, 0), (300, 96, 0, 0), (264, 576, 0, 0), (136, 1040, 16, 16), (7, 47, 0, 0),
-    (300, 97, 1, 1), (129, 511, 2, 3), (280, 1055, 3, 0), (257, 600, 5, 2)], ids=str)
+    (300, 97, 1, 1), (129, 511, 2, 3), (280, 1055, 3, 0), (257, 600, 5, 2), (300, 98, 0, 0),
+    (130, 525, 3, 4), (18, 1043, 1, 0)], ids=str)
 def test_every_kernel(variant, kind, order, N, K, pad, shift):
     """Each kernel on tiles it fills and tiles it does not, K from less than a
     step to several k-tiles, and at any byte address where it takes that: the

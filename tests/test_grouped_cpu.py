@@ -110,8 +110,8 @@ def test_run_variant_refusals():
     wide = dict(lda=1 << 22, ldb=1 << 22)  # rows 8 MiB apart
     e4m3 = dict(type=tla.E4M3)
     for v, bad in ((1, [odd, wide, e4m3, dict(K=0), dict(A=FAKE + 2), dict(stride_b=4097)]),
-                   (2, [odd, dict(kn, N=63), dict(kn, type=tla.I8)]), (3, [kn, odd, dict(B=FAKE + 8)]),
-                   (4, [kn, dict(K=0)]), (5, [kn]), (6, [kn]), (7, [kn, wide, e4m3, dict(K=0)])):
+                   (2, [odd, dict(kn, ldb=65), dict(kn, type=tla.I8)]), (3, [kn, odd, dict(B=FAKE + 2)]),
+                   (4, [kn, dict(K=0)]), (5, [kn]), (6, [kn]), (7, [kn, wide, e4m3, dict(K=0)]), (8, [kn, wide]), (9, [kn, e4m3])):
         for kw in bad:
             assert f(ctypes.byref(_product(**kw)), v, None) == tla.ERR_UNSUPPORTED, (v, kw)
 
@@ -194,6 +194,16 @@ def test_wgrad_refusals(kw, status):
 ])
 def test_quantizer_refusals(args, status):
     assert tla.lib().tla_quantize_rows(*args, None) == status
+
+
+def test_packed_arguments_match_the_structures():
+    for fmt, cls in ((tla._PACK_GROUPED, tla.GroupedGemmArgs), (tla._PACK_WGRAD, tla.GroupedWgradArgs),
+                     (tla._PACK_I8, tla.GemmI8Args)):
+        assert fmt.size <= ctypes.sizeof(cls) < fmt.size + 8  # less the padding at the end
+        vals = [0x101 * (i + 1) for i in range(len(cls._fields_))]
+        raw = fmt.pack(*vals).ljust(ctypes.sizeof(cls), b"\0")
+        a = cls.from_buffer_copy(raw)
+        assert [getattr(a, name) for name, _ in cls._fields_] == vals
 
 
 def test_binding_refuses_host_tensors_and_other_index_types():

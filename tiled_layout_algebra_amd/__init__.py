@@ -12,6 +12,7 @@ raises on first use.  Build it with ``python -m tiled_layout_algebra_amd.build``
 """
 import ctypes
 import os
+import struct
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libtla.so")
@@ -321,23 +322,55 @@ class GemmI8Args(ctypes.Structure):
 
 GROUPED_VARIANTS = 10
 
+# The argument structures above as packing formats: filling one in this way
+# takes a quarter of a ctypes structure's time, which counts in calls of a few
+# microseconds.
+_PACK_GROUPED = struct.Struct("4qPPiqPiqqPiqPPPiPqii")
+_PACK_WGRAD = struct.Struct("4qPPqPqiPiiqqP")
+_PACK_I8 = struct.Struct("3qPqPiqPiqPPPii")
+_packed = {}
 
-def _dev32(t, kind, what):
-    """_dev for a buffer whose element type the library fixes ("int32" or
-    "float32"): another dtype would be misread, so it is refused."""
-    if t is not None and str(t.dtype) != "torch." + kind:
-        raise ValueError("%s must be a %s tensor" % (what, kind))
-    return _dev(t, what)
+
+def _packed_call(name, args, stream, *more):
+    """Calls tla_<name>(&args, *more, stream) with packed arguments."""
+    f = _packed.get(name)
+    if f is None:
+        types = [ctypes.c_char_p] + [ctypes.c_int32] * len(more) + [ctypes.c_void_p]
+        f = _packed[name] = ctypes.CFUNCTYPE(ctypes.c_int, *types)((name, lib()))
+    rc = f(args, *more, stream)
+    if rc != OK:
+        raise TlaError(rc, name)
+
+
+_torch_types = {}
+
+
+def _ptr(t, what, kind=None):
+    """Device address of a CUDA tensor, 0 for None; kind ("int32", "float32"):
+    the element type the library fixes for this buffer, so that another one is
+    refused, not misread."""
+    if t is None:
+        return 0
+    if kind is not None:
+        want = _torch_types.get(kind)
+        if want is None:
+            import torch
+            want = _torch_types[kind] = getattr(torch, kind)
+        if t.dtype is not want:
+            raise ValueError("%s must be a %s tensor" % (what, kind))
+    if not getattr(t, "is_cuda", False):
+        raise ValueError("%s must be a CUDA tensor" % what)
+    return t.data_ptr()
 
 
 def _grouped_gemm_args(groups, rows, N, K, offsets, A, type, lda, B, b_order, ldb, stride_b, D,
                        d_type, ldd, scale_a=None, scale_b=None, bias=None, bias_type=None, Z=None,
                        ldz=0, z_mode=Z_NONE, act=ACT_NONE):
-    return GroupedGemmArgs(
-        groups, rows, N, K, _dev32(offsets, "int32", "offsets"), _dev(A, "A"), type, lda,
-        _dev(B, "B"), b_order, ldb, stride_b, _dev(D, "D"), d_type, ldd,
-        _dev32(scale_a, "float32", "scale_a"), _dev32(scale_b, "float32", "scale_b"),
-        _dev(bias, "bias"), d_type if bias_type is None else bias_type, _dev(Z, "Z"), ldz, z_mode,
+    return _PACK_GROUPED.pack(
+        groups, rows, N, K, _ptr(offsets, "offsets", "int32"), _ptr(A, "A"), type, lda,
+        _ptr(B, "B"), b_order, ldb, stride_b, _ptr(D, "D"), d_type, ldd,
+        _ptr(scale_a, "scale_a", "float32"), _ptr(scale_b, "scale_b", "float32"),
+        _ptr(bias, "bias"), d_type if bias_type is None else bias_type, _ptr(Z, "Z"), ldz, z_mode,
         act)
 
 
@@ -353,16 +386,15 @@ def grouped_gemm(groups, rows, N, K, offsets, A, type, lda, B, b_order, ldb, str
                            d_type, ldd, scale_a, scale_b, bias, bias_type, Z, ldz, z_mode, act)
     s = _stream(stream, A, B, D)
     if variant is None:
-        _check(lib().tla_grouped_gemm(ctypes.byref(a), s), "tla_grouped_gemm")
+        _packed_call("tla_grouped_gemm", a, s)
     else:
-        _check(lib().tla_grouped_gemm_run_variant(ctypes.byref(a), variant, s),
-               "tla_grouped_gemm_run_variant")
+        _packed_call("tla_grouped_gemm_run_variant", a, s, variant)
 
 
 def grouped_gemm_variant(*args, **kw) -> str:
     """Name of the kernel grouped_gemm would launch (host only)."""
     kw.pop("stream", None)
-    a = _grouped_gemm_args(*args, **kw)
+    a = GroupedGemmArgs.from_buffer_copy(_grouped_gemm_args(*args, **kw))
     buf = ctypes.create_string_buffer(64)
     _check(lib().tla_grouped_gemm_variant(ctypes.byref(a), buf, 64), "tla_grouped_gemm_variant")
     return buf.value.decode()
@@ -372,29 +404,28 @@ def grouped_gemm_wgrad(groups, rows, N, K, offsets, A, lda, Y, ldy, type, D, d_t
                        stride_d, dbias=None, stream=None):
     """D_e = A_e^T Y_e and dbias_e = the column sums of Y_e for every expert
     (tla_grouped_gemm_wgrad)."""
-    a = GroupedWgradArgs(groups, rows, N, K, _dev32(offsets, "int32", "offsets"), _dev(A, "A"),
-                         lda, _dev(Y, "Y"), ldy, type, _dev(D, "D"), d_type, d_order, ldd,
-                         stride_d, _dev32(dbias, "float32", "dbias"))
-    _check(lib().tla_grouped_gemm_wgrad(ctypes.byref(a), _stream(stream, A, Y, D)),
-           "tla_grouped_gemm_wgrad")
+    a = _PACK_WGRAD.pack(groups, rows, N, K, _ptr(offsets, "offsets", "int32"), _ptr(A, "A"), lda,
+                         _ptr(Y, "Y"), ldy, type, _ptr(D, "D"), d_type, d_order, ldd, stride_d,
+                         _ptr(dbias, "dbias", "float32"))
+    _packed_call("tla_grouped_gemm_wgrad", a, _stream(stream, A, Y, D))
 
 
 def gemm_i8(M, N, K, A, lda, B, b_order, ldb, D, d_type, ldd, scale_a=None, scale_b=None,
             bias=None, bias_type=None, act=ACT_NONE, stream=None):
     """D = act(scale_a[m] scale_b[n] A.B + bias[n]) with int8 A and B and exact
     integer sums (tla_gemm_i8)."""
-    a = GemmI8Args(M, N, K, _dev(A, "A"), lda, _dev(B, "B"), b_order, ldb, _dev(D, "D"), d_type,
-                   ldd, _dev32(scale_a, "float32", "scale_a"),
-                   _dev32(scale_b, "float32", "scale_b"), _dev(bias, "bias"),
-                   d_type if bias_type is None else bias_type, act)
-    _check(lib().tla_gemm_i8(ctypes.byref(a), _stream(stream, A, B, D)), "tla_gemm_i8")
+    a = _PACK_I8.pack(M, N, K, _ptr(A, "A"), lda, _ptr(B, "B"), b_order, ldb, _ptr(D, "D"), d_type,
+                      ldd, _ptr(scale_a, "scale_a", "float32"), _ptr(scale_b, "scale_b", "float32"),
+                      _ptr(bias, "bias"), d_type if bias_type is None else bias_type, act)
+    _packed_call("tla_gemm_i8", a, _stream(stream, A, B, D))
 
 
 def quantize_rows(M, K, X, x_type, ldx, Q, ldq, scale, stream=None):
     """int8 codes Q and a scale for each row of X (tla_quantize_rows)."""
-    _check(lib().tla_quantize_rows(M, K, _dev(X, "X"), x_type, ldx, _dev(Q, "Q"), ldq,
-                                   _dev32(scale, "float32", "scale"), _stream(stream, X, Q, scale)),
-           "tla_quantize_rows")
+    rc = lib().tla_quantize_rows(M, K, _ptr(X, "X"), x_type, ldx, _ptr(Q, "Q"), ldq,
+                                 _ptr(scale, "scale", "float32"), _stream(stream, X, Q, scale))
+    if rc != OK:
+        raise TlaError(rc, "tla_quantize_rows")
 
 
 # -------------------------------------------------------------- transpose

@@ -112,20 +112,26 @@ __global__ __launch_bounds__(64 * kWM * kWN) void grouped_direct_kernel(const Gr
 
   // kShift: rows begin at any byte.  Copies start at each row's dword, so its
   // bytes land `row_shift` late and the window's last ones in a dword of its
-  // own (tail), a row a lane; records end with the tile's last row's last dword.
+  // own (tail), a row a lane.
   const uint32_t a_rb = (uint32_t)(p.lda * EB), b_rb = (uint32_t)(p.ldb * EB);
-  const uint32_t a_off = (uint32_t)(uintptr_t)A & 3u, b_off = (uint32_t)(uintptr_t)B & 3u;
+  const uint32_t a_off = kShift ? (uint32_t)(uintptr_t)A & 3u : 0u;
+  const uint32_t b_off = kShift ? (uint32_t)(uintptr_t)B & 3u : 0u;
   auto row_shift = [&](bool is_a, int r) {
     return ((is_a ? a_off : b_off) + (uint32_t)r * (is_a ? a_rb : b_rb)) & 3u;
   };
   const int a_last = m_end - 1 - m0, b_last = p.N - 1 - n0;
-  int a_bytes = 0x7FFFFFFF, b_bytes = 0x7FFFFFFF;
   if constexpr (kShift) {
     A -= a_off;
     B -= b_off;
-    a_bytes = (int)((min(a_last, BM - 1) * a_rb + K * EB + a_off + 3) & ~3u);
-    b_bytes = (int)((min(b_last, BN - 1) * b_rb + K * EB + b_off + 3) & ~3u);
   }
+  // each operand's bytes from its base up to the last dword that it needs
+  auto k_rows_bytes = [&](int64_t ld, int lines) {
+    return K > 0 ? (int)min((((K - 1) * ld + lines) * EB + 3) & ~(int64_t)3, (int64_t)0x7FFFFFFC) : 0;
+  };
+  const int a_bytes = kAT ? k_rows_bytes(p.lda, p.M)
+                          : (int)((min(a_last, BM - 1) * a_rb + K * EB + a_off + 3) & ~3u);
+  const int b_bytes = kBT ? k_rows_bytes(p.ldb, p.N)
+                          : (int)((min(b_last, BN - 1) * b_rb + K * EB + b_off + 3) & ~3u);
   // Copy q (A for q < IA, else B): slab row r = tid/kChunks + (NT/kChunks)*q',
   // landing at slab slot wave*64 + NT*q' (lane-linear); the lane fetches the
   // global chunk the swizzle assigns to that slot, from row r clamped to the
@@ -143,16 +149,17 @@ __global__ __launch_bounds__(64 * kWM * kWN) void grouped_direct_kernel(const Gr
                              : 0x80000000u;
     } else if constexpr (kA && kAT) {
       // as for an N-contiguous B: k row r, stored chunk pc holding columns
-      // m0 + 8 (pc ^ 4 (r % 4)) .. + 7, clamped to the last chunk of M
+      // m0 + 8 (pc ^ 4 (r % 4)) .. + 7, clamped to M's last chunk (whose
+      // columns past M feed nothing that is stored)
       const int sc = tid + NT * qq, r = sc / kChAT, pc = sc % kChAT;
-      const int m = min(m0 + 8 * (pc ^ (4 * (r & 3))), p.M - 8);
+      const int m = min(m0 + 8 * (pc ^ (4 * (r & 3))), (p.M - 1) & ~7);
       off[q] = (uint32_t)(((int64_t)r * p.lda + m) * EB);
     } else if constexpr (!kA && kBT) {
       // slab chunk tid + NT q': k row r, stored chunk pc, which holds logical
-      // chunk pc ^ 4 (r % 4): columns n0 + 8 lc .. + 7, clamped to the last
-      // whole chunk of the matrix (columns past N are never stored)
+      // chunk pc ^ 4 (r % 4): columns n0 + 8 lc .. + 7, clamped to the
+      // matrix' last chunk (columns past N are never stored)
       const int sc = tid + NT * qq, r = sc / kChBT, pc = sc % kChBT;
-      const int n = min(n0 + 8 * (pc ^ (4 * (r & 3))), p.N - 8);
+      const int n = min(n0 + 8 * (pc ^ (4 * (r & 3))), (p.N - 1) & ~7);
       off[q] = (uint32_t)(((int64_t)r * p.ldb + n) * EB);
     } else {
       const int r = tid / kChunks + (NT / kChunks) * qq;
@@ -164,9 +171,9 @@ __global__ __launch_bounds__(64 * kWM * kWN) void grouped_direct_kernel(const Gr
                  Swz::chunk(r, tid % kChunks) * 16;
     }
   });
-  // The ragged last k-tile (K a multiple of the 16-byte chunk): bit q is set
-  // when copy q's K-contiguous chunk lies past K -- that copy then reads from
-  // past every record and the range check returns zeros.  An N-contiguous B
+  // The ragged last k-tile: bit q is set when copy q's K-contiguous chunk lies
+  // past K -- that copy then reads from past every record and the range check
+  // returns zeros (the chunk that crosses K: clear_tail).  An N-contiguous B
   // slab's rows past K lie past its record count (K rows).
   uint32_t tail_past = 0;
   static_for<kShift ? 0 : kLoads>([&](auto q) {
@@ -177,8 +184,6 @@ __global__ __launch_bounds__(64 * kWM * kWN) void grouped_direct_kernel(const Gr
       if (Swz::chunk(r, tid % kChunks) * 16 >= (K - KTf * BK) * EB) tail_past |= 1u << q;
     }
   });
-  const int b_records = kBT ? (int)min((int64_t)K * p.ldb * EB, (int64_t)0x7FFFFFFF) : 0;
-  const int a_records = kAT ? (int)min((int64_t)K * p.lda * EB, (int64_t)0x7FFFFFFF) : 0;
   // Fragment bases for each k-step (and each 16-byte half of a 32-byte
   // fragment): row wm0 + lane%32 of the A slot, wn0 + lane%32 of the B slot.
   uint32_t fa[KSTEPS][kSub], fb[KSTEPS][kSub];
@@ -301,17 +306,20 @@ __global__ __launch_bounds__(64 * kWM * kWN) void grouped_direct_kernel(const Gr
       static_for<FN>([&](auto j) { shift(b[buf][j], xb[buf][j], sh_b); });
     }
   };
-  // kShift: clears what a ragged last k-tile in slot S holds past K (the next
-  // row's bytes), a thread a row, between its landing and its first reader
+  // Clears what a last k-tile that ends inside a chunk holds past K (the next
+  // row's bytes) in slot S, a thread a row, between its landing and its first
+  // reader
   auto clear_tail = [&](int kt, auto S) {
-    if constexpr (kShift) {
-      if (kt != KTf) return;
-      if (tid < BM + BN) {
+    if constexpr (kForm != kGrad) {
+      if (kt != KTf || !(kShift || K * EB % 16 != 0)) return;
+      if (tid < (kBT ? BM : BM + BN)) {
         const bool is_a = tid < BM;
         const int r = is_a ? tid : tid - BM;
         uint8_t* row = smem + (is_a ? S * SLAB_A : B_BASE + S * SLAB_B) + r * kRowBytes;
-        const int first = (int)row_shift(is_a, min(r, is_a ? a_last : b_last)) + (K - KTf * BK) * EB;
-        for (int d = first >> 2; d < 33; ++d) {
+        const int first = (kShift ? (int)row_shift(is_a, min(r, is_a ? a_last : b_last)) : 0) +
+                          (K - KTf * BK) * EB;
+        const int end = kShift ? 33 : (first + 15) / 16 * 4;
+        for (int d = first >> 2; d < end; ++d) {
           uint32_t* w = d < 32 ? (uint32_t*)(row + Swz::chunk(r, d >> 2) * 16 + (d & 3) * 4)
                                : (uint32_t*)(smem + TAIL_BASE + S * kTail + 4 * tid);
           *w = d == first >> 2 ? *w & ((1u << (8 * (first & 3))) - 1u) : 0u;
@@ -335,12 +343,12 @@ __global__ __launch_bounds__(64 * kWM * kWN) void grouped_direct_kernel(const Gr
                is_a ? a_bytes : b_bytes);
     } else if constexpr (q < IA && kAT)
       dma16_buf(A, off[q], (uint32_t)(tt * BK) * (uint32_t)(p.lda * EB),
-                smem + slot * SLAB_A + (wave * 64 + NT * q) * 16, a_records);
+                smem + slot * SLAB_A + (wave * 64 + NT * q) * 16, a_bytes);
     else if constexpr (q < IA)
       dma16_buf(A, o, kb, smem + slot * SLAB_A + (wave * 64 + NT * q) * 16, a_bytes);
     else if constexpr (kBT)
       dma16_buf(B, off[q], (uint32_t)(tt * BK) * (uint32_t)(p.ldb * EB),
-                smem + B_BASE + slot * SLAB_B + (wave * 64 + NT * (q - IA)) * 16, b_records);
+                smem + B_BASE + slot * SLAB_B + (wave * 64 + NT * (q - IA)) * 16, b_bytes);
     else
       dma16_buf(B, o, kb, smem + B_BASE + slot * SLAB_B + (wave * 64 + NT * (q - IA)) * 16,
                 b_bytes);

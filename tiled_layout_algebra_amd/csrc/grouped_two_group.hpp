@@ -108,24 +108,26 @@ __device__ __forceinline__ void two_group_tile(const GroupedParams& p, const Til
   uint32_t voff = (uint32_t)(r0 * rb + Swz::chunk(r0, t % kChunks) * 16);
   const int lds_op = grp == 0 ? 0 : B_BASE;
   int recs[kCopies];
+  const uint32_t off = kShift ? (uint32_t)(uintptr_t)op & 3u : 0u;
   static_for<kCopies>([&](auto q) {
-    recs[q] = (int)(min(max(rows_left - 32 * (int)q, 0), 32) * rb);
+    // up to the dword that holds the last row's last byte
+    const int n = min(rows_left - 32 * (int)q, 32);
+    recs[q] = n > 0 ? (int)((uint32_t)((n - 1) * rb + (int64_t)K * EB + off + 3) & ~3u) : 0;
   });
   // per group: the byte step of a k-tile, and (N-contiguous B) of a copy
   uint32_t kt_bytes = kUsed, q_bytes = 0;
   const uint8_t* qbase = op;
   if constexpr (kShift) {
     // every row from the dword that holds its first byte; the window's last
-    // chunk is never read; records end with the last row's last dword
-    const uint32_t off = (uint32_t)(uintptr_t)op & 3u;
+    // chunk is never read
     qbase = op - off;
     const int c = Swz::chunk(r0, t % kChunks);
     voff = c == 7 ? 0x80000000u : (uint32_t)((off + (uint32_t)(r0 * rb)) & ~3u) + c * 16;
-    static_for<kCopies>([&](auto q) {
-      const int n = min(rows_left - 32 * (int)q, 32);
-      recs[q] = n > 0 ? (int)((uint32_t)((n - 1) * rb + (int64_t)K * EB + off + 3) & ~3u) : 0;
-    });
   }
+  // a k-rows operand of `lines` columns: up to its last element's dword
+  auto k_rows_bytes = [&](int64_t ld, int lines) {
+    return K > 0 ? (int)min((((K - 1) * ld + lines) * EB + 3) & ~(int64_t)3, (int64_t)0x7FFFFFFC) : 0;
+  };
   int64_t q_stride = 32 * rb;
   if constexpr (kBT) {
     if (grp == 1) {
@@ -133,36 +135,37 @@ __device__ __forceinline__ void two_group_tile(const GroupedParams& p, const Til
       // holding columns n0 + 8 ((t % 32) ^ 4 (r0 % 4)) .. + 7
       const int64_t ldb = p.ldb;
       const int rt = t >> 5;
-      const int n = min(n0 + 8 * ((t & 31) ^ (4 * (rt & 3))), p.N - 8);
+      const int n = min(n0 + 8 * ((t & 31) ^ (4 * (rt & 3))), (p.N - 1) & ~7);
       voff = (uint32_t)((rt * ldb + n) * EB);
       kt_bytes = (uint32_t)(BK * ldb * EB);
       q_bytes = (uint32_t)(8 * ldb * EB);
       qbase = B;
       q_stride = 0;
-      const int64_t whole = (int64_t)K * ldb * EB;
-      static_for<kCopies>([&](auto q) { recs[q] = (int)min(whole, (int64_t)0x7FFFFFFF); });
+      const int whole = k_rows_bytes(ldb, p.N);
+      static_for<kCopies>([&](auto q) { recs[q] = whole; });
     }
   }
   if constexpr (kAT) {
     if (grp == 0) {
       // the same for an M-contiguous A (column-major M x K, pitch lda):
       // row rt (+ 8 q) of k, stored chunk t % 32 holding columns
-      // m0 + 8 ((t % 32) ^ 4 (rt % 4)) .. + 7, clamped to the last chunk of M
+      // m0 + 8 ((t % 32) ^ 4 (rt % 4)) .. + 7, clamped to M's last chunk
+      // (whose columns past M feed nothing that is stored)
       const int64_t lda = p.lda;
       const int rt = t >> 5;
-      const int m = min(m0 + 8 * ((t & 31) ^ (4 * (rt & 3))), p.M - 8);
+      const int m = min(m0 + 8 * ((t & 31) ^ (4 * (rt & 3))), (p.M - 1) & ~7);
       voff = (uint32_t)((rt * lda + m) * EB);
       kt_bytes = (uint32_t)(BK * lda * EB);
       q_bytes = (uint32_t)(8 * lda * EB);
       qbase = A;
       q_stride = 0;
-      const int64_t whole = (int64_t)K * lda * EB;
-      static_for<kCopies>([&](auto q) { recs[q] = (int)min(whole, (int64_t)0x7FFFFFFF); });
+      const int whole = k_rows_bytes(lda, p.M);
+      static_for<kCopies>([&](auto q) { recs[q] = whole; });
     }
   }
-  // The ragged last k-tile (K a multiple of the 16-byte chunk): a lane whose
-  // K-contiguous chunk lies past K reads from past every record, so the
-  // range check returns zeros; the rows past K of a k-rows slab (an M- or
+  // The ragged last k-tile: a lane whose K-contiguous chunk lies past K reads
+  // from past every record, so the range check returns zeros (the chunk that
+  // crosses K: clear_tail); the rows past K of a k-rows slab (an M- or
   // N-contiguous operand) are past its records already.
   uint32_t voff_tail = voff;
   if (!kShift && ((grp == 0 && !kAT) || (grp == 1 && !kBT))) {
@@ -293,16 +296,18 @@ __device__ __forceinline__ void two_group_tile(const GroupedParams& p, const Til
       });
     }
   };
-  // kShift: clears what a ragged last k-tile holds past K (the next row's
-  // bytes), a thread a row of its group's slab, before anyone reads it.
-  const bool ragged = kShift && KTf < KT;
+  // Clears what a last k-tile that ends inside a chunk holds past K (the next
+  // row's bytes), a thread a row of its group's slab, before anyone reads it.
+  const bool ragged = kForm != kGrad && KTf < KT && (kShift || K * EB % 16 != 0);
   auto clear_tail = [&]() {
     const int kt = KT - 1, slot = grp == 0 ? (kt & 1) : kt % 3;
-    if (kHalf && grp == 0 && t >= BM) return;
+    if ((kHalf && grp == 0 && t >= BM) || (kBT && grp == 1)) return;
     uint8_t* row = smem + lds_op + slot * SLAB + t * kRowBytes;
-    const uint32_t sh = ((uint32_t)(uintptr_t)op + (uint32_t)t * (uint32_t)rb) & 3u;
+    const uint32_t sh =
+        kShift ? ((uint32_t)(uintptr_t)op + (uint32_t)t * (uint32_t)rb) & 3u : 0u;
     const int first = (int)sh + K * EB - KTf * kUsed;  // of the window's bytes, the first past K
-    for (int d = first >> 2; d < 28; ++d) {
+    const int end = kShift ? 28 : (first + 15) / 16 * 4;
+    for (int d = first >> 2; d < end; ++d) {
       uint32_t* w = (uint32_t*)(row + Swz::chunk(t, d >> 2) * 16 + (d & 3) * 4);
       *w = d == first >> 2 ? *w & ((1u << (8 * (first & 3))) - 1u) : 0u;
     }
@@ -415,7 +420,7 @@ __device__ __forceinline__ void two_group_tile(const GroupedParams& p, const Til
       wait_vmcnt<0>();
       barrier();
       for (int kt = 0; kt < KT; ++kt) {
-        if constexpr (kShift) {
+        if constexpr (kForm != kGrad) {
           if (ragged && kt + 1 == KT) {
             clear_tail();
             barrier();
@@ -425,7 +430,7 @@ __device__ __forceinline__ void two_group_tile(const GroupedParams& p, const Til
         wait_lgkmcnt0();
         barrier();
         compute();
-        if constexpr (kShift) pin();
+        if constexpr (kForm != kGrad) pin();
         wait_vmcnt<0>();                             // A of kt+1 landed
         barrier();
       }
@@ -434,7 +439,7 @@ __device__ __forceinline__ void two_group_tile(const GroupedParams& p, const Til
       copy_slab(1, 1, KT > 1, CopiesB{});
       wait_vmcnt<kCopies>();
       barrier();
-      if constexpr (kShift) {
+      if constexpr (kForm != kGrad) {
         if (ragged && KT == 1) {
           clear_tail();
           barrier();
@@ -448,7 +453,7 @@ __device__ __forceinline__ void two_group_tile(const GroupedParams& p, const Til
         wait_lgkmcnt0();
         wait_vmcnt<kCopies>();                       // B of kt+1 landed
         barrier();
-        if constexpr (kShift) {
+        if constexpr (kForm != kGrad) {
           // while group 0 clears the last k-tile's A, before it reads it
           if (ragged && kt + 2 == KT) {
             clear_tail();

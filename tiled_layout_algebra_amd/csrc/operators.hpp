@@ -57,11 +57,9 @@ inline int64_t row_tiles_bound(int64_t rows, int64_t groups, int64_t BM) {
 int launch_grouped_general(const GroupedParams& p, int type, bool b_kc, hipStream_t stream);
 int launch_wgrad_general(const GroupedParams& p, int type, hipStream_t stream);
 
-// The direct-copy kernels.  Product: A's rows and, for nk, B's are 16-byte
-// aligned, a multiple of 16 bytes of K long and less than 8 MiB apart; kn: B
-// is 16-bit with 16-byte aligned rows, N a multiple of 8, a matrix below
-// 2 GiB.  Gradient: both operands have 16-byte aligned rows, M and N are
-// multiples of 8, each operand is below 2 GiB.
+// The direct-copy kernels: every row starts on a dword.  Product: A's rows and,
+// for nk, B's are less than 8 MiB apart; kn: B is 16-bit, a matrix below 2 GiB.
+// Gradient: each operand is below 2 GiB.
 // 256 x 256 tiles (grouped_two_group.hpp)
 int launch_two_group_nk16(const GroupedParams& p, int type, hipStream_t stream);
 int launch_two_group_nk8(const GroupedParams& p, int type, hipStream_t stream);

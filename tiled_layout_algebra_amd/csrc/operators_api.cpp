@@ -40,8 +40,8 @@ struct Plan {
   Kernel kernel;
 };
 
-// Rows of `ld` elements of eb bytes at p start on 16-byte boundaries.
-bool rows16(const void* p, int64_t ld, int eb) { return aligned_to(p, 16) && ld * eb % 16 == 0; }
+// Rows of `ld` elements of eb bytes at p start on dwords.
+bool dword_rows(const void* p, int64_t ld, int eb) { return aligned_to(p, 4) && ld * eb % 4 == 0; }
 
 // Whether a kernel takes the problem.
 bool takes(Kernel k, const tla_grouped_gemm_args* a, int eb, bool b_kc) {
@@ -53,10 +53,10 @@ bool takes(Kernel k, const tla_grouped_gemm_args* a, int eb, bool b_kc) {
   if (a->lda * eb >= (kLimit >> 8) || (b_kc && a->ldb * eb >= (kLimit >> 8))) return false;
   if (k >= kTwoGroupShift) return b_kc;
   if (k == kDirect64 && !b_kc) return false;
-  if (a->K * eb % 16 != 0 || !rows16(a->A, a->lda, eb) || !rows16(a->B, a->ldb, eb) ||
-      (a->groups > 1 && a->stride_b * eb % 16 != 0))
+  if (!dword_rows(a->A, a->lda, eb) || !dword_rows(a->B, a->ldb, eb) ||
+      (a->groups > 1 && a->stride_b * eb % 4 != 0))
     return false;
-  return b_kc || (eb == 2 && a->N % 8 == 0 && a->K * a->ldb * eb < kLimit);
+  return b_kc || (eb == 2 && a->K * a->ldb * eb < kLimit);
 }
 
 // Blocks of bm rows the experts need, about: a block at least for each that
@@ -328,8 +328,8 @@ int tla_grouped_gemm_wgrad(const tla_grouped_wgrad_args* a, void* stream) {
   if (a->ldd % per16 == 0 && a->stride_d % per16 == 0 && aligned_to(a->D, 16)) p.flags |= kOpD16;
   if (!row) p.flags |= kOpSumA;
   // the direct copies' layout (operators.hpp, launch_wgrad_two_group)
-  const bool direct = rows16(a->A, a->lda, 2) && rows16(a->Y, a->ldy, 2) && a->K % 8 == 0 &&
-                      a->N % 8 == 0 && a->rows * a->lda * 2 < kLimit && a->rows * a->ldy * 2 < kLimit;
+  const bool direct = dword_rows(a->A, a->lda, 2) && dword_rows(a->Y, a->ldy, 2) &&
+                      a->rows * a->lda * 2 < kLimit && a->rows * a->ldy * 2 < kLimit;
   // 256 x 256 tiles when they give every compute unit one (8000 rows on 16
   // experts of 2048 x 2048: 82 us against 101 for 128 x 128); below, 128 x 128
   // with two stages (777 rows, 16 experts of 512 x 1024: 17.2 us against 22.6
