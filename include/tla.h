@@ -1,7 +1,8 @@
 /*
  * tla.h -- C ABI of libtla.so: a layout-algebra-driven tiled GEMM with a
  * fused epilogue, a layout-driven tiled transpose, and a device evaluator
- * of shape/stride layouts, for AMD Instinct MI355X (gfx950 / CDNA4).
+ * of shape/stride layouts, for AMD Instinct MI355X (gfx950 / CDNA4); and
+ * products of rows grouped by expert, an int8 product and a quantizer.
  *
  * Conventions shared by every entry point
  * ---------------------------------------

@@ -343,3 +343,60 @@ def test_every_kernel_keeps_and_differentiates(variant):
         for z in (tla.Z_STORE, tla.Z_GRAD):
             Product([150, 3, 0, 70], 200, 512, kind, z=z, act=tla.ACT_GELU,
                     seed=z).call(variant=variant).verify()
+
+
+@pytest.mark.parametrize("variant", range(tla.GROUPED_VARIANTS))
+def test_offsets_past_32_bits(variant):
+    """Rows of A and D and the experts' matrices further apart than 2^32
+    bytes: 1100 rows 4 MiB apart, the second expert's weights 4.3 GB on."""
+    rows, N, K, lda, ldd, stride = 1100, 40, 512, 1 << 21, 1 << 21, (1 << 31) + 64
+    p = Product([600, 500], N, K, tla.BF16, bias=True, seed=13)
+    A = torch.empty(rows, lda, dtype=torch.bfloat16, device="cuda")
+    A[:, :K] = p.A.cuda()
+    D = torch.empty(rows, ldd, dtype=torch.bfloat16, device="cuda")
+    B = torch.empty(stride + N * K, dtype=torch.bfloat16, device="cuda")
+    nk = p.B.transpose(1, 2).contiguous().cuda()
+    for e in range(2):
+        B[e * stride:e * stride + N * K] = nk[e].reshape(-1)
+    off = torch.tensor(p.off, dtype=torch.int32).cuda()
+    tla.grouped_gemm(2, rows, N, K, off, A, tla.BF16, lda, B, tla.COL_MAJOR, K, stride, D, tla.BF16,
+                     ldd, bias=p.bias.cuda(), variant=variant)
+    (_, ref, bound), = p.expect()
+    check(D[:, :N].cpu(), ref, bound, "D")
+
+
+def test_gradient_and_codes_past_32_bits():
+    """A gradient over rows 8 MiB apart (9.2 GB of A), into matrices 4.3 GB
+    apart, and codes of rows 8 MiB apart."""
+    rows, N, K, lda, stride = 1100, 24, 40, 1 << 22, (1 << 30) + 8
+    gen = torch.Generator().manual_seed(6)
+    A, Y = values(gen, (rows, K), tla.BF16), values(gen, (rows, N), tla.BF16)
+    Ad = torch.empty(rows, lda, dtype=torch.bfloat16, device="cuda")
+    Ad[:, :K] = A.cuda()
+    D = torch.empty(stride + K * N, device="cuda")
+    off = [0, 700, rows]
+    tla.grouped_gemm_wgrad(2, rows, N, K, torch.tensor(off, dtype=torch.int32).cuda(), Ad, lda,
+                           Y.cuda(), N, tla.BF16, D, tla.F32, tla.ROW_MAJOR, N, stride)
+    want, S, _, _ = og.wgrad(A, Y, off)
+    for e in range(2):
+        got = D[e * stride:e * stride + K * N].view(K, N).cpu()
+        check(got, want[e], S[e] * (704 * 2.0 ** -24) + half_step(want[e].abs(), tla.F32), "D")
+    Q = torch.empty(rows, lda, dtype=torch.int8, device="cuda")
+    s = torch.empty(rows, device="cuda")
+    tla.quantize_rows(rows, K, Ad, tla.BF16, lda, Q, lda, s)
+    q, scale = og.quantize_rows(A)
+    assert torch.equal(Q[:, :K].cpu(), q) and torch.equal(s.cpu(), scale)
+
+
+@pytest.mark.parametrize("variant", range(tla.GROUPED_VARIANTS))
+def test_e4m3_nan_stays_in_its_row(variant):
+    p = Product([40, 150], 72, 512, tla.E4M3, seed=14)
+    raw = p.A.view(torch.int8)
+    raw[3, 5] = 0x7F
+    raw[100, 511] = -1  # the negative NaN, 0xFF
+    p.call(variant=variant)
+    got = p.logical(p.D)[0]
+    assert got[3].isnan().all() and got[100].isnan().all()
+    rest = [r for r in range(190) if r not in (3, 100)]
+    (_, ref, bound), = p.expect()
+    check(got[rest], ref[rest], bound[rest], "rows beside")

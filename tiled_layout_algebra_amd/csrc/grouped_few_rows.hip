@@ -12,6 +12,11 @@
 //
 // Weights of 8 bits are read as they are: int8 goes to the integer
 // instruction, e4m3 is widened to f16, which holds it exactly.
+//
+// Bound by memory.  Measured: bf16, 128 rows on 32 experts of 2048 x 4096 107 us
+// (537 MB of weights: 5.0 TB/s, what a copy reaches), two rows on two experts of
+// 4096 x 4096 12-14 us (67 MB: 5 TB/s); one int8 row x 4096 x 4096 6.5 us, of which
+// about 4 are a launch's.
 #include "grouped_common.hpp"
 
 namespace tla {

@@ -13,8 +13,13 @@
 // difference, which puts zeros past the end: no load is predicated, none
 // leaves the matrix, and every k-tile runs the same code, two tiles ahead of
 // the MFMAs in two register sets.  (One loop for whole and another, chunk by
-// chunk, for ragged k-tiles: 555 rows' gradient 277 x 1688 took 29 us.)  Lines
-// shorter than a chunk and 8-bit N-contiguous weights go element by element.
+// chunk, for ragged k-tiles: 555 rows' gradient 277 x 1688 took 29 us, 11.6
+// now.)  Lines shorter than a chunk and 8-bit N-contiguous weights go element by
+// element.
+//
+// Bound by LDS (fragment reads and the staged writes) at one workgroup's share
+// of two a compute unit.  Measured: bf16, 16384 rows on 8 experts, [K, N] weights
+// of 4095 x 4095 1030 us, the weight gradient 4095 x 4095 1220 us.
 #include "grouped_common.hpp"
 
 namespace tla {

@@ -16,6 +16,9 @@
 // half a unit of s's last place and at most s/2 in size up to that error, so
 // the fused multiply-add gives it exactly, and comparing it with s/2 rounds as
 // the true quotient does.
+//
+// Measured: 16384 x 8191 bf16 75 us (403 MB: 5.4 TB/s), 12608 x 811 fp32 11 us,
+// 64 x 4096 bf16 4.5 us (a launch).
 #include "grouped_common.hpp"
 
 namespace tla {
