@@ -424,10 +424,27 @@ __device__ __forceinline__ void two_group_tile(const GroupedParams& p, const Til
   // such a conditional barrier into the next period (it does so for e4m3,
   // which then measured 3664 cycles per k-tile): an empty asm reading every
   // accumulator keeps them in front of it.
+  // The columns' bias and scales come into the cache under the loop: a byte of
+  // each is asked for here and waited for with the first slabs, so that no
+  // epilogue pass begins with a trip to memory.
+  [[maybe_unused]] uint32_t warm = 0;
+  if constexpr (kForm != kGrad) {
+    const int64_t at = (int64_t)e * p.N + min(n0 + wn0 + 2 * lane, p.N - 1);
+    if (p.bias) warm = p.bias[at * type_bytes(p.bias_type)];
+    if constexpr (EB == 1) {
+      if (p.sb) warm += *(const uint8_t*)(p.sb + at);
+    }
+  }
+  auto warmed = [&]() {
+#if defined(__HIP_DEVICE_COMPILE__)
+    if constexpr (kForm != kGrad) asm volatile("" ::"v"(warm));
+#endif
+  };
   if (KT > 0) {
     if (grp == 0) {
       copy_slab(0, 0, true, CopiesA{});
       wait_vmcnt<0>();
+      warmed();
       barrier();
       for (int kt = 0; kt < KT; ++kt) {
         if constexpr (kForm != kGrad) {
@@ -448,6 +465,7 @@ __device__ __forceinline__ void two_group_tile(const GroupedParams& p, const Til
       copy_slab(0, 0, true, CopiesB{});
       copy_slab(1, 1, KT > 1, CopiesB{});
       wait_vmcnt<kCopies>();
+      warmed();
       barrier();
       if constexpr (kForm != kGrad) {
         if (ragged && KT == 1) {
