@@ -448,43 +448,45 @@ __device__ __forceinline__ void wgrad_epilogue(const GroupedParams& p, int e, in
 }
 
 // The bias gradient beside the weight gradient: sums over k of each line (a
-// column of dY) of an operand's fragments, by the 16x16 matrix instruction.
-// As its first operand a 32x32 fragment's lane l is row l % 16 and K group
-// l / 16, of which the lowest bit tells lines 0-15 from 16-31; the second
-// operand holds ones where that bit equals its column (0 or 1), so column 0
-// of the result sums lines 0-15 and column 1 lines 16-31.  Half the time of
-// one 32x32 instruction a fragment, four registers each.  One block of tiles
-// along the other extent does it: next to a pass over dY of its own (26 us of
-// 553 for 16384 rows of 4096) it reads nothing.
+// column of dY) of an operand's fragments.  A 32x32 fragment's lane l holds eight
+// values of line l % 32, K half l / 32.  The matrix instruction of sixteen 4x4
+// blocks takes each lane as a column of its own block, so with ones as the other
+// operand every result of lane l is the sum of that lane's four values: two of
+// them a fragment, and a line never meets another one, whose infinity or NaN (a
+// neighbour's, or the padding's behind the last column) stays in its own sum.
+// Half the time of one 32x32 instruction a fragment, four registers each.
+// One block of tiles along the other extent does it: next to a pass
+// over dY of its own (26 us of 553 for 16384 rows of 4096) it reads nothing.
 template <int kCode, int kN>
 struct LineSums {
   f32x4 s[kN];
-  i32x4 ones;
-  __device__ __forceinline__ void init(int lane) {
-    const int h = kCode == kBF16 ? 0x3F803F80 : 0x3C003C00;
-    const int w = (lane & 15) < 2 && ((lane >> 4) & 1) == (lane & 15) ? h : 0;
-    ones = i32x4{w, w, w, w};
+  __device__ __forceinline__ void init() {
     static_for<kN>([&](auto i) { s[i] = f32x4{0.f, 0.f, 0.f, 0.f}; });
   }
   template <int kI>
   __device__ __forceinline__ void add(const i32x4& f) {
-    if constexpr (kCode == kBF16)
-      s[kI] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, f),
-                                                      __builtin_bit_cast(bf16x8, ones), s[kI], 0, 0, 0);
-    else
-      s[kI] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, f),
-                                                     __builtin_bit_cast(f16x8, ones), s[kI], 0, 0, 0);
+    typedef int i32x2 __attribute__((ext_vector_type(2)));
+    static_for<2>([&](auto h) {
+      const i32x2 x = {f[2 * h], f[2 * h + 1]};
+      if constexpr (kCode == kBF16) {
+        const i32x2 ones = {0x3F803F80, 0x3F803F80};
+        s[kI] = __builtin_amdgcn_mfma_f32_4x4x4bf16_1k(__builtin_bit_cast(s16x4, ones),
+                                                       __builtin_bit_cast(s16x4, x), s[kI], 0, 0, 0);
+      } else {
+        typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+        const i32x2 ones = {0x3C003C00, 0x3C003C00};
+        s[kI] = __builtin_amdgcn_mfma_f32_4x4x4f16(__builtin_bit_cast(f16x4, ones),
+                                                   __builtin_bit_cast(f16x4, x), s[kI], 0, 0, 0);
+      }
+    });
   }
   // the sums of fragment i's lines first + 32 i .. that lie below `lines`
   template <int kCount>
   __device__ __forceinline__ void write(float* out, int first, int lines, int lane) const {
-    if ((lane & 15) >= 2) return;
     static_for<kCount>([&](auto i) {
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int n = first + 32 * i + 16 * (lane & 15) + 4 * (lane >> 4) + r;
-        if (n < lines) out[n] = s[i][r];
-      }
+      const float sum = s[i][0] + __shfl_xor(s[i][0], 32);  // the two K halves
+      const int n = first + 32 * i + lane;
+      if (lane < 32 && n < lines) out[n] = sum;
     });
   }
 };

@@ -260,7 +260,7 @@ __global__ __launch_bounds__(64 * kWM * kWN) void grouped_direct_kernel(const Gr
   typename Atom::Acc acc[FM][FN];
   static_for<FM>([&](auto i) { static_for<FN>([&](auto j) { acc[i][j] = typename Atom::Acc{}; }); });
   LineSums<kCode, (FM > FN ? FM : FN)> sums;
-  if constexpr (kForm == kGrad) sums.init(lane);
+  if constexpr (kForm == kGrad) sums.init();
   Frag a[2][FM], b[2][FN];
   auto lds_frag = [&](const uint32_t (&base)[kSub], int imm) -> Frag {
     if constexpr (kSub == 1) {

@@ -132,7 +132,7 @@ __global__ __launch_bounds__(kThreads, kBView == kBElem ? 1 : 2) void grouped_ge
   typename Atom::Acc acc[FM][FN];
   static_for<FM>([&](auto i) { static_for<FN>([&](auto j) { acc[i][j] = typename Atom::Acc{}; }); });
   LineSums<kCode, FM> sums;
-  if constexpr (kWgrad) sums.init(lane);
+  if constexpr (kWgrad) sums.init();
   Frag a[2][FM], b[2][FN];
   auto read_frags = [&](auto buf, const uint8_t* stage, auto ks) {
     static_for<FM>([&](auto i) {

@@ -366,7 +366,7 @@ __device__ __forceinline__ void two_group_tile(const GroupedParams& p, const Til
   typename Atom::Acc acc[FM][FN];
   static_for<FM>([&](auto i) { static_for<FN>([&](auto j) { acc[i][j] = typename Atom::Acc{}; }); });
   LineSums<kCode, FN> sums;
-  if constexpr (kForm == kGrad) sums.init(lane);
+  if constexpr (kForm == kGrad) sums.init();
   // one k-tile of MFMAs, fenced off from the scheduler on both sides so that
   // no wait or memory instruction of a neighbouring phase moves into it
   auto compute = [&]() {
