@@ -239,7 +239,7 @@ int tla_grouped_gemm_variant(const tla_grouped_gemm_args *args, char *buf, int32
  *   1 "grouped_two_group_256x256"        direct copies: rows that start on
  *                                        dwords, less than 8 MiB apart, K > 0;
  *                                        b_order TLA_ROW_MAJOR: 16-bit, each
- *                                        B_e below 2 GiB
+ *                                        B_e (of max(K, 64) rows) below 2 GiB
  *   2 "grouped_direct_128x128"           the same
  *   3 "grouped_direct_64x128"            the same, TLA_COL_MAJOR only
  *   4 "grouped_few_rows_64"              blocks of 64, 32 and 16 rows, weights

@@ -92,3 +92,32 @@ def test_not_finite_stays_in_its_column(kernel, order, kind, bad):
     p.Y[151, 3] = -bad      # of expert 2
     p.A[3, 33] = bad
     p.verify(tla.F32, order, 0, 0, shift)
+
+
+def test_wide_pitches_with_few_rows():
+    """8 rows 128 MiB apart: a slab of the direct copies has 64 rows, whose byte
+    offsets would pass 2^32 and come back to rows and padding in use."""
+    rows, N, K, ld = 8, 24, 40, (1 << 26) + 64
+    gen = torch.Generator().manual_seed(2)
+    A, Y = values(gen, (rows, K), tla.BF16), values(gen, (rows, N), tla.BF16)
+    bufs = []
+    for m in (A, Y):
+        buf = torch.full((rows, ld), float("nan"), dtype=torch.bfloat16, device="cuda")
+        buf[:, :m.shape[1]] = m.cuda()
+        bufs.append(buf)
+    D, db = torch.empty(1, K, N, device="cuda"), torch.empty(1, N, device="cuda")
+    tla.grouped_gemm_wgrad(1, rows, N, K, None, bufs[0], ld, bufs[1], ld, tla.BF16, D, tla.F32,
+                           tla.ROW_MAJOR, N, K * N, dbias=db)
+    want, S, want_b, Sb = og.wgrad(A, Y, [0, rows])
+    eps = (rows + 4) * 2.0 ** -24
+    check(D.cpu(), want, S * eps + half_step(want.abs(), tla.F32), "D")
+    check(db.cpu(), want_b, Sb * eps + 1e-45, "dbias")
+    # the [K, N] product over the same rows: D [rows of X, N] = X A with X [5, 8]
+    X = values(gen, (5, rows), tla.BF16)
+    for buf, m in zip(bufs, (A, Y)):
+        n = m.shape[1]
+        P = torch.empty(5, n, dtype=torch.bfloat16, device="cuda")
+        tla.grouped_gemm(1, 5, n, rows, None, X.cuda(), tla.BF16, rows, buf, tla.ROW_MAJOR, ld, 0, P,
+                         tla.BF16, n)
+        ref, s = X.double() @ m.double(), X.double().abs() @ m.double().abs()
+        check(P.cpu(), ref, s * eps + half_step(ref.abs() + s * eps, tla.BF16), "product")

@@ -249,3 +249,19 @@ def test_quantizer_oracle_rounds_exactly():
         for c in range(60):
             f = Fraction(float(x[r, c])) / Fraction(float(s[r]))
             assert int(q[r, c]) == max(-127, min(127, round(f)))
+
+
+def test_slabs_of_k_rows_stay_within_32_bit_offsets():
+    """[K, N] weights: a slab holds 64 rows of k however few there are, so the
+    direct copies need 64 pitches below 2^31 bytes, and K of them."""
+    kn = dict(b_order=tla.ROW_MAJOR, lda=64)
+    f = tla.lib().tla_grouped_gemm_run_variant
+    for K, ldb in ((8, 1 << 24), (8, 1 << 26), (1, 1 << 30), (64, 1 << 24), (100, 1 << 24), (8, 1 << 62)):
+        kw = dict(kn, K=K, ldb=ldb, lda=(K + 7) & ~7, groups=1)
+        assert _variant(**kw) == "grouped_general_128x128"
+        for v in (1, 2):
+            assert f(ctypes.byref(_product(**kw)), v, None) == tla.ERR_UNSUPPORTED
+    assert _variant(**dict(kn, K=64, ldb=(1 << 24) - 8, groups=1)) == "grouped_direct_128x128"
+    # pitches that no 64-bit count of bytes holds
+    assert f(ctypes.byref(_product(groups=1, rows=1, lda=1 << 62)), 1, None) == tla.ERR_UNSUPPORTED
+    assert f(ctypes.byref(_product(groups=1, N=1, ldb=1 << 62)), 2, None) == tla.ERR_UNSUPPORTED

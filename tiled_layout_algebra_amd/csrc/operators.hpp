@@ -58,8 +58,8 @@ int launch_grouped_general(const GroupedParams& p, int type, bool b_kc, hipStrea
 int launch_wgrad_general(const GroupedParams& p, int type, hipStream_t stream);
 
 // The direct-copy kernels: every row starts on a dword.  Product: A's rows and,
-// for nk, B's are less than 8 MiB apart; kn: B is 16-bit, a matrix below 2 GiB.
-// Gradient: each operand is below 2 GiB.
+// for nk, B's are less than 8 MiB apart; kn: B is 16-bit, a matrix (of 64 rows
+// if it has fewer) below 2 GiB.  Gradient: each operand (likewise) below 2 GiB.
 // 256 x 256 tiles (grouped_two_group.hpp)
 int launch_two_group_nk16(const GroupedParams& p, int type, hipStream_t stream);
 int launch_two_group_nk8(const GroupedParams& p, int type, hipStream_t stream);

@@ -43,6 +43,14 @@ struct Plan {
 // Rows of `ld` elements of eb bytes at p start on dwords.
 bool dword_rows(const void* p, int64_t ld, int eb) { return aligned_to(p, 4) && ld * eb % 4 == 0; }
 
+// Whether the direct copies' 32-bit offsets reach a slab of k rows `ld` elements
+// apart.  A slab has 64 rows however few the sum has, and the range check that
+// zeroes the ones past its end needs their offsets unwrapped: below 2^31 bytes
+// for max(k, 64) rows, so below 2^32 for the last slab's.
+bool k_rows_fit(int64_t k, int64_t ld, int eb) {
+  return ld < kLimit / ((k > 64 ? k : 64) * eb);
+}
+
 // Whether a kernel takes the problem.
 bool takes(Kernel k, const tla_grouped_gemm_args* a, int eb, bool b_kc) {
   if (k == kGeneral) return true;
@@ -50,13 +58,13 @@ bool takes(Kernel k, const tla_grouped_gemm_args* a, int eb, bool b_kc) {
   if (k == kFewRows1 || k == kFewRows2 || k == kFewRows4) return b_kc;
   if (a->type == TLA_E4M3 && a->K < kMinKE4m3) return false;
   // 32-bit offsets within a tile's rows
-  if (a->lda * eb >= (kLimit >> 8) || (b_kc && a->ldb * eb >= (kLimit >> 8))) return false;
+  if (a->lda >= (kLimit >> 8) / eb || (b_kc && a->ldb >= (kLimit >> 8) / eb)) return false;
   if (k >= kTwoGroupShift) return b_kc;
   if (k == kDirect64 && !b_kc) return false;
   if (!dword_rows(a->A, a->lda, eb) || !dword_rows(a->B, a->ldb, eb) ||
       (a->groups > 1 && a->stride_b * eb % 4 != 0))
     return false;
-  return b_kc || (eb == 2 && a->K * a->ldb * eb < kLimit);
+  return b_kc || (eb == 2 && k_rows_fit(a->K, a->ldb, eb));
 }
 
 // Blocks of bm rows the experts need, about: a block at least for each that
@@ -329,7 +337,7 @@ int tla_grouped_gemm_wgrad(const tla_grouped_wgrad_args* a, void* stream) {
   if (!row) p.flags |= kOpSumA;
   // the direct copies' layout (operators.hpp, launch_wgrad_two_group)
   const bool direct = dword_rows(a->A, a->lda, 2) && dword_rows(a->Y, a->ldy, 2) &&
-                      a->rows * a->lda * 2 < kLimit && a->rows * a->ldy * 2 < kLimit;
+                      k_rows_fit(a->rows, a->lda, 2) && k_rows_fit(a->rows, a->ldy, 2);
   // 256 x 256 tiles when they give every compute unit one (8000 rows on 16
   // experts of 2048 x 2048: 82 us against 101 for 128 x 128); below, 128 x 128
   // with two stages (777 rows, 16 experts of 512 x 1024: 17.2 us against 22.6
