@@ -631,19 +631,24 @@ int gemm_dispatch(const GemmProblem& g, hipStream_t stream, bool dry_run, const 
   const bool k_ok = g.K > 0 && (g.K % (16 / eb)) == 0;
   const bool k_slab = g.K > 0 && (g.K % BK) == 0;
   const bool fast = a_vec && b_vec && small_ops && k_ok;
+  // an operand stored as rows of k: a slab has 64 of them however small K is,
+  // and the range check that zeroes the ones past K needs unwrapped offsets
+  auto k_rows_fit = [&](int64_t ld) {
+    return ld <= 0x7FFFFFFF / ((g.K > 64 ? g.K : 64) * eb);
+  };
   // A in the fast layout, B a 16-bit row-major K x N matrix with 16-byte
   // aligned rows and whole 16-byte chunks of columns, below 2 GiB
   const bool bt = !fast && nt && a_vec && b_rows16 && g.N % 8 == 0 &&
                   (int64_t)g.M * g.lda * eb < (int64_t(1) << 31) &&
-                  (int64_t)g.K * g.ldb * eb < (int64_t(1) << 31) && k_ok;
+                  k_rows_fit(g.ldb) && k_ok;
   // A a 16-bit column-major M x K matrix with 16-byte aligned columns, M a
   // multiple of 8, below 2 GiB; B K-contiguous or N-contiguous as above
   const bool b_any = (b_vec && (int64_t)g.N * g.ldb * eb < (int64_t(1) << 31)) ||
                      (nt && b_rows16 && g.N % 8 == 0 &&
-                      (int64_t)g.K * g.ldb * eb < (int64_t(1) << 31));
+                      k_rows_fit(g.ldb));
   const bool at = eb == 2 && g.a_order == TLA_COL_MAJOR && ((g.lda * eb) % 16) == 0 &&
                   aligned(g.A, 16) && g.M % 8 == 0 &&
-                  (int64_t)g.K * g.lda * eb < (int64_t(1) << 31) && k_ok && b_any;
+                  k_rows_fit(g.lda) && k_ok && b_any;
   const int64_t tiles256 = ((g.M + 255) / 256) * ((g.N + 255) / 256);
   const bool big = tiles256 >= 128;
   switch (g.a_type) {

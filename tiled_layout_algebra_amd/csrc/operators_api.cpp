@@ -48,7 +48,7 @@ bool dword_rows(const void* p, int64_t ld, int eb) { return aligned_to(p, 4) && 
 // zeroes the ones past its end needs their offsets unwrapped: below 2^31 bytes
 // for max(k, 64) rows, so below 2^32 for the last slab's.
 bool k_rows_fit(int64_t k, int64_t ld, int eb) {
-  return ld < kLimit / ((k > 64 ? k : 64) * eb);
+  return ld <= (kLimit - 1) / ((k > 64 ? k : 64) * eb);
 }
 
 // Whether a kernel takes the problem.
