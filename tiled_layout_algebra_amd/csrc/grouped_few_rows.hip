@@ -86,7 +86,8 @@ __global__ __launch_bounds__(64 * kWaves) void grouped_few_rows_kernel(const Gro
   const int n0 = t.tn * BN;
   const int rows = min(BM, t.r1 - t.r0), cols = min(BN, p.N - n0);
   // K in steps of 64 bytes, each wave a run of them
-  const int kbytes = p.K * EB, steps = (kbytes + 63) / 64;
+  const int64_t kbytes = (int64_t)p.K * EB;
+  const int steps = (int)((kbytes + 63) / 64);
   const int s0 = (int)((int64_t)steps * wave / kWaves), s1 = (int)((int64_t)steps * (wave + 1) / kWaves);
   const uint8_t *pa[MT], *pb[NT];
   static_for<MT>([&](auto i) {
@@ -102,7 +103,7 @@ __global__ __launch_bounds__(64 * kWaves) void grouped_few_rows_kernel(const Gro
   Acc acc[MT][NT];
   static_for<MT>([&](auto i) { static_for<NT>([&](auto j) { acc[i][j] = Acc{}; }); });
 
-  const int whole = min(s1, kbytes / 64);  // steps inside K
+  const int whole = min(s1, (int)(kbytes / 64));  // steps inside K
   int s = s0;
   for (; s + kU <= whole; s += kU) {
     Chunk<kDword> a[kU][MT], b[kU][NT];
@@ -122,7 +123,7 @@ __global__ __launch_bounds__(64 * kWaves) void grouped_few_rows_kernel(const Gro
   for (; s < s1; ++s) {
     // the rest one step at a time; a lane's bytes past K are zeros, gathered
     // where they begin inside its sixteen
-    const int left = kbytes - (s * 64 + 16 * (lane >> 4));
+    const int left = (int)min(kbytes - (int64_t)s * 64, (int64_t)64) - 16 * (lane >> 4);
     auto get = [&](const uint8_t* base) {
       const uint8_t* q = base + (int64_t)s * 64;
       i32x4 x = {0, 0, 0, 0};
