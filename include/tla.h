@@ -210,8 +210,8 @@ int tla_gemm_variant_info(int32_t variant, int32_t a_type, tla_gemm_kernel_info 
  *
  * rows, N or groups == 0 is a no-op; K == 0 gives z = bias.  Padding is never
  * read or written.  Device pointers must be aligned to their elements; D and
- * Z must not overlap each other or an input.  groups, rows, N and K below
- * 2^31 (TLA_ERR_UNSUPPORTED).
+ * Z must not overlap each other or an input.  groups, rows, N and K at most
+ * 2^31 - 4096 (TLA_ERR_UNSUPPORTED).
  */
 enum { TLA_Z_NONE = 0, TLA_Z_STORE = 1, TLA_Z_GRAD = 2 };
 

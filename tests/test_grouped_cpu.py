@@ -265,3 +265,19 @@ def test_slabs_of_k_rows_stay_within_32_bit_offsets():
     # pitches that no 64-bit count of bytes holds
     assert f(ctypes.byref(_product(groups=1, rows=1, lda=1 << 62)), 1, None) == tla.ERR_UNSUPPORTED
     assert f(ctypes.byref(_product(groups=1, N=1, ldb=1 << 62)), 2, None) == tla.ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("name", ["groups", "rows", "N", "K"])
+def test_extents_leave_room_for_the_kernels_counts(name):
+    """Counts of tiles and of experts taken 64 at a time run in 32 bits, up to a
+    tile past the extent: extents end 4096 short of 2^31."""
+    most = (1 << 31) - 4096
+    wide = dict(lda=most, ldb=most, ldd=most, stride_b=0)
+    L = tla.lib()
+    buf = ctypes.create_string_buffer(64)
+    assert L.tla_grouped_gemm_variant(ctypes.byref(_product(**dict(wide, **{name: most}))), buf, 64) == tla.OK
+    over = dict(wide, lda=1 << 31, ldb=1 << 31, ldd=1 << 31, **{name: most + 1})
+    assert L.tla_grouped_gemm_variant(ctypes.byref(_product(**over)), buf, 64) == tla.ERR_UNSUPPORTED
+    assert L.tla_grouped_gemm(ctypes.byref(_product(**over)), None) == tla.ERR_UNSUPPORTED
+    w = _wgrad(lda=1 << 31, ldy=1 << 31, ldd=1 << 31, stride_d=1 << 62, **{name: most + 1})
+    assert L.tla_grouped_gemm_wgrad(ctypes.byref(w), None) == tla.ERR_UNSUPPORTED

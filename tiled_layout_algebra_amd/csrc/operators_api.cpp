@@ -10,6 +10,12 @@ using namespace tla;
 namespace {
 
 constexpr int64_t kLimit = int64_t(1) << 31;
+// Extents: the kernels count tiles (up to 256 past an extent) and experts (64 at
+// a time) in 32 bits.
+constexpr int64_t kMaxExtent = kLimit - 4096;
+bool too_large(int64_t groups, int64_t rows, int64_t N, int64_t K) {
+  return groups > kMaxExtent || rows > kMaxExtent || N > kMaxExtent || K > kMaxExtent;
+}
 // products of int8 values sum exactly in 32 bits while K * 128 * 128 < 2^31
 constexpr int64_t kMaxKI8 = 131071;
 
@@ -154,8 +160,7 @@ int plan_product(const tla_grouped_gemm_args* a, Plan* out) {
   if (!out16(a->d_type)) return TLA_ERR_UNSUPPORTED;
   if (a->bias && !aux_type(a->bias_type)) return TLA_ERR_UNSUPPORTED;
   if (!eight && (a->scale_a || a->scale_b)) return TLA_ERR_UNSUPPORTED;
-  if (a->groups >= kLimit || a->rows >= kLimit || a->N >= kLimit || a->K >= kLimit)
-    return TLA_ERR_UNSUPPORTED;
+  if (too_large(a->groups, a->rows, a->N, a->K)) return TLA_ERR_UNSUPPORTED;
   if (a->type == TLA_I8 && a->K > kMaxKI8) return TLA_ERR_UNSUPPORTED;
   *out = Plan{};
   out->kernel = kNoop;
@@ -301,8 +306,7 @@ int tla_grouped_gemm_wgrad(const tla_grouped_wgrad_args* a, void* stream) {
   if (a->groups < 0 || a->rows < 0 || a->N < 0 || a->K < 0) return TLA_ERR_INVALID_ARG;
   if (a->d_order != TLA_ROW_MAJOR && a->d_order != TLA_COL_MAJOR) return TLA_ERR_INVALID_ARG;
   if (!out16(a->type) || !aux_type(a->d_type)) return TLA_ERR_UNSUPPORTED;
-  if (a->groups >= kLimit || a->rows >= kLimit || a->N >= kLimit || a->K >= kLimit)
-    return TLA_ERR_UNSUPPORTED;
+  if (too_large(a->groups, a->rows, a->N, a->K)) return TLA_ERR_UNSUPPORTED;
   if (a->groups == 0 || a->K == 0 || a->N == 0) return TLA_OK;
   if (!a->offsets && a->groups != 1) return TLA_ERR_INVALID_ARG;
   if (a->rows > 0 && (!a->Y || a->ldy < a->N)) return TLA_ERR_INVALID_ARG;
