@@ -309,7 +309,8 @@ int tla_gemm_i8(const tla_gemm_i8_args *args, void *stream);
  * exactly (the quotient is rounded as if it were known to all digits).  A
  * row of zeros, or one whose scale rounds to 0, gets zero codes; so does a
  * row with an infinity or a NaN, whose scale is that infinity or NaN.
- * M == 0 is a no-op, K == 0 gives zero scales.
+ * M == 0 is a no-op, K == 0 gives zero scales; M below 2^31
+ * (TLA_ERR_UNSUPPORTED; rows of up to 2048 values: below 2^33).
  */
 int tla_quantize_rows(int64_t M, int64_t K, const void *X, int32_t x_type, int64_t ldx, void *Q,
                       int64_t ldq, float *scale, void *stream);

@@ -108,3 +108,22 @@ def test_codes_and_scales_feed_the_product():
     sx, sw = qs[0][1].cpu().double()[:, None], qs[1][1].cpu().double()[:, None]
     bound = (sx / 2) * w.double().abs().sum(1) + (x.double().abs().sum(1)[:, None] + K * sx / 2) * sw.t() / 2
     assert ((D.cpu().double() - ref).abs() <= bound * (1 + 1e-5) + ref.abs() * 2.0 ** -10).all()
+
+
+@pytest.mark.parametrize("M,K", [((1 << 26) + 5, 8), ((1 << 24) + 3, 2056)])
+def test_more_rows_than_one_launch_holds(M, K):
+    """A launch's threads end at 2^32, 2^26 short rows or 2^24 long ones: rows on
+    both sides of that, and that every row's scale was written."""
+    x = torch.empty(M, K, dtype=torch.bfloat16, device="cuda")
+    x.view(torch.int16).fill_(0x3F80)  # ones
+    probe = torch.tensor(sorted({0, 1, (1 << 24) - 1, 1 << 24, (1 << 24) + 1, M - 2, M - 1}), device="cuda")
+    some = torch.randn(len(probe), K, generator=torch.Generator().manual_seed(K)).bfloat16()
+    x[probe] = some.cuda()
+    Q = torch.empty(M, K, dtype=torch.int8, device="cuda")
+    s = torch.full((M,), 7.0, device="cuda")
+    tla.quantize_rows(M, K, x, tla.BF16, K, Q, K, s)
+    wq, ws = og.quantize_rows(some)
+    assert torch.equal(Q[probe].cpu(), wq) and torch.equal(s[probe].cpu(), ws)
+    assert not (s == 7.0).any()
+    s[probe] = s[2].clone()
+    assert (s == s[2]).all()

@@ -281,3 +281,8 @@ def test_extents_leave_room_for_the_kernels_counts(name):
     assert L.tla_grouped_gemm(ctypes.byref(_product(**over)), None) == tla.ERR_UNSUPPORTED
     w = _wgrad(lda=1 << 31, ldy=1 << 31, ldd=1 << 31, stride_d=1 << 62, **{name: most + 1})
     assert L.tla_grouped_gemm_wgrad(ctypes.byref(w), None) == tla.ERR_UNSUPPORTED
+
+
+def test_quantizer_rows_it_does_not_count():
+    for K, M in ((4096, 1 << 31), (8, 1 << 33), (8, (1 << 63) - 1)):
+        assert tla.lib().tla_quantize_rows(M, K, FAKE, tla.BF16, K, FAKE, K, FAKE, None) == tla.ERR_UNSUPPORTED

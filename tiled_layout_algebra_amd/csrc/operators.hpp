@@ -15,6 +15,9 @@ constexpr int type_bytes(int code) {
   return code == TLA_F32 ? 4 : (code == TLA_E4M3 || code == TLA_I8 ? 1 : 2);
 }
 
+// Threads that a launch's one dimension holds.
+constexpr int64_t kMaxThreads = 0xFFFFFFFF;
+
 // One problem: rows r of A, grouped by expert (rows offsets[e] .. offsets[e +
 // 1] - 1 belong to expert e; offsets == nullptr: one expert with every row).
 //   product            D[r, n] = epilogue(sum_k A[r, k] B_e(k, n))

@@ -200,14 +200,22 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(const uint8_t* X, in
   }
 }
 
+// The rows in launches of fewer than 2^32 threads: the runtime takes a larger
+// count modulo 2^32 and reports nothing.
 template <int kCode, int kTpr, int kV>
 int launch(int64_t M, int64_t K, const void* X, int64_t ldx, int8_t* Q, int64_t ldq, float* scale,
            hipStream_t s) {
-  const int64_t grid = (M + 256 / kTpr - 1) / (256 / kTpr);
-  if (grid > 0x7FFFFFFF) return TLA_ERR_UNSUPPORTED;
-  hipLaunchKernelGGL((quantize_rows_kernel<kCode, kTpr, kV>), dim3((unsigned)grid), dim3(256), 0,
-                     s, (const uint8_t*)X, ldx, Q, ldq, scale, M, K);
-  return hipGetLastError() == hipSuccess ? TLA_OK : TLA_ERR_HIP;
+  constexpr int64_t kRows = 256 / kTpr, kMost = kRows * (kMaxThreads / 256);
+  if (M > kRows * 0x7FFFFFFF) return TLA_ERR_UNSUPPORTED;
+  for (int64_t r = 0; r < M; r += kMost) {
+    const int64_t rows = M - r < kMost ? M - r : kMost;
+    const unsigned grid = (unsigned)((rows + kRows - 1) / kRows);
+    hipLaunchKernelGGL((quantize_rows_kernel<kCode, kTpr, kV>), dim3(grid), dim3(256), 0, s,
+                       (const uint8_t*)X + r * ldx * type_bytes(kCode), ldx, Q + r * ldq, ldq,
+                       scale + r, rows, K);
+    if (hipGetLastError() != hipSuccess) return TLA_ERR_HIP;
+  }
+  return TLA_OK;
 }
 
 // The narrowest form whose registers hold the row: a wavefront for each row
