@@ -211,7 +211,8 @@ int tla_gemm_variant_info(int32_t variant, int32_t a_type, tla_gemm_kernel_info 
  * rows, N or groups == 0 is a no-op; K == 0 gives z = bias.  Padding is never
  * read or written.  Device pointers must be aligned to their elements; D and
  * Z must not overlap each other or an input.  groups, rows, N and K at most
- * 2^31 - 4096 (TLA_ERR_UNSUPPORTED).
+ * 2^31 - 4096, and fewer than 2^24 tiles of 128 x 128 of D for any offsets
+ * (TLA_ERR_UNSUPPORTED).
  */
 enum { TLA_Z_NONE = 0, TLA_Z_STORE = 1, TLA_Z_GRAD = 2 };
 
@@ -266,8 +267,8 @@ int tla_grouped_gemm_run_variant(const tla_grouped_gemm_args *args, int32_t vari
  * (TLA_ROW_MAJOR: [K, N] weights, ldd >= N; TLA_COL_MAJOR: [N, K] weights,
  * ldd >= K).  Sums are fp32, rounded once at the end, in an order that does
  * not change from call to call.  An expert without rows gets zeros; D is
- * overwritten.  offsets as for tla_grouped_gemm.  groups, K or N == 0 is a
- * no-op.
+ * overwritten.  offsets and extents as for tla_grouped_gemm, with fewer than
+ * 2^23 tiles of 256 x 256 over all D_e.  groups, K or N == 0 is a no-op.
  */
 typedef struct {
   int64_t groups, rows, N, K;

@@ -1,0 +1,26 @@
+"""More columns than the workgroups of a one-dimensional launch of every kernel
+reach: each call is right or refused, and the library's own choice is right."""
+import pytest
+import torch
+
+import tiled_layout_algebra_amd as tla
+
+pytestmark = pytest.mark.gpu
+
+
+def test_a_token_times_half_a_billion_columns():
+    N, K = (1 << 29) + 5, 16
+    a = torch.ones(1, K, dtype=torch.int8, device="cuda")
+    b = torch.ones(N, K, dtype=torch.int8, device="cuda")
+    d = torch.empty(1, N, dtype=torch.bfloat16, device="cuda")
+    for variant in [None] + list(range(tla.GROUPED_VARIANTS)):
+        d.fill_(7)
+        args = (1, 1, N, K, None, a, tla.I8, K, b, tla.COL_MAJOR, K, 0, d, tla.BF16, N)
+        if variant in (4, 5, 6):
+            with pytest.raises(tla.TlaError) as err:
+                tla.grouped_gemm(*args, variant=variant)
+            assert err.value.status == tla.ERR_UNSUPPORTED
+            assert (d == 7).all()
+        else:
+            tla.grouped_gemm(*args, variant=variant)
+            assert (d == K).all(), variant

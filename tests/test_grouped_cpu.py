@@ -272,7 +272,7 @@ def test_extents_leave_room_for_the_kernels_counts(name):
     """Counts of tiles and of experts taken 64 at a time run in 32 bits, up to a
     tile past the extent: extents end 4096 short of 2^31."""
     most = (1 << 31) - 4096
-    wide = dict(lda=most, ldb=most, ldd=most, stride_b=0)
+    wide = dict(groups=1, rows=1, lda=most, ldb=most, ldd=most, stride_b=0)
     L = tla.lib()
     buf = ctypes.create_string_buffer(64)
     assert L.tla_grouped_gemm_variant(ctypes.byref(_product(**dict(wide, **{name: most}))), buf, 64) == tla.OK
@@ -286,3 +286,18 @@ def test_extents_leave_room_for_the_kernels_counts(name):
 def test_quantizer_rows_it_does_not_count():
     for K, M in ((4096, 1 << 31), (8, 1 << 33), (8, (1 << 63) - 1)):
         assert tla.lib().tla_quantize_rows(M, K, FAKE, tla.BF16, K, FAKE, K, FAKE, None) == tla.ERR_UNSUPPORTED
+
+
+def test_launches_stay_below_2_to_32_threads():
+    """A kernel whose workgroups pass that is not chosen and is refused by name."""
+    f = tla.lib().tla_grouped_gemm_run_variant
+    wide = dict(groups=1, rows=1, type=tla.I8, K=16, lda=16, ldb=16)
+    assert _variant(**dict(wide, N=(1 << 29) - 32, ldd=1 << 29)).startswith("grouped_few_rows")
+    over = dict(wide, N=1 << 29, ldd=1 << 29)
+    assert not _variant(**over).startswith("grouped_few_rows")
+    for v in (4, 5, 6):
+        assert f(ctypes.byref(_product(**over)), v, None) == tla.ERR_UNSUPPORTED
+    many = dict(groups=1 << 24, rows=1 << 24, N=1, K=1, lda=1, ldb=1, ldd=1, stride_b=0)
+    assert tla.lib().tla_grouped_gemm(ctypes.byref(_product(**many)), None) == tla.ERR_UNSUPPORTED
+    w = dict(groups=1 << 24, rows=4, N=1, K=1, lda=1, ldy=1, ldd=1, stride_d=1)
+    assert tla.lib().tla_grouped_gemm_wgrad(ctypes.byref(_wgrad(**w)), None) == tla.ERR_UNSUPPORTED

@@ -453,7 +453,7 @@ int launch(const GroupedParams& p0, hipStream_t stream) {
   const int64_t grid = kForm == kGrad ? (int64_t)p.groups * p.tiles_m * p.tiles_n
                                       : row_tiles_bound(p.rows, p.groups, BM) * p.tiles_n;
   if (grid <= 0) return TLA_OK;
-  if (grid > 0x7FFFFFFF) return TLA_ERR_UNSUPPORTED;
+  if (!grid_fits(grid, 64 * kWM * kWN)) return TLA_ERR_UNSUPPORTED;
   hipLaunchKernelGGL((grouped_direct_kernel<kCode, kForm, BM, BN, kStages, kFront, kWM, kWN>),
                      dim3((unsigned)grid), dim3(64 * kWM * kWN), 0, stream, p);
   return hipGetLastError() == hipSuccess ? TLA_OK : TLA_ERR_HIP;

@@ -180,7 +180,7 @@ int launch(const GroupedParams& p0, hipStream_t stream) {
   p.tiles_n = (p.N + 16 * NT - 1) / (16 * NT);
   const int64_t grid = row_tiles_bound(p.rows, p.groups, 16 * MT) * p.tiles_n;
   if (grid <= 0) return TLA_OK;
-  if (grid > 0x7FFFFFFF) return TLA_ERR_UNSUPPORTED;
+  if (!grid_fits(grid, 64 * kWaves)) return TLA_ERR_UNSUPPORTED;
   const bool dword = aligned(p.A, 4) && aligned(p.B, 4) && p.lda * EB % 4 == 0 &&
                      p.ldb * EB % 4 == 0 && (p.groups == 1 || p.stride_b * EB % 4 == 0);
   if (dword)
@@ -192,15 +192,12 @@ int launch(const GroupedParams& p0, hipStream_t stream) {
   return hipGetLastError() == hipSuccess ? TLA_OK : TLA_ERR_HIP;
 }
 
-// 32 columns and four waves a workgroup, or, where that would leave compute
-// units without one, 16 columns and eight waves.
 template <int kCode>
 int pick(const GroupedParams& p, int mt, hipStream_t s) {
-  const int64_t wide = (p.rows < p.groups ? p.rows : p.groups) * (int64_t)((p.N + 31) / 32);
-  if (mt == 1 && wide <= 512) return launch<kCode, 1, 1, 8>(p, s);
-  if (mt == 1) return launch<kCode, 1, 2, 4>(p, s);
-  if (mt == 2) return wide <= 512 ? launch<kCode, 2, 1, 8>(p, s) : launch<kCode, 2, 2, 4>(p, s);
-  return wide <= 512 ? launch<kCode, 4, 1, 8>(p, s) : launch<kCode, 4, 2, 4>(p, s);
+  const bool narrow = few_rows_narrow(p.rows, p.groups, p.N);
+  if (mt == 1) return narrow ? launch<kCode, 1, 1, 8>(p, s) : launch<kCode, 1, 2, 4>(p, s);
+  if (mt == 2) return narrow ? launch<kCode, 2, 1, 8>(p, s) : launch<kCode, 2, 2, 4>(p, s);
+  return narrow ? launch<kCode, 4, 1, 8>(p, s) : launch<kCode, 4, 2, 4>(p, s);
 }
 
 }  // namespace

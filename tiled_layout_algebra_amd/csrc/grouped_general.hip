@@ -255,7 +255,7 @@ int launch_form(const GroupedParams& p0, hipStream_t stream) {
   const int64_t grid = kWgrad ? (int64_t)p.groups * p.tiles_m * p.tiles_n
                               : row_tiles_bound(p.rows, p.groups, 128) * p.tiles_n;
   if (grid <= 0) return TLA_OK;
-  if (grid > 0x7FFFFFFF) return TLA_ERR_UNSUPPORTED;
+  if (!grid_fits(grid, kThreads)) return TLA_ERR_UNSUPPORTED;
   hipLaunchKernelGGL((grouped_general_kernel<kCode, kBView, kWgrad, kLoose>), dim3((unsigned)grid),
                      dim3(kThreads), 0, stream, p);
   return hipGetLastError() == hipSuccess ? TLA_OK : TLA_ERR_HIP;

@@ -649,7 +649,7 @@ int launch(const GroupedParams& p0, hipStream_t stream) {
       : p.flags & kOpHalves ? row_tiles_bound(p.rows, p.groups, 128) * p.tiles_n
                             : row_tiles_bound(p.rows, p.groups, 256) * p.tiles_n + 256;
   if (grid <= 0) return TLA_OK;
-  if (grid > 0x7FFFFFFF) return TLA_ERR_UNSUPPORTED;
+  if (!grid_fits(grid, 512)) return TLA_ERR_UNSUPPORTED;
   hipLaunchKernelGGL((grouped_two_group_kernel<kCode, kForm>), dim3((unsigned)grid), dim3(512), 0,
                      stream, p);
   return hipGetLastError() == hipSuccess ? TLA_OK : TLA_ERR_HIP;

@@ -15,8 +15,10 @@ constexpr int type_bytes(int code) {
   return code == TLA_F32 ? 4 : (code == TLA_E4M3 || code == TLA_I8 ? 1 : 2);
 }
 
-// Threads that a launch's one dimension holds.
+// Threads that a launch's one dimension holds: the runtime takes a larger count
+// modulo 2^32 and reports nothing.
 constexpr int64_t kMaxThreads = 0xFFFFFFFF;
+constexpr bool grid_fits(int64_t blocks, int threads) { return blocks <= kMaxThreads / threads; }
 
 // One problem: rows r of A, grouped by expert (rows offsets[e] .. offsets[e +
 // 1] - 1 belong to expert e; offsets == nullptr: one expert with every row).
@@ -78,7 +80,12 @@ int launch_grouped_direct_shift(const GroupedParams& p, int type, int shape, hip
 int launch_wgrad_direct(const GroupedParams& p, int type, int shape, hipStream_t stream);
 
 // The kernel for few rows an expert (grouped_few_rows.hip): B K-contiguous,
-// any pitch and alignment; blocks of 16 mt rows, mt 1, 2 or 4.
+// any pitch and alignment; blocks of 16 mt rows, mt 1, 2 or 4, of 32 columns and
+// four waves, or, where that would leave compute units without one, 16 columns
+// and eight waves.
+inline bool few_rows_narrow(int64_t rows, int64_t groups, int64_t N) {
+  return (rows < groups ? rows : groups) * ((N + 31) / 32) <= 512;
+}
 int launch_grouped_few_rows(const GroupedParams& p, int type, int mt, hipStream_t stream);
 
 int launch_quantize_rows(int64_t M, int64_t K, const void* X, int type, int64_t ldx, int8_t* Q,

@@ -57,10 +57,30 @@ bool k_rows_fit(int64_t k, int64_t ld, int eb) {
   return ld <= (kLimit - 1) / ((k > 64 ? k : 64) * eb);
 }
 
+// Whether a launch holds the kernel's workgroups.
+bool launches(Kernel k, const tla_grouped_gemm_args* a) {
+  auto fits = [&](int64_t bm, int64_t bn, int threads, int64_t more) {
+    return grid_fits(row_tiles_bound(a->rows, a->groups, bm) * ((a->N + bn - 1) / bn) + more, threads);
+  };
+  const bool narrow = few_rows_narrow(a->rows, a->groups, a->N);
+  const int64_t few_n = narrow ? 16 : 32;
+  const int few_threads = narrow ? 512 : 256;
+  switch (k) {
+    case kFewRows1: return fits(16, few_n, few_threads, 0);
+    case kFewRows2: return fits(32, few_n, few_threads, 0);
+    case kFewRows4: return fits(64, few_n, few_threads, 0);
+    case kDirect64: case kDirect64Shift: return fits(64, 128, 256, 0);
+    case kDirect128: case kDirect128Shift: return fits(128, 128, 512, 0);
+    // half tiles throughout, or whole ones and fewer than 256 halves
+    case kTwoGroup: case kTwoGroupShift: return fits(128, 256, 512, 256);
+    default: return fits(128, 128, 256, 0);
+  }
+}
+
 // Whether a kernel takes the problem.
 bool takes(Kernel k, const tla_grouped_gemm_args* a, int eb, bool b_kc) {
   if (k == kGeneral) return true;
-  if (a->K == 0) return false;
+  if (a->K == 0 || !launches(k, a)) return false;
   if (k == kFewRows1 || k == kFewRows2 || k == kFewRows4) return b_kc;
   if (a->type == TLA_E4M3 && a->K < kMinKE4m3) return false;
   // 32-bit offsets within a tile's rows
@@ -209,6 +229,8 @@ int plan_product(const tla_grouped_gemm_args* a, Plan* out) {
   if ((a->N % 4 == 0 || a->groups == 1) && aligned_to(a->scale_b, 16) &&
       (!a->bias || aligned_to(a->bias, 4 * bb)))
     p.flags |= kOpVec4;
+  // no other kernel needs fewer threads than the one that takes everything
+  if (!launches(kGeneral, a)) return TLA_ERR_UNSUPPORTED;
   out->type = a->type;
   out->b_kc = b_kc;
   out->kernel = choose(a, eb, b_kc);

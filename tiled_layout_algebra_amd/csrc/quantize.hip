@@ -200,8 +200,7 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(const uint8_t* X, in
   }
 }
 
-// The rows in launches of fewer than 2^32 threads: the runtime takes a larger
-// count modulo 2^32 and reports nothing.
+// The rows in launches of fewer than 2^32 threads.
 template <int kCode, int kTpr, int kV>
 int launch(int64_t M, int64_t K, const void* X, int64_t ldx, int8_t* Q, int64_t ldq, float* scale,
            hipStream_t s) {
