@@ -10,6 +10,11 @@
 
 namespace tla {
 
+// Threads that a launch's one dimension holds: the runtime takes a larger count
+// modulo 2^32 and reports nothing.
+constexpr int64_t kMaxThreads = 0xFFFFFFFF;
+constexpr bool grid_fits(int64_t blocks, int threads) { return blocks <= kMaxThreads / threads; }
+
 // A validated GEMM problem, in the element units of each operand.
 struct GemmProblem {
   int64_t M, N, K;

@@ -15,11 +15,6 @@ constexpr int type_bytes(int code) {
   return code == TLA_F32 ? 4 : (code == TLA_E4M3 || code == TLA_I8 ? 1 : 2);
 }
 
-// Threads that a launch's one dimension holds: the runtime takes a larger count
-// modulo 2^32 and reports nothing.
-constexpr int64_t kMaxThreads = 0xFFFFFFFF;
-constexpr bool grid_fits(int64_t blocks, int threads) { return blocks <= kMaxThreads / threads; }
-
 // One problem: rows r of A, grouped by expert (rows offsets[e] .. offsets[e +
 // 1] - 1 belong to expert e; offsets == nullptr: one expert with every row).
 //   product            D[r, n] = epilogue(sum_k A[r, k] B_e(k, n))

@@ -159,14 +159,31 @@ struct alignas(16) B16 {
   uint64_t lo, hi;
 };
 
+// tm x tn tiles in bands that a launch of 256 threads a tile holds:
+// f(first tile row, first tile column, tile rows, tile columns).
+template <class F>
+int tile_bands(int64_t tm, int64_t tn, F&& f) {
+  if (tm * tn > 0x7FFFFFFF || tn > 0x7FFFFFFF) return TLA_ERR_UNSUPPORTED;
+  constexpr int64_t kMost = kMaxThreads / 256;
+  const int64_t cols = tn < kMost ? tn : kMost, rows = kMost / cols;
+  for (int64_t c = 0; c < tn; c += cols)
+    for (int64_t r = 0; r < tm; r += rows) {
+      f(r, c, tm - r < rows ? tm - r : rows, tn - c < cols ? tn - c : cols);
+      if (hipGetLastError() != hipSuccess) return TLA_ERR_HIP;
+    }
+  return TLA_OK;
+}
+
 template <typename T>
 int launch_general(const void* src, int64_t ld_src, void* dst, int64_t ld_dst, int64_t M, int64_t N,
                    hipStream_t s) {
-  const int64_t tm = (M + 31) / 32, tn = (N + 31) / 32;
-  if (tm * tn > 0x7FFFFFFF || tn > 0x7FFFFFFF) return TLA_ERR_UNSUPPORTED;
-  hipLaunchKernelGGL(transpose_tile32_kernel<T>, dim3((unsigned)(tm * tn)), dim3(256), 0, s,
-                     (const T*)src, ld_src, (T*)dst, ld_dst, M, N, (int)tn);
-  return hipGetLastError() == hipSuccess ? TLA_OK : TLA_ERR_HIP;
+  return tile_bands((M + 31) / 32, (N + 31) / 32, [&](int64_t r, int64_t c, int64_t tm, int64_t tn) {
+    const int64_t m = M - 32 * r, n = N - 32 * c;  // from the band's first tile on
+    hipLaunchKernelGGL(transpose_tile32_kernel<T>, dim3((unsigned)(tm * tn)), dim3(256), 0, s,
+                       (const T*)src + 32 * r * ld_src + 32 * c, ld_src,
+                       (T*)dst + 32 * c * ld_dst + 32 * r, ld_dst, m < 32 * tm ? m : 32 * tm,
+                       n < 32 * tn ? n : 32 * tn, (int)tn);
+  });
 }
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
@@ -174,14 +191,19 @@ bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 template <typename V>
 int launch_copy(const void* src, int64_t ld_src, void* dst, int64_t ld_dst, int64_t M,
                 int64_t row_len, hipStream_t s) {
-  const int64_t chunks = (row_len + 255) / 256;
-  if (chunks > 0x7FFFFFFF) return TLA_ERR_UNSUPPORTED;
-  // rows in batches of at most 65535, the grid's y limit
-  for (int64_t r0 = 0; r0 < M; r0 += 65535) {
-    const int64_t rows = M - r0 < 65535 ? M - r0 : 65535;
-    hipLaunchKernelGGL(copy_rows_kernel<V>, dim3((unsigned)chunks, (unsigned)rows), dim3(256), 0, s,
-                       (const V*)src + r0 * ld_src, ld_src, (V*)dst + r0 * ld_dst, ld_dst, row_len);
-    if (hipGetLastError() != hipSuccess) return TLA_ERR_HIP;
+  if ((row_len + 255) / 256 > 0x7FFFFFFF) return TLA_ERR_UNSUPPORTED;
+  // rows in batches of at most 65535, the grid's y limit, and of as many
+  // vectors as its x dimension has threads
+  constexpr int64_t kMost = kMaxThreads / 256 * 256;
+  for (int64_t c0 = 0; c0 < row_len; c0 += kMost) {
+    const int64_t len = row_len - c0 < kMost ? row_len - c0 : kMost;
+    for (int64_t r0 = 0; r0 < M; r0 += 65535) {
+      const int64_t rows = M - r0 < 65535 ? M - r0 : 65535;
+      hipLaunchKernelGGL(copy_rows_kernel<V>, dim3((unsigned)((len + 255) / 256), (unsigned)rows), dim3(256),
+                         0, s, (const V*)src + r0 * ld_src + c0, ld_src, (V*)dst + r0 * ld_dst + c0, ld_dst,
+                         len);
+      if (hipGetLastError() != hipSuccess) return TLA_ERR_HIP;
+    }
   }
   return TLA_OK;
 }
@@ -202,11 +224,13 @@ int transpose_dispatch(const void* src, int64_t ld_src, void* dst, int64_t ld_ds
     // (4x4 micro-tiles, 8 x 8 lanes, 128-byte runs both ways) peaked at
     // 5481 with 64 x 256 tiles.
     constexpr int TM = 256, TN = 64;
-    const int64_t tm = (M + TM - 1) / TM, tn = (N + TN - 1) / TN;
-    if (tm * tn > 0x7FFFFFFF) return TLA_ERR_UNSUPPORTED;
-    hipLaunchKernelGGL((transpose_lds_kernel<TM, TN>), dim3((unsigned)(tm * tn)), dim3(256), 0, s,
-                       (const uint32_t*)src, ld_src, (uint32_t*)dst, ld_dst, M, N, (int)tm);
-    return hipGetLastError() == hipSuccess ? TLA_OK : TLA_ERR_HIP;
+    return tile_bands((M + TM - 1) / TM, (N + TN - 1) / TN, [&](int64_t r, int64_t c, int64_t tm, int64_t tn) {
+      const int64_t m = M - TM * r, n = N - TN * c;
+      hipLaunchKernelGGL((transpose_lds_kernel<TM, TN>), dim3((unsigned)(tm * tn)), dim3(256), 0, s,
+                         (const uint32_t*)src + TM * r * ld_src + TN * c, ld_src,
+                         (uint32_t*)dst + TN * c * ld_dst + TM * r, ld_dst, m < TM * tm ? m : TM * tm,
+                         n < TN * tn ? n : TN * tn, (int)tm);
+    });
   }
   switch (eb) {
     case 1: return launch_general<uint8_t>(src, ld_src, dst, ld_dst, M, N, s);
