@@ -301,3 +301,22 @@ def test_launches_stay_below_2_to_32_threads():
     assert tla.lib().tla_grouped_gemm(ctypes.byref(_product(**many)), None) == tla.ERR_UNSUPPORTED
     w = dict(groups=1 << 24, rows=4, N=1, K=1, lda=1, ldy=1, ldd=1, stride_d=1)
     assert tla.lib().tla_grouped_gemm_wgrad(ctypes.byref(_wgrad(**w)), None) == tla.ERR_UNSUPPORTED
+
+
+def test_binding_refuses_strided_vectors():
+    """offsets, scales and bias have no stride argument, so a strided view would
+    be misread."""
+    t, f = torch.zeros(64), torch.zeros(8, 2)
+    call = lambda **kw: tla.grouped_gemm(  # noqa: E731
+        1, 1, 8, 8, kw.pop("offsets", None), None, tla.I8, 8, None, tla.COL_MAJOR, 8, 64, None, tla.BF16, 8, **kw)
+    for kw in (dict(offsets=torch.zeros(4, dtype=torch.int32)[::2]), dict(scale_a=f[:, 0]), dict(scale_b=f[:, 1]),
+               dict(bias=f[:, 0])):
+        with pytest.raises(ValueError, match="%s must be contiguous" % list(kw)[0]):
+            call(**kw)
+    with pytest.raises(ValueError, match="dbias must be contiguous"):
+        tla.grouped_gemm_wgrad(1, 1, 8, 8, None, None, 8, None, 8, tla.BF16, None, tla.F32, tla.ROW_MAJOR, 8, 64,
+                               dbias=f[:, 0])
+    with pytest.raises(ValueError, match="scale must be contiguous"):
+        tla.quantize_rows(8, 0, None, tla.F32, 0, None, 0, f[:, 0])
+    with pytest.raises(ValueError, match="bias must be contiguous"):
+        tla.gemm_i8(1, 8, 8, None, 8, None, tla.COL_MAJOR, 8, None, tla.BF16, 8, bias=t.view(8, 8)[:, 0])

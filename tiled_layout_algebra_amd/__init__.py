@@ -345,10 +345,11 @@ def _packed_call(name, args, stream, *more):
 _torch_types = {}
 
 
-def _ptr(t, what, kind=None):
+def _ptr(t, what, kind=None, dense=False):
     """Device address of a CUDA tensor, 0 for None; kind ("int32", "float32"):
-    the element type the library fixes for this buffer, so that another one is
-    refused, not misread."""
+    the element type the library fixes for this buffer.  Those buffers, and
+    dense ones, have no stride among the arguments: another type or a strided
+    view is refused, not misread."""
     if t is None:
         return 0
     if kind is not None:
@@ -358,6 +359,9 @@ def _ptr(t, what, kind=None):
             want = _torch_types[kind] = getattr(torch, kind)
         if t.dtype is not want:
             raise ValueError("%s must be a %s tensor" % (what, kind))
+        dense = True
+    if dense and not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % what)
     if not getattr(t, "is_cuda", False):
         raise ValueError("%s must be a CUDA tensor" % what)
     return t.data_ptr()
@@ -370,7 +374,7 @@ def _grouped_gemm_args(groups, rows, N, K, offsets, A, type, lda, B, b_order, ld
         groups, rows, N, K, _ptr(offsets, "offsets", "int32"), _ptr(A, "A"), type, lda,
         _ptr(B, "B"), b_order, ldb, stride_b, _ptr(D, "D"), d_type, ldd,
         _ptr(scale_a, "scale_a", "float32"), _ptr(scale_b, "scale_b", "float32"),
-        _ptr(bias, "bias"), d_type if bias_type is None else bias_type, _ptr(Z, "Z"), ldz, z_mode,
+        _ptr(bias, "bias", dense=True), d_type if bias_type is None else bias_type, _ptr(Z, "Z"), ldz, z_mode,
         act)
 
 
@@ -416,7 +420,7 @@ def gemm_i8(M, N, K, A, lda, B, b_order, ldb, D, d_type, ldd, scale_a=None, scal
     integer sums (tla_gemm_i8)."""
     a = _PACK_I8.pack(M, N, K, _ptr(A, "A"), lda, _ptr(B, "B"), b_order, ldb, _ptr(D, "D"), d_type,
                       ldd, _ptr(scale_a, "scale_a", "float32"), _ptr(scale_b, "scale_b", "float32"),
-                      _ptr(bias, "bias"), d_type if bias_type is None else bias_type, act)
+                      _ptr(bias, "bias", dense=True), d_type if bias_type is None else bias_type, act)
     _packed_call("tla_gemm_i8", a, _stream(stream, A, B, D))
 
 
