@@ -320,3 +320,22 @@ def test_binding_refuses_strided_vectors():
         tla.quantize_rows(8, 0, None, tla.F32, 0, None, 0, f[:, 0])
     with pytest.raises(ValueError, match="bias must be contiguous"):
         tla.gemm_i8(1, 8, 8, None, 8, None, tla.COL_MAJOR, 8, None, tla.BF16, 8, bias=t.view(8, 8)[:, 0])
+
+
+def test_expert_layer_refuses_what_it_would_misread():
+    from tiled_layout_algebra_amd.expert_layer import ExpertLayer
+    t = lambda *shape, dtype=torch.bfloat16: torch.zeros(*shape, dtype=dtype)  # noqa: E731
+    W1, b1, W2 = t(2, 8, 16), t(2, 16), t(2, 16, 8)
+    for bad in ((W1, b1, t(2, 8, 16)), (W1, b1.float(), W2), (W1, b1, t(2, 8, 16).transpose(1, 2)),
+                (t(2, 16, 8).transpose(1, 2), b1, W2)):
+        with pytest.raises(ValueError, match="contiguous bfloat16"):
+            ExpertLayer(*bad)
+    layer, off = ExpertLayer(W1, b1, W2), torch.tensor([0, 2, 3], dtype=torch.int32)
+    for x in (t(3, 9), t(3, 16)[:, :8], t(3, 8, dtype=torch.float16), t(8, 3).t()):
+        for call in (layer.forward, layer.decode):
+            with pytest.raises(ValueError, match="x must be"):
+                call(x, off)
+    saved = (t(3, 8), t(3, 16), t(3, 16), off)
+    for dy in (t(1, 8).expand(3, 8), t(3, 8, dtype=torch.float32), t(2, 8)):
+        with pytest.raises(ValueError, match="dy must be"):
+            layer.backward(dy, saved)

@@ -19,19 +19,30 @@ import sys
 import tiled_layout_algebra_amd as tla
 
 
+def _check(t, what, shape):
+    """Refuses what the calls below, which take dense bf16, would misread."""
+    import torch
+    if t.dtype is not torch.bfloat16 or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous bfloat16 tensor of shape %s" % (what, list(shape)))
+
+
 class ExpertLayer:
     """Weights W1 [experts, width, hidden], b1 [experts, hidden] and W2
-    [experts, hidden, width], bf16 CUDA tensors, stored [K, N] for their own
-    forward product."""
+    [experts, hidden, width], contiguous bf16 CUDA tensors, stored [K, N] for
+    their own forward product."""
 
     def __init__(self, W1, b1, W2):
         self.W1, self.b1, self.W2 = W1, b1, W2
-        self.experts, self.width, self.hidden = W1.shape
+        self.experts, self.width, self.hidden = g, w, h = tuple(W1.shape)
+        _check(W1, "W1", (g, w, h))
+        _check(b1, "b1", (g, h))
+        _check(W2, "W2", (g, h, w))
 
     def forward(self, x, offsets):
         """y and what the backward pass needs.  x [rows, width] sorted by
         expert, offsets int32 [experts + 1]."""
         import torch
+        _check(x, "x", (x.shape[0], self.width))
         g, w, h, rows = self.experts, self.width, self.hidden, x.shape[0]
         act, z = (torch.empty(rows, h, dtype=x.dtype, device=x.device) for _ in range(2))
         y = torch.empty(rows, w, dtype=x.dtype, device=x.device)
@@ -46,6 +57,7 @@ class ExpertLayer:
         """dx and the gradients (fp32) dW1, db1, dW2."""
         import torch
         x, act, z, offsets = saved
+        _check(dy, "dy", tuple(x.shape))
         g, w, h, rows = self.experts, self.width, self.hidden, x.shape[0]
         dz = torch.empty(rows, h, dtype=x.dtype, device=x.device)
         dx = torch.empty_like(x)
@@ -81,6 +93,7 @@ class ExpertLayer:
     def decode(self, x, offsets):
         """y in int8: tokens quantized, both products with their scales."""
         import torch
+        _check(x, "x", (x.shape[0], self.width))
         g, w, h, rows = self.experts, self.width, self.hidden, x.shape[0]
         for k, n, (W, s), bias, act in ((w, h, self.q1, self.b1, tla.ACT_GELU),
                                         (h, w, self.q2, None, tla.ACT_NONE)):
