@@ -121,3 +121,22 @@ def test_wide_pitches_with_few_rows():
                          tla.BF16, n)
         ref, s = X.double() @ m.double(), X.double().abs() @ m.double().abs()
         check(P.cpu(), ref, s * eps + half_step(ref.abs() + s * eps, tla.BF16), "product")
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+@ORDERS
+@pytest.mark.parametrize("kind", [tla.BF16, tla.F16])
+@pytest.mark.parametrize("d_type", [tla.F32, tla.BF16, tla.F16])
+def test_results_of_each_kernel(kernel, order, kind, d_type):
+    """Every result type from every kernel, extents off the tile and off a
+    chunk, D's rows pitched at any element."""
+    experts, least, shift = KERNELS[kernel]
+    Gradient(counts_of(experts), least + 74, least + 53, kind, seed=1).verify(d_type, order, 3, 6, shift, pad_d=5)
+    Gradient(counts_of(experts), least + 64, least + 72, kind, seed=2).verify(d_type, order, 0, 0, shift)
+
+
+@ORDERS
+@pytest.mark.parametrize("kind,d_type", [(tla.BF16, tla.F32), (tla.F16, tla.F32), (tla.F16, tla.F16)])
+def test_two_group_tiles_filled(order, kind, d_type):
+    """280 tiles of 256 x 256 over whole and ragged ones, rows pitched on dwords."""
+    Gradient([333, 0, 1000, 1], 1550, 2314, kind, seed=3).verify(d_type, order, 6, 2, pad_d=2)

@@ -1,9 +1,11 @@
-"""More columns than the workgroups of a one-dimensional launch of every kernel
-reach: each call is right or refused, and the library's own choice is right."""
+"""Products over more columns than the workgroups of a one-dimensional launch of
+every kernel reach: each call is right or refused, and the library's own choice
+is right; and 8-bit [K, N] weights over many tiles."""
 import pytest
 import torch
 
 import tiled_layout_algebra_amd as tla
+from tests.grouped_util import Product
 
 pytestmark = pytest.mark.gpu
 
@@ -24,3 +26,10 @@ def test_a_token_times_half_a_billion_columns():
         else:
             tla.grouped_gemm(*args, variant=variant)
             assert (d == K).all(), variant
+
+
+@pytest.mark.parametrize("kind", [tla.E4M3, tla.I8], ids=["e4m3", "i8"])
+def test_8_bit_weights_stored_k_by_n_over_many_tiles(kind):
+    for z in (tla.Z_STORE, tla.Z_GRAD):
+        Product([1500, 0, 2100, 777], 2312, 320, kind, order=tla.ROW_MAJOR, bias=z == tla.Z_STORE,
+                act=tla.ACT_GELU, z=z, seed=7).call().verify()
