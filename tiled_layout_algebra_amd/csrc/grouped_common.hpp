@@ -169,7 +169,9 @@ __device__ __forceinline__ float abs16(float y) {
 // of degree 6, is the fit of log2 h on [0, 6.5] that has the least largest error
 // in h (fitted here by reweighted least squares); beyond, P keeps falling faster
 // than log2 h, so h is cut off early where it no longer counts.  |Phi - exact| <=
-// 1.5e-7 in fp32.  14 operations' time (56 cycles a wave), the hardware exp2
+// 1.5e-7, so GELU is off by 1.5e-7 |y| and a rounding; for y << 0, where it gets
+// small itself, that is 3e-5 of the value down to y = -3, 0.25 % at -4, 2.1 % at -5 (-1.4e-6)
+// and 8.9 % at -6 (-5.9e-9).  14 operations' time (56 cycles a wave), the hardware exp2
 // among them; a rational erfc with its reciprocal took 21 (84) at 3e-7.  The
 // epilogue applies it to 128 values a lane: int8 3001 x 4096 x 4096 with bias and
 // GELU 61.8 -> 60.4 us, 8192^3 487 -> 482, and one row, which shares the code's
@@ -186,8 +188,8 @@ __device__ __forceinline__ float gelu_nan(float y) {
 }
 // d/dz z Phi(z) = Phi(z) + z phi(z) = g for z < 0 and 1 - g otherwise, g = h - |z|
 // phi(z) = e^(-z^2/2) R(|z|): R, of degree 9, is the fit of erfcx(|z| / sqrt 2) / 2
-// - |z| / sqrt(2 pi) on [0, 6] with the least largest error in g.  |g - exact| <=
-// 3.2e-7 in fp32.
+// - |z| / sqrt(2 pi) on [0, 6] with the least largest error in g.  In fp32 g is off
+// by at most 3.2e-7, and 1 - g, rounded once more, by 3.6e-7.
 __device__ __forceinline__ float gelu_slope(float z) {
   const float a = abs16(z), b = a * 0.8493218003f;  // |z| sqrt(log2(e) / 2)
   float r = fmaf(a, -8.06307162e-06f, 0.000151941887f);
@@ -454,9 +456,9 @@ __device__ __forceinline__ void wgrad_epilogue(const GroupedParams& p, int e, in
 // operand every result of lane l is the sum of that lane's four values: two of
 // them a fragment, and a line never meets another one, whose infinity or NaN (a
 // neighbour's, or the padding's behind the last column) stays in its own sum.
-// Half the time of one 32x32 instruction a fragment, four registers each.
-// One block of tiles along the other extent does it: next to a pass
-// over dY of its own (26 us of 553 for 16384 rows of 4096) it reads nothing.
+// Four registers a fragment.  One block of tiles along the other extent does it:
+// 516 us instead of 505 for 16384 rows on 8 experts of 4096 x 4096, where a pass
+// over dY of its own took 26; it reads nothing more.
 template <int kCode, int kN>
 struct LineSums {
   f32x4 s[kN];

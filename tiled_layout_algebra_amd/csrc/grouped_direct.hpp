@@ -13,9 +13,9 @@
 // Bound by LDS reads (a 64 x 32 wave tile reads three 16-byte fragments for two
 // MFMAs: about 1020 of a k-tile's 1190 cycles) or, with few rows an expert, by
 // the weights' way from memory.  Measured: bf16, 4096 rows on 32 experts of
-// 2048 x 4096 151 us (128 x 128; 537 MB of weights: 3.7 TB/s), 2048 rows 132 us
-// (64 x 128), int8 512 rows x 4096 x 4096 17 us; kNKShift, 4096 rows 2048 x 4095
-// 247 us (its dword loads and copies across two lines cost the difference);
+// 2048 x 4096 151 us (128 x 128; 537 MB of weights: 3.6 TB/s), 2048 rows 117 us
+// (64 x 128; 4.6 TB/s), int8 512 rows x 4096 x 4096 17 us; kNKShift, 4096 rows 2048 x
+// 4095 241 us (its dword loads and copies across two lines cost the difference);
 // 777 rows' fp32 gradients on 16 experts of 512 x 1024 12 us (33.5 MB written).
 #pragma once
 

@@ -13,10 +13,11 @@
 // Weights of 8 bits are read as they are: int8 goes to the integer
 // instruction, e4m3 is widened to f16, which holds it exactly.
 //
-// Bound by memory.  Measured: bf16, 128 rows on 32 experts of 2048 x 4096 107 us
-// (537 MB of weights: 5.0 TB/s, what a copy reaches), two rows on two experts of
-// 4096 x 4096 12-14 us (67 MB: 5 TB/s); one int8 row x 4096 x 4096 6.5 us, of which
-// about 4 are a launch's.
+// Bound by memory.  Measured: bf16, 128 rows on 32 experts of 2048 x 4096 110 us
+// (537 MB of weights: 4.9 TB/s; a large copy reaches 6.7, reads and writes together),
+// two rows on two experts of 4096 x 4096 12-13.6 us (67 MB: 5 TB/s and more); one
+// row x 4096 x 4096 6.3 us in int8 and in e4m3, of which about 4 are a launch's; 128
+// e4m3 rows on the 32 experts 43 us.
 #include "grouped_common.hpp"
 
 namespace tla {
@@ -54,8 +55,8 @@ struct Step16<kE4M3> {
 
 // Sixteen bytes of a row.  kDword: rows start on dwords, one load.  Otherwise
 // the dword-aligned sixteen bytes and the dword after them, shifted into place
-// when they are used: loads at other addresses take twice as long (128 bf16
-// rows on 32 experts of 2048 x 4095: 243 us unaligned).
+// when they are used (128 bf16 rows on 32 experts of 2048 x 4095: 163 us so, 243
+// with loads at the rows' own addresses).
 template <bool kDword>
 struct Chunk {
   i32x4 v;

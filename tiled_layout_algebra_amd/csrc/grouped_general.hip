@@ -19,7 +19,9 @@
 //
 // Bound by LDS (fragment reads and the staged writes) at one workgroup's share
 // of two a compute unit.  Measured: bf16, 16384 rows on 8 experts, [K, N] weights
-// of 4095 x 4095 1030 us, the weight gradient 4095 x 4095 1220 us.
+// of 4095 x 4095 1075 us, the weight gradient 4095 x 4095 1085 us; 4096 rows x 4096 x
+// 4096 with 8-bit [K, N] weights, a byte a load, 311 us in int8 and 342 in e4m3; 4096
+// e4m3 rows on 8 experts of 4096 x 256 28 us.
 #include "grouped_common.hpp"
 
 namespace tla {

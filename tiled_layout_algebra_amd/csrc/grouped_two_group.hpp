@@ -29,13 +29,15 @@
 //             three MFMA steps a period instead of four.
 //
 // Bound by the matrix cores (busy 0.72 of the time in the int8 case below, at
-// the clock that leaves).  Measured: bf16, 16384 rows, one expert of 4096 x 4096
-// 407 us = 1350 TFLOP/s, [K, N] weights 411 us; the same rows over 8 experts
-// with GELU, bias and the pre-activation kept 540 us, the input gradient with
-// GELU's derivative 521 us, the weight gradient 557 us (a tile's epilogue writes
-// 128 KiB, 256 KiB with the pre-activation, and every compute unit does so at
-// once); int8 8192^3 with bias and GELU 460 us = 2390 TOP/s; kNKShift on 8
-// experts of 4096 x 4095 718 us.  A round of tiles that fills part of the card
+// the clock that leaves).  Measured, calls in a row on the same buffers; boxes
+// differ by up to 8 %: bf16, 16384 rows, one expert of 4096 x 4096 423 us = 1300
+// TFLOP/s, [K, N] weights 421 us; the same rows over 8 experts with GELU, bias and
+// the pre-activation kept 546 us, the input gradient of 16001 rows with GELU's
+// derivative 557 us, the weight gradient 516 us in bf16 (618 where every call finds
+// other buffers) and 587 in fp32 (a tile's epilogue writes 128 KiB, 256 KiB with the
+// pre-activation or in fp32, and every compute unit does so at once); 8192^3 with
+// bias and GELU 472 us = 2330 TOP/s in int8, 411 us = 2670 TFLOP/s in e4m3; kNKShift
+// on 8 experts of 4096 x 4095 720 us.  A round of tiles that fills part of the card
 // costs most of a whole one: see two_group_lookup.
 #pragma once
 

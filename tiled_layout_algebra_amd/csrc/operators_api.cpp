@@ -113,19 +113,19 @@ double two_group_rounds(const tla_grouped_gemm_args* a, bool halves) {
   return whole + (last < 1.0 ? last : 1.0);
 }
 
-// The kernel with the smallest estimated time (us).  No kernel reads the
-// weights faster than 5.0 TB/s.  Measured with [N, K] weights of 4096 x 4096
+// The kernel with the smallest estimated time (us).  These kernels read the
+// weights at 5.0 TB/s at most.  Measured with [N, K] weights of 4096 x 4096
 // int8 (32 k-tiles of 128 bytes), one expert, M rows:
 //      M     few 16   few 32   few 64   64x128   128x128   256x256
-//      1       6.7      6.9      8.1     13.6      15.9      30.4
-//     32      11.0      9.4     10.8     14.3      16.1      30.7
-//     64      19.2     14.4     13.3     14.8      16.4      31.2
-//    512       125       90       75     17.2      18.7      39.6
-//   2048                                 50.0      46.5      43.8
-//   3001                                 74.6      68.0      54.0
-// and in bf16 for 32 experts of 2048 x 4096: 128 rows 107 (few 16), 111
-// (64x128), 4096 rows 178 (64x128), 151 (128x128), 192 (256x256); for 8
-// experts of 4096 x 4096 with 2000 rows 136, 127, 96.
+//      1       6.3      6.7      7.4     12.8      15.5      23.6
+//     32      10.5      9.0     10.1     13.0      15.6      24.3
+//     64      19.0     14.5     12.8     13.3      16.0      24.6
+//    512       118       88       75     16.7      19.0      27.3
+//   2048       453      340      286     51.3      45.8      40.5
+//   3001       662      497      416     78.8      67.2      55.4
+// and in bf16 for 32 experts of 2048 x 4096: 128 rows 110 (few 16), 123
+// (64x128), 4096 rows 174 (64x128), 144 (128x128), 147 (256x256); for 8
+// experts of 4096 x 4096 with 2000 rows 129, 123, 89.
 Kernel choose(const tla_grouped_gemm_args* a, int eb, bool b_kc) {
   const double live = (double)(a->rows < a->groups ? a->rows : a->groups);
   const double matrix = (double)a->N * (double)a->K * eb * 1e-6;  // MB
@@ -158,9 +158,9 @@ Kernel choose(const tla_grouped_gemm_args* a, int eb, bool b_kc) {
   const double mixed = two_group_rounds(a, false), halved = two_group_rounds(a, true);
   const double two = mixed < halved ? mixed : halved;
   consider(kTwoGroup, at_least(4.0 + 1.2 * weights, 5.0 + kt * 1.6 * two));
-  // any alignment: with B 4096 x 4095 int8, 3001 rows: 121 us (64 rows), 99
-  // (128), 68 (256), 115 (general); with 988 x 2371, 400 rows 18, 23, 40, 33;
-  // bf16, 4096 rows on 32 experts of 2048 x 4095: 305, 247, 285, 269
+  // any alignment: with B 4096 x 4095 int8, 3001 rows: 122 us (64 rows), 99
+  // (128), 69 (256), 99 (general); with 988 x 2371, 400 rows 16, 18, 29, 28;
+  // bf16, 4096 rows on 32 experts of 2048 x 4095: 324, 241, 254, 234
   const double kt96 = (double)(a->K * eb / 96 + 1);
   consider(kDirect64Shift, 4.5 + kt * at_least(0.6, (eb == 1 ? 0.0024 : 0.0032) * t64));
   consider(kDirect128Shift, 4.8 + kt * 0.96 * rounds(t128));
@@ -262,8 +262,8 @@ int run_product(const tla_grouped_gemm_args* a, hipStream_t stream, int forced =
     case kDirect128: {
       if (plan.b_kc) return launch_grouped_direct(p, t, kDirect128x3, stream);
       // three stages while every workgroup has a compute unit of its own (500
-      // rows on 4 experts of 1024 x 1024: 10.6 us against 15.9 with two), two
-      // stages and two workgroups a unit beyond (16000 rows: 49 against 57)
+      // rows on 4 experts of 1024 x 1024: 10.2 us against 12.2 with two), two
+      // stages and two workgroups a unit beyond (16000 rows on 8: 57 against 63)
       const int64_t blocks = row_tiles_bound(p.rows, p.groups, 128) * ((p.N + 127) / 128);
       return launch_grouped_direct_kn(p, t, blocks <= 256 ? kDirect128x3 : kDirect128x2, stream);
     }
@@ -365,10 +365,10 @@ int tla_grouped_gemm_wgrad(const tla_grouped_wgrad_args* a, void* stream) {
   const bool direct = dword_rows(a->A, a->lda, 2) && dword_rows(a->Y, a->ldy, 2) &&
                       k_rows_fit(a->rows, a->lda, 2) && k_rows_fit(a->rows, a->ldy, 2);
   // 256 x 256 tiles when they give every compute unit one (8000 rows on 16
-  // experts of 2048 x 2048: 82 us against 101 for 128 x 128); below, 128 x 128
-  // with two stages (777 rows, 16 experts of 512 x 1024: 17.2 us against 22.6
-  // and 18.5 with three), three stages when they all fit at once (1000 rows, 2
-  // experts of 1024 x 1024: 8.1 against 9.5)
+  // experts of 2048 x 2048: 105 us against 124 for 128 x 128); below, 128 x 128
+  // with two stages (777 rows, 16 experts of 512 x 1024: 11.7 us against 17.0
+  // and 13.5 with three), three stages when they all fit at once (1000 rows, 2
+  // experts of 1024 x 1024: 9.0 against 10.7)
   const int64_t tiles = a->groups * ((a->K + 255) / 256) * ((a->N + 255) / 256);
   const int64_t tiles128 = a->groups * ((a->K + 127) / 128) * ((a->N + 127) / 128);
   if (direct && tiles >= 256) return launch_wgrad_two_group(p, a->type, (hipStream_t)stream);

@@ -17,8 +17,8 @@
 // the fused multiply-add gives it exactly, and comparing it with s/2 rounds as
 // the true quotient does.
 //
-// Measured: 16384 x 8191 bf16 75 us (403 MB: 5.4 TB/s), 12608 x 811 fp32 11 us,
-// 64 x 4096 bf16 4.5 us (a launch).
+// Measured: 16384 x 8191 bf16 76 us (403 MB: 5.3 TB/s), 12608 x 811 fp32 11 us,
+// 64 x 4096 bf16 4.4 us (a launch).
 #include "grouped_common.hpp"
 
 namespace tla {
