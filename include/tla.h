@@ -2,7 +2,8 @@
  * tla.h -- C ABI of libtla.so: a layout-algebra-driven tiled GEMM with a
  * fused epilogue, a layout-driven tiled transpose, and a device evaluator
  * of shape/stride layouts, for AMD Instinct MI355X (gfx950 / CDNA4); and
- * products of rows grouped by expert, an int8 product and a quantizer.
+ * products of rows grouped by expert, gated feed-forward products, int8 and
+ * block-scaled e4m3 products and their quantizers.
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -71,7 +72,8 @@ typedef enum { TLA_ROW_MAJOR = 0, TLA_COL_MAJOR = 1 } tla_order;
 typedef enum {
   TLA_ACT_NONE = 0,
   TLA_ACT_RELU = 1, /* max(y, 0)                                        */
-  TLA_ACT_GELU = 2  /* y * Phi(y), the erf form                         */
+  TLA_ACT_GELU = 2, /* y * Phi(y), the erf form                         */
+  TLA_ACT_SILU = 3  /* y / (1 + e^-y): gated and block-scaled products  */
 } tla_act;
 
 /* -------------------------------------------------------------- GEMM */
@@ -320,6 +322,130 @@ int tla_gemm_i8(const tla_gemm_i8_args *args, void *stream);
  */
 int tla_quantize_rows(int64_t M, int64_t K, const void *X, int32_t x_type, int64_t ldx, void *Q,
                       int64_t ldq, float *scale, void *stream);
+
+/* --------------------------------------- gated feed-forward products */
+/*
+ * The first half of a gated feed-forward layer, for rows grouped by expert as
+ * in tla_grouped_gemm (offsets NULL with groups == 1: a dense layer):
+ *   g[r, n] = sum_k X[r, k] Wg_e(k, n) + b_gate[e, n]
+ *   u[r, n] = sum_k X[r, k] Wu_e(k, n) + b_up[e, n]
+ *   H[r, n] = act(g) u,  and Z_gate = g, Z_up = u unless these are NULL
+ * Wg_e and Wu_e start stride_w elements after the expert's before and are K x N
+ * in w_order with pitch ldw (TLA_COL_MAJOR: stored [N, K]); they may be halves
+ * of one buffer ([2 N, K], or [K, 2 N] with ldw = 2 N), and so may Z_gate and
+ * Z_up (ldz = 2 N).
+ *
+ * type F16 or BF16: any order, pitch and alignment to the element; the scales
+ * are NULL.  type E4M3, with block scales as in tla_gemm_blocks: scale_x of X's
+ * rows, scale_gate and scale_up of each 128 x 128 block, TLA_COL_MAJOR weights
+ * only.  H, Z: F16 or BF16 (h_type), row-major.  Biases (groups x N, dense, or
+ * NULL) F16, BF16 or F32.  act: any of tla_act.  Sums and the epilogue are fp32,
+ * each output is rounded once.  SiLU is z times the sigmoid, so SiLU(-inf) is
+ * NaN; the sigmoid is off by at most (|z| + 4) 2^-24 of its value and is 0 below
+ * 2^-126, GELU as said for tla_grouped_gemm.
+ *
+ * groups, rows or N == 0 is a no-op, K == 0 gives g = b_gate, u = b_up.  Offsets,
+ * extents (2 N in the place of N), padding, aliasing and rows of no expert as for
+ * tla_grouped_gemm.
+ */
+typedef struct {
+  int64_t groups, rows, N, K;
+  const int32_t *offsets;
+  const void *X; int32_t type; int64_t ldx;
+  const void *W_gate, *W_up; int32_t w_order; int64_t ldw, stride_w;
+  void *H; int32_t h_type; int64_t ldh;
+  const void *b_gate, *b_up; int32_t bias_type;
+  void *Z_gate, *Z_up; int64_t ldz;
+  const float *scale_x; int32_t sx_order; int64_t ldsx;
+  const float *scale_gate, *scale_up; int32_t sw_order; int64_t ldsw, stride_sw;
+  int32_t act; /* tla_act */
+} tla_gated_gemm_args;
+
+int tla_gated_gemm(const tla_gated_gemm_args *args, void *stream);
+
+/*
+ * Its backward pass up to the projections' outputs, from the gradient dY of the
+ * layer's output and the matrix W_e (K x N in w_order) that takes it back to the
+ * hidden layer, the down projection read in the other order:
+ *   dh[r, n] = sum_k dY[r, k] W_e(k, n)             (never stored)
+ *   dZ_gate = dh u act'(g),  dZ_up = dh act(g),  H = act(g) u unless NULL
+ * with g = Z_gate, u = Z_up as the forward pass kept them, in d_type like the
+ * outputs.  act' of tla_grouped_gemm; SiLU': p + z p (1 - p), p the sigmoid; 1
+ * without an activation.  H lets a program drop the hidden layer after the
+ * forward pass; it is what the down projection's weight gradient reads.
+ * The rest of the backward pass: dX = dZ_gate Wg^T + dZ_up Wu^T (one product
+ * where they are halves of a buffer), the weight and bias gradients
+ * tla_grouped_gemm_wgrad.
+ * type (dY and W) F16 or BF16.  Outputs must not overlap each other or an input.
+ * K == 0 gives dh = 0.  The rest as above, with N columns in the extents.
+ */
+typedef struct {
+  int64_t groups, rows, N, K;
+  const int32_t *offsets;
+  const void *dY; int32_t type; int64_t ldy;
+  const void *W; int32_t w_order; int64_t ldw, stride_w;
+  const void *Z_gate, *Z_up; int64_t ldz;
+  void *dZ_gate, *dZ_up; int32_t d_type; int64_t ldd;
+  void *H; int64_t ldh;
+  int32_t act; /* tla_act */
+} tla_gated_grad_args;
+
+int tla_gated_gemm_grad(const tla_gated_grad_args *args, void *stream);
+
+/* ------------------------------------------- block-scaled e4m3 product */
+/*
+ * D[r, n] = act( sum_k sa[r, k / 128] A[r, k] sb_e[n / 128, k / 128] B_e[n, k]
+ *                + bias[e, n] )
+ * for rows grouped by expert as in tla_grouped_gemm.  A: rows x K row-major
+ * e4m3; B_e: stored [N, K] with pitch ldb, stride_b elements after the expert's
+ * before.  scale_a: rows x ceil(K / 128) fp32 in sa_order with pitch ldsa
+ * (TLA_COL_MAJOR: rows together, which the kernels read best); scale_b:
+ * ceil(N / 128) x ceil(K / 128) in sb_order with pitch ldsb for each expert,
+ * stride_sb elements apart.  The last block of K and of N may be short.  D F16
+ * or BF16; bias (groups x N, dense, or NULL) F16, BF16 or F32; act any of
+ * tla_act.
+ * A block's products are summed by the 8-bit matrix instruction, which loses
+ * what lies below about 2^-14.3 of the largest; that sum times both scales is
+ * added in fp32.  With few rows they are summed exactly instead.
+ * Extents, offsets, padding, aliasing and no-ops as for tla_grouped_gemm; rows
+ * that do not start on dwords run at the few-row kernel's rate.
+ */
+typedef struct {
+  int64_t groups, rows, N, K;
+  const int32_t *offsets;
+  const void *A; int64_t lda;
+  const float *scale_a; int32_t sa_order; int64_t ldsa;
+  const void *B; int64_t ldb, stride_b;
+  const float *scale_b; int32_t sb_order; int64_t ldsb, stride_sb;
+  void *D; int32_t d_type; int64_t ldd;
+  const void *bias; int32_t bias_type;
+  int32_t act; /* tla_act */
+} tla_gemm_blocks_args;
+
+int tla_gemm_blocks(const tla_gemm_blocks_args *args, void *stream);
+
+/*
+ * e4m3 codes and a scale for each block of block_rows (1 or 128) x 128 values of
+ * X (M x K row-major, F16, BF16 or F32, pitch ldx):
+ *   scale[b] = max |X| / 448                       (fp32, correctly rounded)
+ *   Q = X / scale to the nearest e4m3 value, ties to even
+ * exactly (the quotient is rounded as if it were known to all digits; at most
+ * +-448).  scale: ceil(M / block_rows) x ceil(K / 128) in s_order with pitch lds;
+ * the last blocks may be short.  A block of zeros, or one whose scale rounds to
+ * 0, gets zero codes; so does a block with an infinity or a NaN, whose scale is
+ * that infinity or NaN.  Q: row-major, pitch ldq >= K, any alignment; its padding
+ * is not written.  M or K == 0 is a no-op; M and K at most 2^31 - 4096.
+ */
+int tla_quantize_blocks(int64_t M, int64_t K, const void *X, int32_t x_type, int64_t ldx,
+                        int32_t block_rows, void *Q, int64_t ldq, float *scale, int32_t s_order,
+                        int64_t lds, void *stream);
+
+/* These products on the kernel asked for (ids of tla_grouped_gemm_run_variant, 0
+ * to 6, of which the gradient has 0 to 3 and e4m3 1 to 6), with the same
+ * semantics, or TLA_ERR_UNSUPPORTED where that kernel does not take the problem. */
+int tla_gated_gemm_run_variant(const tla_gated_gemm_args *args, int32_t variant, void *stream);
+int tla_gated_gemm_grad_run_variant(const tla_gated_grad_args *args, int32_t variant, void *stream);
+int tla_gemm_blocks_run_variant(const tla_gemm_blocks_args *args, int32_t variant, void *stream);
 
 /* --------------------------------------------------------- transpose */
 /*

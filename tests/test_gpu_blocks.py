@@ -1,0 +1,115 @@
+"""The block-scaled e4m3 product, plain and gated, on the GPU: every kernel by
+name over odd sizes, short last blocks, orders of the scales, pitches and
+alignments with poisoned padding.  Bounds: tests/gated_util.py."""
+import pytest
+import torch
+
+import tiled_layout_algebra_amd as tla
+from tests.gated_util import VARIANTS, Blocks, Gated, raw
+
+pytestmark = pytest.mark.gpu
+KERNELS = ["two_group", "direct128", "direct64", "few64", "few32", "few16"]
+SHAPES = [
+    ([1], 16, 128, 0),
+    ([37], 130, 72, 4),
+    ([300], 264, 1040, 16),
+    ([5, 0, 131, 1], 200, 200, 8),
+    ([256, 130, 0], 129, 388, 0),
+    ([0, 0, 70], 390, 16, 16),
+]
+
+
+@pytest.mark.parametrize("variant", KERNELS)
+@pytest.mark.parametrize("shape", range(len(SHAPES)))
+def test_every_kernel(variant, shape):
+    counts, N, K, pad = SHAPES[shape]
+    Blocks(counts, N, K, d_type=shape % 2, bias=shape in (1, 3), act=(0, 3, 2, 1, 0, 0)[shape],
+           pad=pad, lost=shape % 2 * 3, a_order=shape % 2, b_order=shape % 3 % 2,
+           seed=shape).call(variant=VARIANTS[variant]).verify()
+
+
+@pytest.mark.parametrize("variant", KERNELS)
+@pytest.mark.parametrize("shape", range(len(SHAPES)))
+def test_gated_every_kernel(variant, shape):
+    counts, N, K, pad = SHAPES[shape]
+    Gated(counts, N, K, tla.E4M3, h_type=shape % 2, bias=(shape in (1, 3), shape in (1, 4)),
+          act=(3, 2, 1, 3, 0, 3)[shape], pad=pad, lost=shape % 2 * 3, keep=shape % 3 == 0,
+          x_order=shape % 2, w_order=shape % 3 % 2, seed=shape).call(variant=VARIANTS[variant]).verify()
+
+
+@pytest.mark.parametrize("rows,K,pad,shift", [(3, 77, 0, 0), (90, 301, 1, 1), (20, 128, 3, 2), (5, 1, 0, 1),
+                                              (2, 129, 0, 3)])
+def test_rows_at_any_byte(rows, K, pad, shift):
+    """Rows off a dword take the few-row kernel, whatever their number."""
+    b = Blocks([rows, 0, 2], 50, K, pad=pad, shift=0)
+    b.call()
+    b.exact_sums = True
+    b.verify()
+    for name in ("few16", "few32", "few64"):
+        b = Blocks([rows, 0, 2], 50, K, pad=pad).call(variant=VARIANTS[name])
+        b.verify()
+    g = Gated([rows, 0, 2], 50, K, tla.E4M3, pad=pad).call()
+    g.exact_sums = True
+    g.verify()
+
+
+@pytest.mark.parametrize("rows", [1, 16, 40, 100, 300, 1000])
+def test_the_librarys_choice(rows):
+    Blocks([rows], 520, 640, no_offsets=True, bias=True, act=tla.ACT_GELU).call().verify()
+    Gated([rows], 264, 640, tla.E4M3, no_offsets=True).call().verify()
+
+
+def test_no_k():
+    Blocks([40], 24, 0, bias=True).call().verify()
+    Gated([40], 24, 0, tla.E4M3, bias=(True, True)).call().verify()
+
+
+@pytest.mark.parametrize("variant", KERNELS)
+def test_a_scale_reaches_its_block_alone(variant):
+    """An infinite scale of one row's block, and of one 128 x 128 block of B."""
+    b = Blocks([150], 300, 400)
+    b.sa[7, 2] = float("inf")
+    b.sb[0, 1, 3] = float("nan")
+    b.call(variant=VARIANTS[variant])
+    torch.cuda.synchronize()
+    got, _ = raw(b.D, b.rows, b.N, b.N)
+    assert not got[7].isfinite().any() and got[:, 128:256].isnan().all()
+    rows = [i for i in range(150) if i != 7]
+    assert got[rows][:, :128].isfinite().all() and got[rows][:, 256:].isfinite().all()
+
+
+def test_wrong_offsets_stay_inside():
+    c = Blocks([20, 20, 20], 64, 256).call()
+    for bad in ([0, 90, 20, 60], [-5, 20, 1000, 2000], [60, 40, 20, 0], [0, 0, 0, 0]):
+        args = list(c.args)
+        args[4] = torch.tensor(bad, dtype=torch.int32).cuda()
+        for v in range(1, 7):
+            tla.gemm_blocks(*args, variant=v, **c.kw)
+    torch.cuda.synchronize()
+    c.again()
+    c.verify()
+
+
+@pytest.mark.parametrize("make", [lambda: Blocks([70, 0, 300], 136, 384), lambda: Blocks([2], 136, 384),
+                                  lambda: Gated([70, 0, 300], 136, 384, tla.E4M3)])
+def test_streams_and_graphs(make):
+    c = make()
+    s = torch.cuda.Stream()
+    c.call(stream=s.cuda_stream)
+    s.synchronize()
+    c.verify()
+    out = c.D if isinstance(c, Blocks) else c.H
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.again()
+    x = c.args[5].view(torch.int8)
+    for k in range(4):
+        x.copy_(x.roll(c.args[6 if isinstance(c, Blocks) else 7]) if k else x)
+        out.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        first = out.clone()
+        out.fill_(7.0)
+        c.again()
+        torch.cuda.synchronize()
+        assert torch.equal(first.view(torch.int16), out.view(torch.int16))

@@ -21,7 +21,7 @@ LIB_PATH = os.path.join(_HERE, "libtla.so")
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_OVERLAP, ERR_HIP = 0, -1, -2, -3, -4
 F16, BF16, E4M3, F32, I8 = 0, 1, 2, 3, 4
 ROW_MAJOR, COL_MAJOR = 0, 1
-ACT_NONE, ACT_RELU, ACT_GELU = 0, 1, 2
+ACT_NONE, ACT_RELU, ACT_GELU, ACT_SILU = 0, 1, 2, 3
 Z_NONE, Z_STORE, Z_GRAD = 0, 1, 2
 MAX_MODES, MAX_LEAVES = 8, 16
 
@@ -35,6 +35,9 @@ EXPORTED = [
     "tla_status_string", "tla_version",
     "tla_grouped_gemm", "tla_grouped_gemm_variant", "tla_grouped_gemm_run_variant",
     "tla_grouped_gemm_wgrad", "tla_gemm_i8", "tla_quantize_rows",
+    "tla_gated_gemm", "tla_gated_gemm_run_variant", "tla_gated_gemm_grad",
+    "tla_gated_gemm_grad_run_variant", "tla_gemm_blocks", "tla_gemm_blocks_run_variant",
+    "tla_quantize_blocks",
 ]
 
 
@@ -112,6 +115,11 @@ def lib() -> ctypes.CDLL:
         L.tla_grouped_gemm_wgrad.argtypes = [ctypes.POINTER(GroupedWgradArgs), P]
         L.tla_gemm_i8.argtypes = [ctypes.POINTER(GemmI8Args), P]
         L.tla_quantize_rows.argtypes = [I64, I64, P, I32, I64, P, I64, P, P]
+        for name, args in (("gated_gemm", GatedGemmArgs), ("gated_gemm_grad", GatedGradArgs),
+                           ("gemm_blocks", GemmBlocksArgs)):
+            getattr(L, "tla_" + name).argtypes = [ctypes.POINTER(args), P]
+            getattr(L, "tla_%s_run_variant" % name).argtypes = [ctypes.POINTER(args), I32, P]
+        L.tla_quantize_blocks.argtypes = [I64, I64, P, I32, I64, I32, P, I64, P, I32, I64, P]
         L.tla_status_string.argtypes = [ctypes.c_int]
         L.tla_status_string.restype = ctypes.c_char_p
         for name in EXPORTED:
@@ -345,11 +353,11 @@ def _packed_call(name, args, stream, *more):
 _torch_types = {}
 
 
-def _ptr(t, what, kind=None, dense=False):
+def _ptr(t, what, kind=None, dense=False, pitched=False):
     """Device address of a CUDA tensor, 0 for None; kind ("int32", "float32"):
-    the element type the library fixes for this buffer.  Those buffers, and
-    dense ones, have no stride among the arguments: another type or a strided
-    view is refused, not misread."""
+    the element type the library fixes for this buffer.  Those buffers (but for
+    pitched ones, whose pitch is an argument), and dense ones, have no stride
+    among the arguments: another type or a strided view is refused, not misread."""
     if t is None:
         return 0
     if kind is not None:
@@ -359,7 +367,7 @@ def _ptr(t, what, kind=None, dense=False):
             want = _torch_types[kind] = getattr(torch, kind)
         if t.dtype is not want:
             raise ValueError("%s must be a %s tensor" % (what, kind))
-        dense = True
+        dense = not pitched
     if dense and not t.is_contiguous():
         raise ValueError("%s must be contiguous" % what)
     if not getattr(t, "is_cuda", False):
@@ -430,6 +438,121 @@ def quantize_rows(M, K, X, x_type, ldx, Q, ldq, scale, stream=None):
                                  _ptr(scale, "scale", "float32"), _stream(stream, X, Q, scale))
     if rc != OK:
         raise TlaError(rc, "tla_quantize_rows")
+
+
+# -------------------------- gated feed-forward and block-scaled products
+
+class GatedGemmArgs(ctypes.Structure):
+    _fields_ = [
+        ("groups", ctypes.c_int64), ("rows", ctypes.c_int64), ("N", ctypes.c_int64),
+        ("K", ctypes.c_int64), ("offsets", ctypes.c_void_p),
+        ("X", ctypes.c_void_p), ("type", ctypes.c_int32), ("ldx", ctypes.c_int64),
+        ("W_gate", ctypes.c_void_p), ("W_up", ctypes.c_void_p), ("w_order", ctypes.c_int32),
+        ("ldw", ctypes.c_int64), ("stride_w", ctypes.c_int64),
+        ("H", ctypes.c_void_p), ("h_type", ctypes.c_int32), ("ldh", ctypes.c_int64),
+        ("b_gate", ctypes.c_void_p), ("b_up", ctypes.c_void_p), ("bias_type", ctypes.c_int32),
+        ("Z_gate", ctypes.c_void_p), ("Z_up", ctypes.c_void_p), ("ldz", ctypes.c_int64),
+        ("scale_x", ctypes.c_void_p), ("sx_order", ctypes.c_int32), ("ldsx", ctypes.c_int64),
+        ("scale_gate", ctypes.c_void_p), ("scale_up", ctypes.c_void_p),
+        ("sw_order", ctypes.c_int32), ("ldsw", ctypes.c_int64), ("stride_sw", ctypes.c_int64),
+        ("act", ctypes.c_int32),
+    ]
+
+
+class GatedGradArgs(ctypes.Structure):
+    _fields_ = [
+        ("groups", ctypes.c_int64), ("rows", ctypes.c_int64), ("N", ctypes.c_int64),
+        ("K", ctypes.c_int64), ("offsets", ctypes.c_void_p),
+        ("dY", ctypes.c_void_p), ("type", ctypes.c_int32), ("ldy", ctypes.c_int64),
+        ("W", ctypes.c_void_p), ("w_order", ctypes.c_int32), ("ldw", ctypes.c_int64),
+        ("stride_w", ctypes.c_int64),
+        ("Z_gate", ctypes.c_void_p), ("Z_up", ctypes.c_void_p), ("ldz", ctypes.c_int64),
+        ("dZ_gate", ctypes.c_void_p), ("dZ_up", ctypes.c_void_p), ("d_type", ctypes.c_int32),
+        ("ldd", ctypes.c_int64), ("H", ctypes.c_void_p), ("ldh", ctypes.c_int64),
+        ("act", ctypes.c_int32),
+    ]
+
+
+class GemmBlocksArgs(ctypes.Structure):
+    _fields_ = [
+        ("groups", ctypes.c_int64), ("rows", ctypes.c_int64), ("N", ctypes.c_int64),
+        ("K", ctypes.c_int64), ("offsets", ctypes.c_void_p),
+        ("A", ctypes.c_void_p), ("lda", ctypes.c_int64),
+        ("scale_a", ctypes.c_void_p), ("sa_order", ctypes.c_int32), ("ldsa", ctypes.c_int64),
+        ("B", ctypes.c_void_p), ("ldb", ctypes.c_int64), ("stride_b", ctypes.c_int64),
+        ("scale_b", ctypes.c_void_p), ("sb_order", ctypes.c_int32), ("ldsb", ctypes.c_int64),
+        ("stride_sb", ctypes.c_int64),
+        ("D", ctypes.c_void_p), ("d_type", ctypes.c_int32), ("ldd", ctypes.c_int64),
+        ("bias", ctypes.c_void_p), ("bias_type", ctypes.c_int32), ("act", ctypes.c_int32),
+    ]
+
+
+_PACK_GATED = struct.Struct("4qPPiqPPiqqPiqPPiPPqPiqPPiqqi")
+_PACK_GATED_GRAD = struct.Struct("4qPPiqPiqqPPqPPiqPqi")
+_PACK_BLOCKS = struct.Struct("4qPPqPiqPqqPiqqPiqPii")
+
+
+def _run(name, args, stream, variant):
+    if variant is None:
+        _packed_call(name, args, stream)
+    else:
+        _packed_call(name + "_run_variant", args, stream, variant)
+
+
+def gated_gemm(groups, rows, N, K, offsets, X, type, ldx, W_gate, W_up, w_order, ldw, stride_w, H,
+               h_type, ldh, b_gate=None, b_up=None, bias_type=None, Z_gate=None, Z_up=None, ldz=0,
+               scale_x=None, sx_order=COL_MAJOR, ldsx=0, scale_gate=None, scale_up=None,
+               sw_order=ROW_MAJOR, ldsw=0, stride_sw=0, act=ACT_SILU, stream=None, variant=None):
+    """Both projections of a gated feed-forward layer, the activation and the
+    product (tla_gated_gemm): g = X.Wg + b_gate, u = X.Wu + b_up, H = act(g) u, and
+    Z_gate = g, Z_up = u when they are given.  E4M3 with block scales (scale_x: a
+    block of 128 of a row, scale_gate and scale_up: a 128 x 128 block).  offsets as
+    for grouped_gemm (None: one expert, a dense layer)."""
+    a = _PACK_GATED.pack(
+        groups, rows, N, K, _ptr(offsets, "offsets", "int32"), _ptr(X, "X"), type, ldx,
+        _ptr(W_gate, "W_gate"), _ptr(W_up, "W_up"), w_order, ldw, stride_w, _ptr(H, "H"), h_type, ldh,
+        _ptr(b_gate, "b_gate", dense=True), _ptr(b_up, "b_up", dense=True),
+        h_type if bias_type is None else bias_type, _ptr(Z_gate, "Z_gate"), _ptr(Z_up, "Z_up"), ldz,
+        _ptr(scale_x, "scale_x", "float32", pitched=True), sx_order, ldsx,
+        _ptr(scale_gate, "scale_gate", "float32", pitched=True),
+        _ptr(scale_up, "scale_up", "float32", pitched=True), sw_order, ldsw, stride_sw, act)
+    _run("tla_gated_gemm", a, _stream(stream, X, W_gate, H), variant)
+
+
+def gated_gemm_grad(groups, rows, N, K, offsets, dY, type, ldy, W, w_order, ldw, stride_w, Z_gate,
+                    Z_up, ldz, dZ_gate, dZ_up, d_type, ldd, H=None, ldh=0, act=ACT_SILU,
+                    stream=None, variant=None):
+    """The backward pass of gated_gemm up to the projections' outputs
+    (tla_gated_gemm_grad): dh = dY.W, dZ_gate = dh u act'(g), dZ_up = dh act(g) with
+    g = Z_gate and u = Z_up, and H = act(g) u when it is given."""
+    a = _PACK_GATED_GRAD.pack(
+        groups, rows, N, K, _ptr(offsets, "offsets", "int32"), _ptr(dY, "dY"), type, ldy,
+        _ptr(W, "W"), w_order, ldw, stride_w, _ptr(Z_gate, "Z_gate"), _ptr(Z_up, "Z_up"), ldz,
+        _ptr(dZ_gate, "dZ_gate"), _ptr(dZ_up, "dZ_up"), d_type, ldd, _ptr(H, "H"), ldh, act)
+    _run("tla_gated_gemm_grad", a, _stream(stream, dY, W, dZ_gate), variant)
+
+
+def gemm_blocks(groups, rows, N, K, offsets, A, lda, scale_a, sa_order, ldsa, B, ldb, stride_b,
+                scale_b, sb_order, ldsb, stride_sb, D, d_type, ldd, bias=None, bias_type=None,
+                act=ACT_NONE, stream=None, variant=None):
+    """D = act(A.B + bias) with e4m3 A (rows x K) and B ([N, K]) and a scale for
+    each 1 x 128 block of A and 128 x 128 block of B (tla_gemm_blocks)."""
+    a = _PACK_BLOCKS.pack(
+        groups, rows, N, K, _ptr(offsets, "offsets", "int32"), _ptr(A, "A"), lda,
+        _ptr(scale_a, "scale_a", "float32", pitched=True), sa_order, ldsa, _ptr(B, "B"), ldb, stride_b,
+        _ptr(scale_b, "scale_b", "float32", pitched=True), sb_order, ldsb, stride_sb, _ptr(D, "D"),
+        d_type, ldd, _ptr(bias, "bias", dense=True), d_type if bias_type is None else bias_type, act)
+    _run("tla_gemm_blocks", a, _stream(stream, A, B, D), variant)
+
+
+def quantize_blocks(M, K, X, x_type, ldx, block_rows, Q, ldq, scale, s_order, lds, stream=None):
+    """e4m3 codes Q and a scale for each block_rows (1 or 128) x 128 block of X
+    (tla_quantize_blocks)."""
+    rc = lib().tla_quantize_blocks(M, K, _ptr(X, "X"), x_type, ldx, block_rows, _ptr(Q, "Q"), ldq,
+                                   _ptr(scale, "scale", "float32", pitched=True), s_order, lds,
+                                   _stream(stream, X, Q, scale))
+    if rc != OK:
+        raise TlaError(rc, "tla_quantize_blocks")
 
 
 # -------------------------------------------------------------- transpose

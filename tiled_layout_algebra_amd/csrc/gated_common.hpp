@@ -1,0 +1,303 @@
+// gated_common.hpp -- what the kernels of the gated feed-forward products and
+// of the block-scaled e4m3 product share: the block-scaled matrix-core atom and
+// the epilogues.
+#pragma once
+
+#include "grouped_common.hpp"
+
+namespace tla {
+
+// e4m3 with a scale for each block of 128 along K: the 16x16x128 instruction
+// takes a whole block, from a zero accumulator, and the caller adds its result
+// times the two operands' scales to an fp32 sum.  (A 32x32 result would hold 16
+// registers of a block's partial sums at a time instead of 4.)  Lane l holds 32
+// consecutive K of row l % 16; results: row l % 16 of the second operand,
+// columns 4 (l / 16) .. + 3 of the first.
+template <>
+struct OpAtom<kE4M3Blocks> {
+  static constexpr int kK = 128;
+  static constexpr int kLaneBytes = 32;
+  typedef i32x8 Frag;
+  typedef f32x4 Acc;
+  static __device__ __forceinline__ f32x4 block(const Frag& a, const Frag& b) {
+    const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, zero, 0, 0, 0, 127, 0, 127);
+  }
+};
+
+namespace {
+
+// One k-tile (a block of 128) of a wave's MFMA tiles: acc += scale part, the
+// sums of a tile kAhead instructions behind its matrix instruction, so that
+// these follow each other without waiting for a result.  s[0]: the scales of the
+// plain sums or of the first half of the columns (the gate's), s[1]: of the
+// other half.  b holds FB of the FN column fragments; after(j) is called behind
+// the last use of fragment j and issues kReads LDS reads where j + FB < FN, for
+// fragment j + FB in its place.
+template <int FM, int FN, bool kTwo, int kReads, int FB, class F>
+__device__ __forceinline__ void blocks_mma(f32x4 (&acc)[FM][FN], const i32x8 (&a)[FM],
+                                           i32x8 (&b)[FB], const float (&s)[2][FM], F&& after) {
+  constexpr int kN = FM * FN, kAhead = kN < 4 ? kN : 4;
+  f32x4 part[kAhead];
+  static_for<kN + kAhead>([&](auto x) {
+    if constexpr (x >= kAhead) {
+      constexpr int y = x - kAhead, i = y % FM, j = y / FM;
+      const float c = s[kTwo && j >= FN / 2][i];
+      static_for<4>([&](auto q) {
+        acc[i][j][(int)q] = fmaf(part[y % kAhead][(int)q], c, acc[i][j][(int)q]);
+      });
+    }
+    if constexpr (x < kN) {
+      part[x % kAhead] = OpAtom<kE4M3Blocks>::block(b[x / FM % FB], a[x % FM]);
+      if constexpr (x % FM == FM - 1 && x / FM + FB < FN) after(std::integral_constant<int, x / FM>{});
+    }
+  });
+  static_for<kN + kAhead>([&](auto x) {
+    if constexpr (x >= kAhead) __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+    if constexpr (x < kN) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      if constexpr (x % FM == FM - 1 && x / FM + FB < FN)
+        __builtin_amdgcn_sched_group_barrier(0x100, kReads, 0);
+    }
+  });
+}
+
+// sigmoid(z) = 1 / (1 + 2^(-z log2 e)) by the hardware's exp2 and reciprocal
+// (one unit each); the exponent's rounding makes it off by (|z| + 4) 2^-24 of
+// its value.
+__device__ __forceinline__ float sigmoid(float z) {
+  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * -1.44269504f));
+}
+
+template <int kAct>
+__device__ __forceinline__ float act_value(float z) {
+  if constexpr (kAct == TLA_ACT_RELU) return relu_nan(z);
+  if constexpr (kAct == TLA_ACT_GELU) return gelu_nan(z);
+  if constexpr (kAct == TLA_ACT_SILU) return z * sigmoid(z);
+  return z;
+}
+// act(z) and act'(z); SiLU: p + z p (1 - p), p = sigmoid(z)
+template <int kAct>
+__device__ __forceinline__ void act_both(float z, float& value, float& slope) {
+  if constexpr (kAct == TLA_ACT_SILU) {
+    const float s = sigmoid(z);
+    value = z * s;
+    slope = fmaf(value, 1.f - s, s);
+  } else {
+    value = act_value<kAct>(z);
+    slope = kAct == TLA_ACT_RELU ? (z > 0.f ? 1.f : 0.f) : kAct == TLA_ACT_GELU ? gelu_slope(z) : 1.f;
+  }
+}
+// f(integral_constant<act>)
+template <class F>
+__device__ __forceinline__ void with_act(int act, F&& f) {
+  if (act == TLA_ACT_SILU) f(std::integral_constant<int, TLA_ACT_SILU>{});
+  else if (act == TLA_ACT_GELU) f(std::integral_constant<int, TLA_ACT_GELU>{});
+  else if (act == TLA_ACT_RELU) f(std::integral_constant<int, TLA_ACT_RELU>{});
+  else f(std::integral_constant<int, TLA_ACT_NONE>{});
+}
+__device__ __forceinline__ float act_any(float z, int act) {
+  float y = z;
+  with_act(act, [&](auto a) { y = act_value<a>(z); });
+  return y;
+}
+
+// A wave's piece of a row-major 16-bit matrix in LDS (WaveRegion) seen from MFMA
+// tiles of FR rows: FR 32: lane l holds row 32 i + l % 32, columns 32 j + 8 g + 4
+// (l / 32) .. + 3; FR 16: row 16 i + l % 16, columns 16 j + 4 (l / 16) .. + 3.
+template <int FR, int WM, int WN>
+struct Piece {
+  using R = WaveRegion<WM / 32, WN / 32>;
+  static constexpr int kG = FR == 32 ? 4 : 1, kBytes = WM * WN * 2;
+  static __device__ __forceinline__ int column(int lane, int j, int g) {
+    return FR * j + 8 * g + 4 * (lane / FR);
+  }
+  static __device__ __forceinline__ uint2* slot(uint8_t* region, int lane, int i, int j, int g) {
+    const int r = FR * i + lane % FR, c = column(lane, j, g);
+    return (uint2*)(region + r * R::kRowB + R::swz(r, c / 8) * 16 + (c & 4) * 2);
+  }
+};
+
+// Four bias values from column n (clamped to the last) of expert e
+__device__ __forceinline__ f32x4 bias4(const GroupedParams& p, const uint8_t* bias, int e, int n) {
+  f32x4 x;
+  const int64_t at = (int64_t)e * p.N;
+  static_for<4>([&](auto q) { x[(int)q] = load_elem(bias, p.bias_type, at + min(n + q, p.N - 1)); });
+  return x;
+}
+
+__device__ __forceinline__ void wave_fence() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
+
+// One pass over pairs of sums: f(gate, up) packed into a region.
+template <int FR, int WM, int WN, bool kBf, class Acc, int FM, int FN, class F>
+__device__ __forceinline__ void pair_pass(int lane, const Acc (&acc)[FM][FN], uint8_t* region, F&& f) {
+  using P = Piece<FR, WM, WN>;
+  static_for<FN / 2>([&](auto j) {
+    static_for<P::kG>([&](auto g) {
+      static_for<FM>([&](auto i) {
+        float y[4];
+        static_for<4>([&](auto q) { y[q] = f(acc[i][j][4 * g + q], acc[i][j + FN / 2][4 * g + q]); });
+        *P::slot(region, lane, i, j, g) = uint2{pack2<kBf>(y[0], y[1]), pack2<kBf>(y[2], y[3])};
+      });
+    });
+  });
+}
+
+// The gated product's epilogue for a wave's sums: rows row .., columns col ..
+// (WN of them) of the hidden layer, the expert's rows end at r1; tiles j < FN / 2
+// are the gate's, the others the up projection's.  fp32 throughout, one rounding
+// for each output.  region: 2 WM WN 16-bit values.
+template <int FR, int WM, int WN, class Acc, int FM, int FN>
+__device__ __forceinline__ void gated_epilogue(const GroupedParams& p, int e, int r1, int row,
+                                               int col, int lane, Acc (&acc)[FM][FN],
+                                               uint8_t* region) {
+  using P = Piece<FR, WM, WN>;
+  using R = typename P::R;
+  const int rows = min(WM, r1 - row), cols = min(WN, p.N - col);
+  if (rows <= 0 || cols <= 0) return;
+  const bool v16 = p.flags & kOpD16;
+  if (p.bias || p.bias2) {
+    static_for<FN>([&](auto j) {
+      const uint8_t* bias = j < FN / 2 ? p.bias : p.bias2;
+      if (bias) {
+        static_for<P::kG>([&](auto g) {
+          const f32x4 b = bias4(p, bias, e, col + P::column(lane, j % (FN / 2), g));
+          static_for<FM>([&](auto i) {
+            static_for<4>([&](auto q) { acc[i][j][4 * g + q] += b[(int)q]; });
+          });
+        });
+      }
+    });
+  }
+  auto run = [&](auto kb) {
+    if (p.Z) {
+      pair_pass<FR, WM, WN, kb>(lane, acc, region, [](float g, float) { return g; });
+      pair_pass<FR, WM, WN, kb>(lane, acc, region + P::kBytes, [](float, float u) { return u; });
+      wave_fence();
+      const int64_t at = ((int64_t)row * p.ldz + col) * 2;
+      R::store(p.Z + at, p.ldz, region, lane, rows, cols, v16);
+      R::store(p.Z2 + at, p.ldz, region + P::kBytes, lane, rows, cols, v16);
+      wave_fence();
+    }
+    with_act(p.act, [&](auto act) {
+      constexpr int kAct = act;
+      pair_pass<FR, WM, WN, kb>(lane, acc, region,
+                                [](float g, float u) { return act_value<kAct>(g) * u; });
+    });
+    wave_fence();
+    R::store(p.D + ((int64_t)row * p.ldd + col) * 2, p.ldd, region, lane, rows, cols, v16);
+  };
+  if (p.d_type == TLA_BF16) run(std::true_type{});
+  else run(std::false_type{});
+}
+
+// The gradient's epilogue: acc is dh; D = dh up act'(gate), D2 = dh act(gate),
+// H = act(gate) up with gate and up read from Z and Z2.  WN columns in parts of
+// half of them (or all 32): a part's gate and up go through LDS as whole rows,
+// the gradients back the same way, the hidden layer waits in the sums' registers.
+// region: WM WN 16-bit values, 2 WM WN for WN = 32.
+template <int WM, int WN, int FM, int FN>
+__device__ __forceinline__ void gate_grad_epilogue(const GroupedParams& p, int r1, int row, int col,
+                                                   int lane, f32x16 (&acc)[FM][FN],
+                                                   uint8_t* region) {
+  constexpr int kPart = WN >= 64 ? WN / 2 : WN, FP = kPart / 32;
+  using P = Piece<32, WM, kPart>;
+  using R = typename P::R;
+  const int rows = min(WM, r1 - row);
+  if (rows <= 0) return;
+  const bool v16 = p.flags & kOpD16;
+  uint8_t* region2 = region + P::kBytes;
+  auto run = [&](auto kb, auto act) {
+    static_for<WN / kPart>([&](auto part) {
+      const int c = col + part * kPart, cols = min(kPart, p.N - c);
+      if (cols <= 0) return;
+      const int64_t zat = ((int64_t)row * p.ldz + c) * 2, dat = ((int64_t)row * p.ldd + c) * 2;
+      R::load(p.Z + zat, p.ldz, region, lane, rows, cols);
+      R::load(p.Z2 + zat, p.ldz, region2, lane, rows, cols);
+      wave_fence();
+      static_for<FP>([&](auto jj) {
+        constexpr int j = part * FP + jj;
+        static_for<4>([&](auto g) {
+          static_for<FM>([&](auto i) {
+            uint2 *gate = P::slot(region, lane, i, jj, g), *up = P::slot(region2, lane, i, jj, g);
+            const uint2 zg = *gate, zu = *up;
+            const float g4[4] = {widen_lo<kb>(zg.x), widen_hi<kb>(zg.x), widen_lo<kb>(zg.y),
+                                 widen_hi<kb>(zg.y)};
+            const float u4[4] = {widen_lo<kb>(zu.x), widen_hi<kb>(zu.x), widen_lo<kb>(zu.y),
+                                 widen_hi<kb>(zu.y)};
+            float dg[4], du[4];
+            static_for<4>([&](auto q) {
+              float value, slope;
+              act_both<act>(g4[q], value, slope);
+              const float dh = acc[i][j][4 * g + q];
+              dg[q] = dh * (u4[q] * slope);
+              du[q] = dh * value;
+              acc[i][j][4 * g + q] = value * u4[q];
+            });
+            *gate = uint2{pack2<kb>(dg[0], dg[1]), pack2<kb>(dg[2], dg[3])};
+            *up = uint2{pack2<kb>(du[0], du[1]), pack2<kb>(du[2], du[3])};
+          });
+        });
+      });
+      wave_fence();
+      R::store(p.D + dat, p.ldd, region, lane, rows, cols, v16);
+      R::store(p.D2 + dat, p.ldd, region2, lane, rows, cols, v16);
+      wave_fence();
+      if (p.H) {
+        static_for<FP>([&](auto jj) {
+          constexpr int j = part * FP + jj;
+          static_for<4>([&](auto g) {
+            static_for<FM>([&](auto i) {
+              *P::slot(region, lane, i, jj, g) =
+                  uint2{pack2<kb>(acc[i][j][4 * g], acc[i][j][4 * g + 1]),
+                        pack2<kb>(acc[i][j][4 * g + 2], acc[i][j][4 * g + 3])};
+            });
+          });
+        });
+        wave_fence();
+        R::store(p.H + ((int64_t)row * p.ldh + c) * 2, p.ldh, region, lane, rows, cols, v16);
+        wave_fence();
+      }
+    });
+  };
+  with_act(p.act, [&](auto act) {
+    if (p.d_type == TLA_BF16) run(std::true_type{}, act);
+    else run(std::false_type{}, act);
+  });
+}
+
+// The block-scaled product's epilogue: D = act(sum + bias).
+template <int WM, int WN, int FM, int FN>
+__device__ __forceinline__ void blocks_epilogue(const GroupedParams& p, int e, int r1, int row,
+                                                int col, int lane, f32x4 (&acc)[FM][FN],
+                                                uint8_t* region) {
+  using P = Piece<16, WM, WN>;
+  using R = typename P::R;
+  const int rows = min(WM, r1 - row), cols = min(WN, p.N - col);
+  if (rows <= 0 || cols <= 0) return;
+  if (p.bias) {
+    static_for<FN>([&](auto j) {
+      const f32x4 b = bias4(p, p.bias, e, col + P::column(lane, j, 0));
+      static_for<FM>([&](auto i) { acc[i][j] += b; });
+    });
+  }
+  auto run = [&](auto kb) {
+    with_act(p.act, [&](auto act) {
+      static_for<FN>([&](auto j) {
+        static_for<FM>([&](auto i) {
+          float y[4];
+          static_for<4>([&](auto q) { y[q] = act_value<act>(acc[i][j][(int)q]); });
+          *P::slot(region, lane, i, j, 0) = uint2{pack2<kb>(y[0], y[1]), pack2<kb>(y[2], y[3])};
+        });
+      });
+    });
+    wave_fence();
+    R::store(p.D + ((int64_t)row * p.ldd + col) * 2, p.ldd, region, lane, rows, cols,
+             p.flags & kOpD16);
+  };
+  if (p.d_type == TLA_BF16) run(std::true_type{});
+  else run(std::false_type{});
+}
+
+}  // namespace
+}  // namespace tla

@@ -19,7 +19,7 @@
 // 777 rows' fp32 gradients on 16 experts of 512 x 1024 12 us (33.5 MB written).
 #pragma once
 
-#include "grouped_common.hpp"
+#include "gated_common.hpp"
 
 namespace tla {
 namespace {
@@ -36,7 +36,8 @@ __device__ __forceinline__ void dma4_buf(const uint8_t* base, uint32_t voffset, 
 #endif
 }
 
-template <int kCode, int kForm, int BM, int BN, int kStages, int kFront, int kWM, int kWN>
+template <int kCode, int kForm, int BM, int BN, int kStages, int kFront, int kWM, int kWN,
+          int kRole = kPlain>
 __global__ __launch_bounds__(64 * kWM * kWN) void grouped_direct_kernel(const GroupedParams p) {
   constexpr bool kShift = kForm == kNKShift;
   using Atom = std::conditional_t<kShift && kCode == kE4M3, E4m3Bytes, OpAtom<kCode>>;
@@ -58,7 +59,13 @@ __global__ __launch_bounds__(64 * kWM * kWN) void grouped_direct_kernel(const Gr
   static_assert(kStages * (SLAB_A + SLAB_B) <= 160 * 1024, "LDS budget");
   static_assert(!kBT || (EB == 2 && BN >= 128), "N-contiguous B: 16-bit");
   static_assert(!kAT || (EB == 2 && BM >= 128), "M-contiguous A: 16-bit");
-  constexpr int kRowBT = BN * 2;                   // bytes per k row of an N-contiguous slab
+  // kGated: the first half of B's slab is the gate's columns, the other half the
+  // same columns of the up projection (an N-contiguous slab: 64 rows of each); a
+  // wave's first FN / 2 MFMA tiles are the gate's
+  constexpr bool kTwo = kRole == kGated;
+  constexpr int BNO = kTwo ? BN / 2 : BN, FH = FN / 2;  // columns of D; of a wave's tiles, one operand's
+  static_assert(!kTwo || FN % 2 == 0, "a wave holds both sums of an element");
+  constexpr int kRowBT = BNO * 2;                  // bytes per k row of an N-contiguous slab
   constexpr int kChBT = kRowBT / 16;
   constexpr int kRowAT = BM * 2;                   // bytes per k row of an M-contiguous slab
   constexpr int kChAT = kRowAT / 16;
@@ -108,13 +115,15 @@ __global__ __launch_bounds__(64 * kWM * kWN) void grouped_direct_kernel(const Gr
     e = rt.e;
     m0 = rt.r0;
     m_end = rt.r1;
-    n0 = rt.tn * BN;
+    n0 = rt.tn * BNO;
     K = p.K;
     // 32-bit offsets count from the tile's first row
     A += (int64_t)m0 * p.lda * EB;
     B += ((int64_t)e * p.stride_b + (kBT ? 0 : (int64_t)n0 * p.ldb)) * EB;
   }
   const int wm0 = (wave % kWM) * WM, wn0 = (wave / kWM) * WN;
+  const int wb0 = kTwo ? wn0 / 2 : wn0;  // the wave's first column
+  const int64_t up_by = kTwo ? p.B2 - p.B : 0;
   const int KT = (K + BK - 1) / BK;
   const int KTf = K / BK;  // whole k-tiles; tile KTf, if K ends inside it, is ragged
 
@@ -139,7 +148,7 @@ __global__ __launch_bounds__(64 * kWM * kWN) void grouped_direct_kernel(const Gr
   const int a_bytes = kAT ? k_rows_bytes(p.lda, p.M)
                           : (int)((min(a_last, BM - 1) * a_rb + K * EB + a_off + 3) & ~3u);
   const int b_bytes = kBT ? k_rows_bytes(p.ldb, p.N)
-                          : (int)((min(b_last, BN - 1) * b_rb + K * EB + b_off + 3) & ~3u);
+                          : (int)((min(b_last, BNO - 1) * b_rb + K * EB + b_off + 3) & ~3u);
   // Copy q (A for q < IA, else B): slab row r = tid/kChunks + (NT/kChunks)*q',
   // landing at slab slot wave*64 + NT*q' (lane-linear); the lane fetches the
   // global chunk the swizzle assigns to that slot, from row r clamped to the
@@ -166,11 +175,14 @@ __global__ __launch_bounds__(64 * kWM * kWN) void grouped_direct_kernel(const Gr
       // slab chunk tid + NT q': k row r, stored chunk pc, which holds logical
       // chunk pc ^ 4 (r % 4): columns n0 + 8 lc .. + 7, clamped to the
       // matrix' last chunk (columns past N are never stored)
-      const int sc = tid + NT * qq, r = sc / kChBT, pc = sc % kChBT;
-      const int n = min(n0 + 8 * (pc ^ (4 * (r & 3))), (p.N - 1) & ~7);
+      // (kTwo: of the half slab, whose 128-byte rows swap halves by r / 2)
+      constexpr int qh = kTwo ? qq % (IB / 2) : qq;
+      const int sc = tid + NT * qh, r = sc / kChBT, pc = sc % kChBT;
+      const int n = min(n0 + 8 * (pc ^ (4 * (kTwo ? (r >> 1) & 1 : r & 3))), (p.N - 1) & ~7);
       off[q] = (uint32_t)(((int64_t)r * p.ldb + n) * EB);
     } else {
-      const int r = tid / kChunks + (NT / kChunks) * qq;
+      constexpr int qh = kTwo && !kA ? qq % (IB / 2) : qq;
+      const int r = tid / kChunks + (NT / kChunks) * qh;
       const int64_t row = kA ? min(r, m_end - 1 - m0) : min(r, p.N - 1 - n0);
       const int64_t rb = (kA ? p.lda : p.ldb) * EB;
       off[q] = (uint32_t)(row * rb + Swz::chunk(r, tid % kChunks) * 16);
@@ -198,7 +210,7 @@ __global__ __launch_bounds__(64 * kWM * kWN) void grouped_direct_kernel(const Gr
   static_for<KSTEPS>([&](auto ks) {
     static_for<kSub>([&](auto u) {
       const int c = (ks * kStepBytes + (lane >> 5) * Atom::kLaneBytes) / 16 + u;
-      const int ra = wm0 + (lane & 31), rb = wn0 + (lane & 31);
+      const int ra = wm0 + (lane & 31), rb = wb0 + (lane & 31);
       fa[ks][u] = (uint32_t)(ra * kRowBytes + Swz::chunk(ra, c) * 16);
       fb[ks][u] = (uint32_t)(B_BASE + rb * kRowBytes + Swz::chunk(rb, c) * 16);
     });
@@ -212,9 +224,11 @@ __global__ __launch_bounds__(64 * kWM * kWN) void grouped_direct_kernel(const Gr
       static_for<FN>([&](auto j) {
         static_for<2>([&](auto h) {
           const int k = 16 * ks + 8 * (qw >> 1) + 4 * h + (a4 >> 2);
-          const int n = wn0 + 32 * j + 16 * (qw & 1) + 4 * (a4 & 3);
-          fbt[ks][j][h] = (uint32_t)(B_BASE + k * kRowBT + (((n >> 3) ^ (4 * (k & 3))) * 16) +
-                                     (n & 7) * 2);
+          const int jj = kTwo ? (int)j % FH : (int)j;
+          const int n = wb0 + 32 * jj + 16 * (qw & 1) + 4 * (a4 & 3);
+          const int swap = 4 * (kTwo ? (k >> 1) & 1 : k & 3);
+          fbt[ks][j][h] = (uint32_t)(B_BASE + (kTwo && j >= FH ? SLAB_B / 2 : 0) + k * kRowBT +
+                                     (((n >> 3) ^ swap) * 16) + (n & 7) * 2);
         });
       });
     });
@@ -286,7 +300,10 @@ __global__ __launch_bounds__(64 * kWM * kWN) void grouped_direct_kernel(const Gr
     if constexpr (kBT)
       static_for<FN>([&](auto j) { b[buf][j] = lds_frag_t(fbt[ks][j], slot * SLAB_B); });
     else
-      static_for<FN>([&](auto j) { b[buf][j] = lds_frag(fb[ks], slot * SLAB_B + j * 32 * kRowBytes); });
+      static_for<FN>([&](auto j) {
+        constexpr int at = kTwo ? j % FH * 32 * kRowBytes + j / FH * (SLAB_B / 2) : j * 32 * kRowBytes;
+        b[buf][j] = lds_frag(fb[ks], slot * SLAB_B + at);
+      });
     if constexpr (kShift) {
       static_for<FM>([&](auto i) {
         const uint32_t at = ks + 1 < KSTEPS ? na[ks] + slot * SLAB_A + i * 32 * kRowBytes
@@ -322,7 +339,7 @@ __global__ __launch_bounds__(64 * kWM * kWN) void grouped_direct_kernel(const Gr
       if (kt != KTf || !(kShift || K * EB % 16 != 0)) return;
       if (tid < (kBT ? BM : BM + BN)) {
         const bool is_a = tid < BM;
-        const int r = is_a ? tid : tid - BM;
+        const int r = is_a ? tid : tid - BM;  // (the swizzle repeats within half a slab)
         uint8_t* row = smem + (is_a ? S * SLAB_A : B_BASE + S * SLAB_B) + r * kRowBytes;
         const int first = (kShift ? (int)row_shift(is_a, min(r, is_a ? a_last : b_last)) : 0) +
                           (K - KTf * BK) * EB;
@@ -354,12 +371,16 @@ __global__ __launch_bounds__(64 * kWM * kWN) void grouped_direct_kernel(const Gr
                 smem + slot * SLAB_A + (wave * 64 + NT * q) * 16, a_bytes);
     else if constexpr (q < IA)
       dma16_buf(A, o, kb, smem + slot * SLAB_A + (wave * 64 + NT * q) * 16, a_bytes);
-    else if constexpr (kBT)
-      dma16_buf(B, off[q], (uint32_t)(tt * BK) * (uint32_t)(p.ldb * EB),
-                smem + B_BASE + slot * SLAB_B + (wave * 64 + NT * (q - IA)) * 16, b_bytes);
-    else
-      dma16_buf(B, o, kb, smem + B_BASE + slot * SLAB_B + (wave * 64 + NT * (q - IA)) * 16,
-                b_bytes);
+    else {
+      const uint8_t* from = B;
+      if constexpr (kTwo && q - IA >= IB / 2) from += up_by;
+      if constexpr (kBT)
+        dma16_buf(from, off[q], (uint32_t)(tt * BK) * (uint32_t)(p.ldb * EB),
+                  smem + B_BASE + slot * SLAB_B + (wave * 64 + NT * (q - IA)) * 16, b_bytes);
+      else
+        dma16_buf(from, o, kb, smem + B_BASE + slot * SLAB_B + (wave * 64 + NT * (q - IA)) * 16,
+                  b_bytes);
+    }
   };
   // MFMAs [lo, hi) of a step with copies [q0, q0 + nq) of tile t spread
   // evenly between them: after MFMA k come copies [k*nq/n, (k+1)*nq/n).
@@ -441,20 +462,26 @@ __global__ __launch_bounds__(64 * kWM * kWN) void grouped_direct_kernel(const Gr
   }
   if constexpr (kForm == kGrad)
     wgrad_epilogue<FM, FN>(p, e, m0 + wm0, n0 + wn0, lane, acc, region);
+  else if constexpr (kRole == kGated)
+    gated_epilogue<32, WM, WN / 2>(p, e, m_end, m0 + wm0, n0 + wb0, lane, acc, region);
+  else if constexpr (kRole == kGateGrad)
+    gate_grad_epilogue<WM, WN>(p, m_end, m0 + wm0, n0 + wn0, lane, acc, region);
   else
     grouped_epilogue<kCode, FM, FN>(p, e, m_end, m0 + wm0, n0 + wn0, lane, acc, region);
 }
 
-template <int kCode, int kForm, int BM, int BN, int kStages, int kFront, int kWM, int kWN>
+template <int kCode, int kForm, int BM, int BN, int kStages, int kFront, int kWM, int kWN,
+          int kRole = kPlain>
 int launch(const GroupedParams& p0, hipStream_t stream) {
   GroupedParams p = p0;
-  p.tiles_n = (p.N + BN - 1) / BN;
+  constexpr int kCols = kRole == kGated ? BN / 2 : BN;
+  p.tiles_n = (p.N + kCols - 1) / kCols;
   p.tiles_m = (p.M + BM - 1) / BM;
   const int64_t grid = kForm == kGrad ? (int64_t)p.groups * p.tiles_m * p.tiles_n
                                       : row_tiles_bound(p.rows, p.groups, BM) * p.tiles_n;
   if (grid <= 0) return TLA_OK;
   if (!grid_fits(grid, 64 * kWM * kWN)) return TLA_ERR_UNSUPPORTED;
-  hipLaunchKernelGGL((grouped_direct_kernel<kCode, kForm, BM, BN, kStages, kFront, kWM, kWN>),
+  hipLaunchKernelGGL((grouped_direct_kernel<kCode, kForm, BM, BN, kStages, kFront, kWM, kWN, kRole>),
                      dim3((unsigned)grid), dim3(64 * kWM * kWN), 0, stream, p);
   return hipGetLastError() == hipSuccess ? TLA_OK : TLA_ERR_HIP;
 }

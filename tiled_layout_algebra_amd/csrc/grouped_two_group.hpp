@@ -41,7 +41,7 @@
 // costs most of a whole one: see two_group_lookup.
 #pragma once
 
-#include "grouped_common.hpp"
+#include "gated_common.hpp"
 
 namespace tla {
 namespace {
@@ -57,14 +57,14 @@ constexpr int kTwoGroupLds = 5 * 256 * 128;
 // and n0 columns of them; sum_a / sum_b: this wave sums dY's lines.
 struct TileSpan {
   int e, m0, m_end, n0, K;
-  const uint8_t *A, *B;
+  const uint8_t *A, *B, *B2;  // (B2: role kGated)
   bool sum_a, sum_b;
 };
 
 // The tile program.  kHalf: 128 x 256 instead of 256 x 256, for blocks of at
 // most 128 rows: both groups share the rows and take half the columns each, so
 // every wave multiplies 64 x 64 (16 MFMAs a k-tile, not 32) and none idles.
-template <int kCode, int kForm, bool kHalf>
+template <int kCode, int kForm, bool kHalf, int kRole>
 __device__ __forceinline__ void two_group_tile(const GroupedParams& p, const TileSpan& ts,
                                                uint8_t* smem) {
   constexpr bool kShift = kForm == kNKShift;
@@ -79,7 +79,9 @@ __device__ __forceinline__ void two_group_tile(const GroupedParams& p, const Til
   constexpr int BK = kUsed / EB;                // K elements per k-tile
   constexpr int BM = kHalf ? 128 : 256, BN = 256;
   constexpr int WM = 64, WN = kHalf ? 64 : 128;  // wave tile
-  constexpr int FM = WM / 32, FN = WN / 32;     // MFMA tiles per wave
+  constexpr bool kBlocks = kCode == kE4M3Blocks;
+  constexpr int FR = kBlocks ? 16 : 32;         // rows of an MFMA tile
+  constexpr int FM = WM / FR, FN = WN / FR;     // MFMA tiles per wave
   constexpr int KSTEPS = BK / Atom::kK;         // MFMA k-steps per k-tile
   constexpr int kSub = Atom::kLaneBytes / 16;   // 16-byte reads per fragment
   constexpr int kStepBytes = Atom::kK * EB;
@@ -87,6 +89,7 @@ __device__ __forceinline__ void two_group_tile(const GroupedParams& p, const Til
   constexpr int B_BASE = 2 * SLAB;              // LDS: [A0 A1 | B0 B1 B2]
   constexpr int kCopies = SLAB / (256 * 16);    // 16-byte copies per thread per slab
   constexpr int kCopiesA = BM * kRowBytes / (256 * 16);
+  constexpr int kRowBT = kRole == kGated ? 256 : 512;  // bytes of a k row in B's slab
   static_assert(BK % Atom::kK == 0 && kCopies == 8, "k-tile geometry");
   static_assert(!kShift || (kSub == 1 && kStepBytes == 32), "a dword follows every fragment");
   static_assert((1 << Slab<kRowBytes>::kRowShift) * kChunks <= 32,
@@ -104,6 +107,12 @@ __device__ __forceinline__ void two_group_tile(const GroupedParams& p, const Til
   const bool sum_a = ts.sum_a, sum_b = ts.sum_b;
   const int wm0 = kHalf ? WM * (wave & 1) : 128 * grp + WM * (wave & 1);
   const int wn0 = WN * (kHalf ? 2 * grp + ((wave >> 1) & 1) : ((wave >> 1) & 1));
+  // kGated: the first half of B's slab is the gate's columns n0 .., the other
+  // half the same columns of the up projection; a wave's first FN / 2 MFMA tiles
+  // are the gate's, so a lane holds both sums of an element
+  constexpr bool kTwo = kRole == kGated;
+  constexpr int FH = FN / 2;
+  const int wb0 = kTwo ? wn0 / 2 : wn0;         // the wave's first column
   const bool busy = kForm == kGrad || m0 + wm0 < m_end;  // a wave without a row multiplies nothing
   const int KT = (K + BK - 1) / BK;
   const int KTf = K / BK;  // whole k-tiles; tile KTf, if K ends inside it, is ragged
@@ -123,7 +132,7 @@ __device__ __forceinline__ void two_group_tile(const GroupedParams& p, const Til
   const uint32_t off = kShift ? (uint32_t)(uintptr_t)op & 3u : 0u;
   static_for<kCopies>([&](auto q) {
     // up to the dword that holds the last row's last byte
-    const int n = min(rows_left - 32 * (int)q, 32);
+    const int n = min(rows_left - 32 * (kTwo && grp ? (int)q % 4 : (int)q), 32);
     recs[q] = n > 0 ? (int)((uint32_t)((n - 1) * rb + (int64_t)K * EB + off + 3) & ~3u) : 0;
   });
   // per group: the byte step of a k-tile, and (N-contiguous B) of a copy
@@ -141,7 +150,21 @@ __device__ __forceinline__ void two_group_tile(const GroupedParams& p, const Til
     return K > 0 ? (int)min((((K - 1) * ld + lines) * EB + 3) & ~(int64_t)3, (int64_t)0x7FFFFFFC) : 0;
   };
   int64_t q_stride = 32 * rb;
-  if constexpr (kBT) {
+  if constexpr (kBT && kTwo) {
+    if (grp == 1) {
+      // each half slab 64 rows of k x 128 columns: chunk t + 256 (q % 4) of the
+      // half is row t / 16 (+ 16 (q % 4)), stored chunk t % 16
+      const int rt = t >> 4;
+      const int n = min(n0 + 8 * ((t & 15) ^ (4 * (rt & 3))), (p.N - 1) & ~7);
+      voff = (uint32_t)((rt * p.ldb + n) * EB);
+      kt_bytes = (uint32_t)(BK * p.ldb * EB);
+      q_bytes = (uint32_t)(16 * p.ldb * EB);
+      qbase = B;
+      q_stride = 0;
+      const int whole = k_rows_bytes(p.ldb, p.N);
+      static_for<kCopies>([&](auto q) { recs[q] = whole; });
+    }
+  } else if constexpr (kBT) {
     if (grp == 1) {
       // slab chunk t + 256 q: row r0 = t / 32 (+ 8 q), stored chunk t % 32
       // holding columns n0 + 8 ((t % 32) ^ 4 (r0 % 4)) .. + 7
@@ -186,14 +209,18 @@ __device__ __forceinline__ void two_group_tile(const GroupedParams& p, const Til
   // Copy q of k-tile kt into `slot`.  A copy past the last k-tile still runs
   // (so the instruction stream and the wait counts never change) but with no
   // records: it writes zeros into a slot nobody reads any more.
+  // kTwo: copies 4 .. 7 of B are the up projection's, `up_by` bytes from the gate's
+  const int64_t up_by = kTwo && grp ? ts.B2 - ts.B : 0;
   auto copy_one = [&](int kt, int slot, bool live, auto q) {
+    const int qq = kTwo && grp ? (int)q % 4 : (int)q;
+    const uint8_t* base = qbase + (int64_t)qq * q_stride;
+    if constexpr (kTwo && q >= 4) base += up_by;
     const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
-        (void*)(qbase + (int64_t)q * q_stride), 0,
-        __builtin_amdgcn_readfirstlane(recs[q] & -(int)live), 0x00020000);
+        (void*)base, 0, __builtin_amdgcn_readfirstlane(recs[q] & -(int)live), 0x00020000);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(
         r, (__attribute__((address_space(3))) void*)(smem + lds_op + slot * SLAB + q * 4096 +
                                                      (wave & 3) * 1024),
-        16, kt == KTf ? voff_tail : voff, (uint32_t)kt * kt_bytes + (uint32_t)q * q_bytes, 0, 0);
+        16, kt == KTf ? voff_tail : voff, (uint32_t)kt * kt_bytes + (uint32_t)qq * q_bytes, 0, 0);
   };
   auto copy_slab = [&](int kt, int slot, bool live, auto n) {
     static_for<n>([&](auto q) { copy_one(kt, slot, live, q); });
@@ -211,8 +238,8 @@ __device__ __forceinline__ void two_group_tile(const GroupedParams& p, const Til
   static_assert(kSub == 1 || (Atom::kLaneBytes == 32 && kStepBytes % 32 == 0), "chunk pairs");
   uint32_t fa[kAT ? 1 : KSTEPS], fb[kBT ? 1 : KSTEPS];
   static_for<KSTEPS>([&](auto ks) {
-    const int c = (ks * kStepBytes + (lane >> 5) * Atom::kLaneBytes) / 16;
-    const int ra = wm0 + (lane & 31), rbw = wn0 + (lane & 31);
+    const int c = (ks * kStepBytes + lane / FR * Atom::kLaneBytes) / 16;
+    const int ra = wm0 + lane % FR, rbw = wb0 + lane % FR;
     if constexpr (!kAT) fa[ks] = (uint32_t)(ra * kRowBytes + Swz::chunk(ra, c) * 16);
     if constexpr (!kBT)
       fb[ks] = (uint32_t)(B_BASE + rbw * kRowBytes + Swz::chunk(rbw, c) * 16);  // B slot 0
@@ -245,11 +272,15 @@ __device__ __forceinline__ void two_group_tile(const GroupedParams& p, const Til
     // (ks = h = 0) serves all: + 8192 ks + 2048 h, and XOR 64 j for
     // fragment j
     const int qw = lane >> 4, a4 = lane & 15;
+    // (kTwo: rows of 128 columns, so + 4096 ks + 1024 h)
     const int k = 8 * (qw >> 1) + (a4 >> 2);
-    const int n = wn0 + 16 * (qw & 1) + 4 * (a4 & 3);
-    fb[0] = (uint32_t)(B_BASE + k * 512 + (((n >> 3) ^ (4 * (k & 3))) * 16) + (n & 7) * 2);
+    const int n = wb0 + 16 * (qw & 1) + 4 * (a4 & 3);
+    fb[0] = (uint32_t)(B_BASE + k * kRowBT + (((n >> 3) ^ (4 * (k & 3))) * 16) + (n & 7) * 2);
   }
-  Frag a[KSTEPS][FM], b[KSTEPS][FN];
+  // kBlocks: B's fragments half at a time, the second half read between the MFMAs
+  // (256 registers do not hold the sums, both operands and the partial sums)
+  constexpr int FB = kBlocks ? FN / 2 : FN;
+  Frag a[KSTEPS][FM], b[KSTEPS][FB];
   uint32_t xa[kShift ? KSTEPS : 1][FM], xb[kShift ? KSTEPS : 1][FN];
   auto lds_frag = [&](uint32_t base, int imm) -> Frag {
     if constexpr (kSub == 1) {
@@ -264,23 +295,27 @@ __device__ __forceinline__ void two_group_tile(const GroupedParams& p, const Til
   };
   // k-tile kt: A slot kt % 2 (immediate), B slot kt % 3 (in fb); afterwards
   // fb moves on to B slot (kt + 1) % 3
-  auto lds_frag_t = [&](uint32_t addr) -> Frag {
+  auto lds_frag_t = [&](uint32_t addr, auto row_bytes) -> Frag {
     typedef int s32x2 __attribute__((ext_vector_type(2)));
     const s16x4 lo = ds_read_tr16(smem + addr);
-    const s16x4 hi = ds_read_tr16(smem + addr + 2048);
+    const s16x4 hi = ds_read_tr16(smem + addr + 4 * row_bytes);
     const s32x2 l2 = __builtin_bit_cast(s32x2, lo), h2 = __builtin_bit_cast(s32x2, hi);
     return Frag{l2[0], l2[1], h2[0], h2[1]};
   };
   auto read_frag = [&](int kt, auto r) {
     constexpr int ks = r / (FM + FN), f = r % (FM + FN);
+    // B's MFMA tile: its place among the wave's columns, and the half slab
+    constexpr int j = kTwo ? (f - FM) % FH : f - FM, up = kTwo && f - FM >= FH ? SLAB / 2 : 0;
     if constexpr (f < FM && kAT)
-      a[ks][f] = lds_frag_t((fa[0] ^ (64u * f)) + 8192 * ks + (kt & 1) * SLAB);
+      a[ks][f] = lds_frag_t((fa[0] ^ (64u * f)) + 8192 * ks + (kt & 1) * SLAB,
+                            std::integral_constant<int, 512>{});
     else if constexpr (f < FM)
-      a[ks][f] = lds_frag(fa[ks], (kt & 1) * SLAB + f * 32 * kRowBytes);
+      a[ks][f] = lds_frag(fa[ks], (kt & 1) * SLAB + f * FR * kRowBytes);
     else if constexpr (kBT)
-      b[ks][f - FM] = lds_frag_t((fb[0] ^ (64u * (f - FM))) + 8192 * ks);
+      b[ks][f - FM] = lds_frag_t((fb[0] ^ (64u * j)) + 16 * kRowBT * ks + up,
+                                 std::integral_constant<int, kRowBT>{});
     else
-      b[ks][f - FM] = lds_frag(fb[ks], (f - FM) * 32 * kRowBytes);
+      b[ks][(f - FM) % FB] = lds_frag(fb[ks], j * FR * kRowBytes + up);
     if constexpr (kShift) {
       uint32_t base = (f < FM ? fa[ks] : fb[ks]) ^ (ks == 1 ? next1 : next02);
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -338,7 +373,7 @@ __device__ __forceinline__ void two_group_tile(const GroupedParams& p, const Til
   // kernel per k-tile of 256 x 256 x 128 bytes: 2508 cycles interleaved against 2590 with the
   // copies after the reads (16-bit), 3728 against 3952 (reads first) and
   // 4276 (copies first) for e4m3.
-  constexpr int kReads = KSTEPS * (FM + FN);  // fragments per k-tile
+  constexpr int kReads = KSTEPS * (FM + FB);  // fragments per k-tile
   // LDS read instructions of fragments [first, first + n)
   auto read_insts = [](int first, int n) constexpr {
     int c = 0;
@@ -346,8 +381,44 @@ __device__ __forceinline__ void two_group_tile(const GroupedParams& p, const Til
       c += kShift ? 2 : (r % (FM + FN) < FM) ? (kAT ? 2 : kSub) : (kBT ? 2 : kSub);
     return c;
   };
+  // kBlocks: the scales of a block of k.  Lane l asks for row wm0 + l's and, by
+  // its parity, for the gate's (or only) and the up projection's of the wave's
+  // columns, a period before they are used: two loads in front of the period's
+  // copies, so a wait for earlier copies leaves them in flight.
+  constexpr int kScaleLoads = kBlocks ? 2 : 0;
+  const float *sa_at = nullptr, *sb_at = nullptr;
+  float raw_a = 0.f, raw_b = 0.f, scale[2][FM];
+  if constexpr (kBlocks) {
+    sa_at = p.sa + (int64_t)min(m0 + wm0 + lane, m_end - 1) * p.sa_row;
+    sb_at = (kTwo && (lane & 1) ? p.sb2 : p.sb) + (int64_t)e * p.stride_sb +
+            (int64_t)(min(n0 + wb0, p.N - 1) >> 7) * p.sb_col;
+  }
+  auto ask_scales = [&](int kt) {
+    if constexpr (kBlocks) {
+      const int k = min(kt, KT - 1);
+      raw_a = sa_at[(int64_t)k * p.sa_kb];
+      raw_b = sb_at[(int64_t)k * p.sb_kb];
+    }
+  };
+  auto place_scales = [&]() {
+    if constexpr (kBlocks) {
+      static_for<kTwo ? 2 : 1>([&](auto h) {
+        const float s = raw_a * __builtin_bit_cast(float, __builtin_amdgcn_readlane(
+                                                              __builtin_bit_cast(int, raw_b), h));
+        static_for<FM>([&](auto i) {
+          scale[h][i] = __builtin_bit_cast(
+              float, __builtin_amdgcn_ds_bpermute(4 * (FR * i + lane % FR), __builtin_bit_cast(int, s)));
+        });
+      });
+    }
+  };
   auto memory_phase = [&](int kt, int ct, int slot, bool live, auto copies) {
     constexpr int kPer = kReads / copies, kRem = kReads % copies;
+    if constexpr (kBlocks) {
+      __builtin_amdgcn_sched_barrier(0);
+      place_scales();
+      ask_scales(kt + 1);
+    }
     __builtin_amdgcn_sched_barrier(0);
     static_for<copies>([&](auto q) {
       copy_one(ct, slot, live, q);
@@ -362,7 +433,7 @@ __device__ __forceinline__ void two_group_tile(const GroupedParams& p, const Til
       __builtin_amdgcn_sched_group_barrier(0x100, read_insts(first, n), 0);
     });
     place();
-    advance_b(kt);
+    if constexpr (!kBlocks) advance_b(kt);
     __builtin_amdgcn_sched_barrier(0);
   };
   typename Atom::Acc acc[FM][FN];
@@ -371,9 +442,15 @@ __device__ __forceinline__ void two_group_tile(const GroupedParams& p, const Til
   if constexpr (kForm == kGrad) sums.init();
   // one k-tile of MFMAs, fenced off from the scheduler on both sides so that
   // no wait or memory instruction of a neighbouring phase moves into it
-  auto compute = [&]() {
+  auto compute = [&](int kt) {
     __builtin_amdgcn_sched_barrier(0);
-    if (busy) {
+    if constexpr (kBlocks) {
+      if (busy)
+        blocks_mma<FM, FN, kTwo, kSub>(acc, a[0], b[0], scale, [&](auto j) {
+          read_frag(kt, std::integral_constant<int, FM + j + FB>{});
+        });
+      advance_b(kt);
+    } else if (busy) {
       static_for<KSTEPS * FM * FN>([&](auto idx) {
         constexpr int ks = idx / (FM * FN), i = (idx / FN) % FM, j = idx % FN;
         Atom::mma(acc[i][j], b[ks][j], a[ks][i]);
@@ -431,9 +508,12 @@ __device__ __forceinline__ void two_group_tile(const GroupedParams& p, const Til
   // epilogue pass begins with a trip to memory.
   [[maybe_unused]] uint32_t warm = 0;
   if constexpr (kForm != kGrad) {
-    const int64_t at = (int64_t)e * p.N + min(n0 + wn0 + 2 * lane, p.N - 1);
+    const int64_t at = (int64_t)e * p.N + min(n0 + wb0 + 2 * lane, p.N - 1);
     if (p.bias) warm = p.bias[at * type_bytes(p.bias_type)];
-    if constexpr (EB == 1) {
+    if constexpr (kTwo) {
+      if (p.bias2) warm += p.bias2[at * type_bytes(p.bias_type)];
+    }
+    if constexpr (EB == 1 && !kBlocks) {
       if (p.sb) warm += *(const uint8_t*)(p.sb + at);
     }
   }
@@ -444,6 +524,7 @@ __device__ __forceinline__ void two_group_tile(const GroupedParams& p, const Til
   };
   if (KT > 0) {
     if (grp == 0) {
+      ask_scales(0);
       copy_slab(0, 0, true, CopiesA{});
       wait_vmcnt<0>();
       warmed();
@@ -458,12 +539,13 @@ __device__ __forceinline__ void two_group_tile(const GroupedParams& p, const Til
         memory_phase(kt, kt + 1, (kt + 1) & 1, kt + 1 < KT, CopiesA{});
         wait_lgkmcnt0();
         barrier();
-        compute();
+        compute(kt);
         if constexpr (kForm != kGrad) pin();
         wait_vmcnt<0>();                             // A of kt+1 landed
         barrier();
       }
     } else {
+      ask_scales(0);
       copy_slab(0, 0, true, CopiesB{});
       copy_slab(1, 1, KT > 1, CopiesB{});
       wait_vmcnt<kCopies>();
@@ -481,7 +563,7 @@ __device__ __forceinline__ void two_group_tile(const GroupedParams& p, const Til
       for (int kt = 0; kt < KT; ++kt) {
         memory_phase(kt, kt + 2, (kt + 2) % 3, kt + 2 < KT, CopiesB{});
         wait_lgkmcnt0();
-        wait_vmcnt<kCopies>();                       // B of kt+1 landed
+        wait_vmcnt<kCopies + kScaleLoads>();         // B of kt+1 landed
         barrier();
         if constexpr (kForm != kGrad) {
           // while group 0 clears the last k-tile's A, before it reads it
@@ -490,7 +572,7 @@ __device__ __forceinline__ void two_group_tile(const GroupedParams& p, const Til
             barrier();
           }
         }
-        compute();
+        compute(kt);
         pin();
         if (kt + 1 < KT) barrier();
       }
@@ -500,13 +582,19 @@ __device__ __forceinline__ void two_group_tile(const GroupedParams& p, const Til
   // Every LDS read of the main loop finished before the last barrier and no
   // copy is in flight, so the slots are free for the epilogue: group 0
   // starts while group 1 still multiplies the last k-tile.
-  uint8_t* region = smem + wave * (32 * FM) * (64 * FN);
+  uint8_t* region = smem + wave * WM * WN * 2;
   if constexpr (kForm == kGrad) {
     if (sum_b) sums.template write<FN>(p.dbias + (int64_t)e * p.N, n0 + wn0, p.N, lane);
     if (sum_a) sums.template write<FM>(p.dbias + (int64_t)e * p.M, m0 + wm0, p.M, lane);
   }
   if constexpr (kForm == kGrad)
     wgrad_epilogue<FM, FN>(p, e, m0 + wm0, n0 + wn0, lane, acc, region);
+  else if constexpr (kRole == kGated)
+    gated_epilogue<FR, WM, WN / 2>(p, e, m_end, m0 + wm0, n0 + wb0, lane, acc, region);
+  else if constexpr (kRole == kGateGrad)
+    gate_grad_epilogue<WM, WN>(p, m_end, m0 + wm0, n0 + wn0, lane, acc, region);
+  else if constexpr (kBlocks)
+    blocks_epilogue<WM, WN>(p, e, m_end, m0 + wm0, n0 + wn0, lane, acc, region);
   else
     grouped_epilogue<kCode, FM, FN>(p, e, m_end, m0 + wm0, n0 + wn0, lane, acc, region);
 }
@@ -605,7 +693,7 @@ __device__ __forceinline__ bool two_group_lookup(const GroupedParams& p, int bid
   return false;
 }
 
-template <int kCode, int kForm>
+template <int kCode, int kForm, int kRole = kPlain>
 __global__ __launch_bounds__(512) void grouped_two_group_kernel(const GroupedParams p) {
   constexpr int EB = type_bytes(kCode);
   __shared__ __attribute__((aligned(1024))) uint8_t smem[kTwoGroupLds];
@@ -623,7 +711,7 @@ __global__ __launch_bounds__(512) void grouped_two_group_kernel(const GroupedPar
     ts.K = hi - lo;
     ts.A = p.A + (int64_t)lo * p.lda * EB;
     ts.B = p.B + (int64_t)lo * p.ldb * EB;
-    two_group_tile<kCode, kForm, false>(p, ts, smem);
+    two_group_tile<kCode, kForm, false, kRole>(p, ts, smem);
   } else {
     HalfTile t;
     if (!two_group_lookup(p, blockIdx.x, t)) return;
@@ -631,19 +719,20 @@ __global__ __launch_bounds__(512) void grouped_two_group_kernel(const GroupedPar
     ts.e = __builtin_amdgcn_readfirstlane(t.e);
     ts.m0 = __builtin_amdgcn_readfirstlane(t.r0);
     ts.m_end = __builtin_amdgcn_readfirstlane(t.r1);
-    ts.n0 = __builtin_amdgcn_readfirstlane(t.tn) * 256;
+    ts.n0 = __builtin_amdgcn_readfirstlane(t.tn) * (kRole == kGated ? 128 : 256);
     ts.K = p.K;
     ts.A = p.A;
     ts.B = p.B + (int64_t)ts.e * p.stride_b * EB;
-    if (t.half) two_group_tile<kCode, kForm, true>(p, ts, smem);
-    else two_group_tile<kCode, kForm, false>(p, ts, smem);
+    if constexpr (kRole == kGated) ts.B2 = p.B2 + (int64_t)ts.e * p.stride_b * EB;
+    if (t.half) two_group_tile<kCode, kForm, true, kRole>(p, ts, smem);
+    else two_group_tile<kCode, kForm, false, kRole>(p, ts, smem);
   }
 }
 
-template <int kCode, int kForm>
+template <int kCode, int kForm, int kRole = kPlain>
 int launch(const GroupedParams& p0, hipStream_t stream) {
   GroupedParams p = p0;
-  p.tiles_n = (p.N + 255) / 256;
+  p.tiles_n = kRole == kGated ? (p.N + 127) / 128 : (p.N + 255) / 256;
   p.tiles_m = (p.M + 255) / 256;
   // a split round adds fewer than 256 tiles
   const int64_t grid =
@@ -652,7 +741,7 @@ int launch(const GroupedParams& p0, hipStream_t stream) {
                             : row_tiles_bound(p.rows, p.groups, 256) * p.tiles_n + 256;
   if (grid <= 0) return TLA_OK;
   if (!grid_fits(grid, 512)) return TLA_ERR_UNSUPPORTED;
-  hipLaunchKernelGGL((grouped_two_group_kernel<kCode, kForm>), dim3((unsigned)grid), dim3(512), 0,
+  hipLaunchKernelGGL((grouped_two_group_kernel<kCode, kForm, kRole>), dim3((unsigned)grid), dim3(512), 0,
                      stream, p);
   return hipGetLastError() == hipSuccess ? TLA_OK : TLA_ERR_HIP;
 }

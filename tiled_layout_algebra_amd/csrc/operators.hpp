@@ -9,10 +9,11 @@
 namespace tla {
 
 constexpr int kI8 = TLA_I8;
+constexpr int kE4M3Blocks = 16;  // e4m3 with block scales: a kernel's operand code only
 
 // Bytes of an element of any type code of the public header.
 constexpr int type_bytes(int code) {
-  return code == TLA_F32 ? 4 : (code == TLA_E4M3 || code == TLA_I8 ? 1 : 2);
+  return code == TLA_F32 ? 4 : (code == TLA_E4M3 || code == TLA_I8 || code == kE4M3Blocks ? 1 : 2);
 }
 
 // One problem: rows r of A, grouped by expert (rows offsets[e] .. offsets[e +
@@ -37,13 +38,37 @@ struct GroupedParams {
   int d_type, bias_type, act, z_mode;
   int tiles_m, tiles_n;  // weight gradient: tiles of one D_e; product: tiles_n only
   int flags;
+  // gated product: the up projection beside the gate's B and bias, both kept
+  // pre-activations in Z (gate) and Z2 (up), D the hidden layer.  Its gradient:
+  // Z, Z2 read; D, D2 the gradients of gate and up; H the hidden layer or null.
+  const uint8_t *B2, *bias2;
+  uint8_t *Z2, *D2, *H;
+  int64_t ldh;
+  // block scales (sa: a row's, sb and sb2: of 128 columns): element strides of
+  // a row, a block of columns and a block of 128 k; distance between experts'
+  const float* sb2;
+  int64_t sa_row, sa_kb, sb_col, sb_kb, stride_sb;
 };
+// What a product's kernel makes of its sums.
+enum Role : int { kPlain = 0, kGated = 1, kGateGrad = 2 };
 enum : int {
   kOpD16 = 1,    // D (and Z) rows are 16-byte aligned
   kOpVec4 = 2,   // sb and bias rows allow aligned 4-element vectors
   kOpSumA = 4,   // gradient: dY is operand A (column-major D), else B
   kOpHalves = 8, // two-group product: blocks of 128 rows throughout
 };
+
+// What a validated call runs: the variant ids of the public header, or nothing.
+enum Kernel {
+  kNoop = -1, kGeneral, kTwoGroup, kDirect128, kDirect64, kFewRows4, kFewRows2, kFewRows1,
+  kTwoGroupShift, kDirect128Shift, kDirect64Shift
+};
+constexpr unsigned kAnyKernel = ~0u;
+// Of the kernels whose bit is set and that take the problem, the one with the
+// smallest estimated time, or kNoop; and whether the two-group kernel then cuts
+// its rows into half tiles throughout.  (operators_api.cpp)
+Kernel choose_product(const tla_grouped_gemm_args* a, int eb, bool b_kc, unsigned allowed);
+bool product_halves(const tla_grouped_gemm_args* a);
 
 // Blocks of BM rows that `rows` rows in `groups` groups can need: every
 // non-empty group's last block may hold a single row.
@@ -82,6 +107,26 @@ inline bool few_rows_narrow(int64_t rows, int64_t groups, int64_t N) {
   return (rows < groups ? rows : groups) * ((N + 31) / 32) <= 512;
 }
 int launch_grouped_few_rows(const GroupedParams& p, int type, int mt, hipStream_t stream);
+
+// The gated product (role kGated) and its gradient (kGateGrad) on the same
+// kernels, with the same conditions; 16-bit operands.
+int launch_gated_general(const GroupedParams& p, int type, bool b_kc, int role, hipStream_t stream);
+int launch_gated_two_group_nk(const GroupedParams& p, int type, int role, hipStream_t stream);
+int launch_gated_two_group_kn(const GroupedParams& p, int type, int role, hipStream_t stream);
+int launch_gated_direct_nk(const GroupedParams& p, int type, int shape, int role, hipStream_t stream);
+int launch_gated_direct_kn(const GroupedParams& p, int type, int role, hipStream_t stream);
+int launch_gated_few_rows(const GroupedParams& p, int type, int mt, hipStream_t stream);
+
+// e4m3 with block scales, B K-contiguous: 256 x 256, 128 x 128 and 64 x 128
+// tiles for rows that start on dwords less than 8 MiB apart, and the kernel for
+// few rows, which takes any.  gated: role kGated.
+int launch_blocks_two_group(const GroupedParams& p, bool gated, hipStream_t stream);
+int launch_blocks_direct(const GroupedParams& p, int bm, bool gated, hipStream_t stream);
+int launch_blocks_few_rows(const GroupedParams& p, int mt, bool gated, hipStream_t stream);
+
+int launch_quantize_blocks(int64_t M, int64_t K, const void* X, int type, int64_t ldx,
+                           int block_rows, uint8_t* Q, int64_t ldq, float* scale, int64_t s_row,
+                           int64_t s_kb, hipStream_t stream);
 
 int launch_quantize_rows(int64_t M, int64_t K, const void* X, int type, int64_t ldx, int8_t* Q,
                          int64_t ldq, float* scale, hipStream_t stream);

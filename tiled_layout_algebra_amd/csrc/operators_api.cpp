@@ -29,11 +29,6 @@ bool aux_type(int t) { return out16(t) || t == TLA_F32; }
 
 bool aligned_to(const void* p, int64_t bytes) { return (uintptr_t)p % (uintptr_t)bytes == 0; }
 
-// what a validated call runs: the variant ids of the public header, or nothing
-enum Kernel {
-  kNoop = -1, kGeneral, kTwoGroup, kDirect128, kDirect64, kFewRows4, kFewRows2, kFewRows1,
-  kTwoGroupShift, kDirect128Shift, kDirect64Shift
-};
 const char* const kNames[TLA_GROUPED_VARIANTS] = {
     "grouped_general_128x128", "grouped_two_group_256x256", "grouped_direct_128x128",
     "grouped_direct_64x128", "grouped_few_rows_64", "grouped_few_rows_32", "grouped_few_rows_16",
@@ -126,15 +121,15 @@ double two_group_rounds(const tla_grouped_gemm_args* a, bool halves) {
 // and in bf16 for 32 experts of 2048 x 4096: 128 rows 110 (few 16), 123
 // (64x128), 4096 rows 174 (64x128), 144 (128x128), 147 (256x256); for 8
 // experts of 4096 x 4096 with 2000 rows 129, 123, 89.
-Kernel choose(const tla_grouped_gemm_args* a, int eb, bool b_kc) {
+Kernel choose(const tla_grouped_gemm_args* a, int eb, bool b_kc, unsigned allowed) {
   const double live = (double)(a->rows < a->groups ? a->rows : a->groups);
   const double matrix = (double)a->N * (double)a->K * eb * 1e-6;  // MB
   const double weights = live * matrix / 5.0;
   const double kt = (double)((a->K * eb + 127) / 128);
-  Kernel best = kGeneral;
+  Kernel best = kNoop;
   double best_us = 1e30;
   auto consider = [&](Kernel k, double us) {
-    if (!takes(k, a, eb, b_kc)) return;
+    if (!(allowed >> k & 1) || !takes(k, a, eb, b_kc)) return;
     us = us > weights + 4.0 ? us : weights + 4.0;
     if (us < best_us) {
       best = k;
@@ -233,7 +228,7 @@ int plan_product(const tla_grouped_gemm_args* a, Plan* out) {
   if (!launches(kGeneral, a)) return TLA_ERR_UNSUPPORTED;
   out->type = a->type;
   out->b_kc = b_kc;
-  out->kernel = choose(a, eb, b_kc);
+  out->kernel = choose(a, eb, b_kc, kAnyKernel);
   return TLA_OK;
 }
 
@@ -247,7 +242,7 @@ int run_product(const tla_grouped_gemm_args* a, hipStream_t stream, int forced =
     plan.kernel = (Kernel)forced;
   }
   GroupedParams& p = plan.p;
-  if (two_group_rounds(a, true) < two_group_rounds(a, false)) p.flags |= kOpHalves;
+  if (product_halves(a)) p.flags |= kOpHalves;
   const int t = plan.type;
   switch (plan.kernel) {
     case kNoop: return TLA_OK;
@@ -276,6 +271,17 @@ int run_product(const tla_grouped_gemm_args* a, hipStream_t stream, int forced =
 }
 
 }  // namespace
+
+namespace tla {
+
+Kernel choose_product(const tla_grouped_gemm_args* a, int eb, bool b_kc, unsigned allowed) {
+  return choose(a, eb, b_kc, allowed);
+}
+bool product_halves(const tla_grouped_gemm_args* a) {
+  return two_group_rounds(a, true) < two_group_rounds(a, false);
+}
+
+}  // namespace tla
 
 extern "C" {
 
