@@ -338,7 +338,7 @@ int tla_quantize_rows(int64_t M, int64_t K, const void *X, int32_t x_type, int64
  * type F16 or BF16: any order, pitch and alignment to the element; the scales
  * are NULL.  type E4M3, with block scales as in tla_gemm_blocks: scale_x of X's
  * rows, scale_gate and scale_up of each 128 x 128 block, TLA_COL_MAJOR weights
- * only.  H, Z: F16 or BF16 (h_type), row-major.  Biases (groups x N, dense, or
+ * only.  H, Z: row-major, h_type: type, or for E4M3 F16 or BF16.  Biases (groups x N, dense, or
  * NULL) F16, BF16 or F32.  act: any of tla_act.  Sums and the epilogue are fp32,
  * each output is rounded once.  SiLU is z times the sigmoid, so SiLU(-inf) is
  * NaN; the sigmoid is off by at most (|z| + 4) 2^-24 of its value and is 0 below
@@ -369,14 +369,13 @@ int tla_gated_gemm(const tla_gated_gemm_args *args, void *stream);
  * hidden layer, the down projection read in the other order:
  *   dh[r, n] = sum_k dY[r, k] W_e(k, n)             (never stored)
  *   dZ_gate = dh u act'(g),  dZ_up = dh act(g),  H = act(g) u unless NULL
- * with g = Z_gate, u = Z_up as the forward pass kept them, in d_type like the
- * outputs.  act' of tla_grouped_gemm; SiLU': p + z p (1 - p), p the sigmoid; 1
+ * with g = Z_gate, u = Z_up as the forward pass kept them.  act' of tla_grouped_gemm; SiLU': p + z p (1 - p), p the sigmoid; 1
  * without an activation.  H lets a program drop the hidden layer after the
  * forward pass; it is what the down projection's weight gradient reads.
  * The rest of the backward pass: dX = dZ_gate Wg^T + dZ_up Wu^T (one product
  * where they are halves of a buffer), the weight and bias gradients
  * tla_grouped_gemm_wgrad.
- * type (dY and W) F16 or BF16.  Outputs must not overlap each other or an input.
+ * type F16 or BF16, of everything (d_type: the same).  Outputs must not overlap each other or an input.
  * K == 0 gives dh = 0.  The rest as above, with N columns in the extents.
  */
 typedef struct {

@@ -53,6 +53,7 @@ SHARED = [
 ]
 GATED = SHARED + [
     (dict(w_order=2), I), (dict(type=tla.F32), U), (dict(type=tla.I8), U), (dict(h_type=tla.F32), U),
+    (dict(h_type=tla.F16), U), (dict(SCALED, h_type=tla.F32), U),
     (dict(b_gate=FAKE, bias_type=tla.I8), U), (dict(b_up=FAKE, bias_type=5), U),
     (dict(scale_x=FAKE), U), (dict(scale_gate=FAKE), U), (dict(scale_up=FAKE), U),
     (dict(X=None), I), (dict(W_gate=None), I), (dict(W_up=None), I), (dict(H=None), I),
@@ -69,7 +70,7 @@ GATED = SHARED + [
 ]
 GRAD = SHARED + [
     (dict(w_order=2), I), (dict(type=tla.F32), U), (dict(type=tla.E4M3), U), (dict(d_type=tla.F32), U),
-    (dict(dY=None), I), (dict(W=None), I), (dict(Z_gate=None), I), (dict(Z_up=None), I),
+    (dict(d_type=tla.F16), U), (dict(dY=None), I), (dict(W=None), I), (dict(Z_gate=None), I), (dict(Z_up=None), I),
     (dict(dZ_gate=None), I), (dict(dZ_up=None), I), (dict(ldy=63), I), (dict(ldw=63), I),
     (dict(ldz=63), I), (dict(ldd=63), I), (dict(ldh=63), I), (dict(stride_w=-1), I),
     (dict(dZ_gate=5 * FAKE), I), (dict(H=4 * FAKE), I), (dict(dZ_up=2 * FAKE), I), (dict(H=3 * FAKE), I),

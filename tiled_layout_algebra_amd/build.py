@@ -23,7 +23,8 @@ SOURCES = ["api.cpp", "algebra.cpp", "gemm.hip", "gemm_general.hip", "gemm_pingp
            "grouped_few_rows.hip", "grouped_general.hip", "grouped_two_group.hip", "grouped_two_group_8bit.hip",
            "grouped_two_group_rows.hip", "grouped_two_group_shift.hip", "quantize.hip",
            "gated_api.cpp", "gated_direct.hip", "gated_few_rows.hip", "gated_general.hip",
-           "gated_two_group.hip", "gated_two_group_rows.hip", "blocks_direct.hip",
+           "gated_two_group_gated_nk.hip", "gated_two_group_gated_kn.hip",
+           "gated_two_group_grad_nk.hip", "gated_two_group_grad_kn.hip", "blocks_direct.hip",
            "blocks_few_rows.hip", "blocks_two_group.hip", "quantize_blocks.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -119,7 +119,7 @@ __global__ __launch_bounds__(64 * kWM * kWN) void blocks_direct_kernel(const Gro
       constexpr int at = kTwo ? j % FH * 16 * kRowBytes + j / FH * (SLAB_B / 2) : j * 16 * kRowBytes;
       b[j] = frag(fb + S * STAGE + SLAB_A + at);
     });
-    blocks_mma<FM, FN, kTwo, 0>(acc, a, b, s, [](auto) {});
+    blocks_mma<FM, FN, kTwo>(acc, a, b, s, [](auto) {});
   };
   if (KT > 0) {
     // the first tile's scales before its copies, so that the loop's first wait covers them
@@ -134,10 +134,8 @@ __global__ __launch_bounds__(64 * kWM * kWN) void blocks_direct_kernel(const Gro
   }
   __syncthreads();  // the stages become the waves' epilogue regions
   uint8_t* region = smem + wave * WM * WN * 2;
-  if constexpr (kTwo)
-    gated_epilogue<16, WM, WN / 2>(p, e, m_end, m0 + wm0, n0 + wb0, lane, acc, region);
-  else
-    blocks_epilogue<WM, WN>(p, e, m_end, m0 + wm0, n0 + wn0, lane, acc, region);
+  role_epilogue<kE4M3Blocks, kTwo ? kGated : kPlain, 0, 16, WM, kTwo ? WN / 2 : WN>(
+      p, e, m_end, m0 + wm0, n0 + wb0, lane, acc, region);
 }
 
 template <int BM, int kStages, int kWM, int kWN, bool kTwo>

@@ -5,7 +5,7 @@
 namespace tla {
 
 int launch_blocks_two_group(const GroupedParams& p, bool gated, hipStream_t s) {
-  return gated ? launch<kE4M3Blocks, kNK, kGated>(p, s) : launch<kE4M3Blocks, kNK>(p, s);
+  return gated ? launch_act<kE4M3Blocks, kNK, kGated>(p, s) : launch_act<kE4M3Blocks, kNK, kPlain>(p, s);
 }
 
 }  // namespace tla

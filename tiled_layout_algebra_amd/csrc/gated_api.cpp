@@ -79,8 +79,9 @@ int run(const Plan& plan, hipStream_t s) {
   }
   switch (plan.kernel) {
     case kTwoGroup:
-      return plan.b_kc ? launch_gated_two_group_nk(p, t, role, s)
-                       : launch_gated_two_group_kn(p, t, role, s);
+      if (role == kGated)
+        return plan.b_kc ? launch_two_group_gated_nk(p, t, s) : launch_two_group_gated_kn(p, t, s);
+      return plan.b_kc ? launch_two_group_grad_nk(p, t, s) : launch_two_group_grad_kn(p, t, s);
     case kDirect128:
       return plan.b_kc ? launch_gated_direct_nk(p, t, kDirect128x3, role, s)
                        : launch_gated_direct_kn(p, t, role, s);
@@ -110,7 +111,7 @@ int plan_gated(const tla_gated_gemm_args* a, Plan* out, int forced) {
   if (const int rc = check_shape(a->groups, a->rows, a->N, a->K, a->act, a->w_order)) return rc;
   const bool blocks = a->type == TLA_E4M3;
   if (!blocks && !out16(a->type)) return TLA_ERR_UNSUPPORTED;
-  if (!out16(a->h_type)) return TLA_ERR_UNSUPPORTED;
+  if (blocks ? !out16(a->h_type) : a->h_type != a->type) return TLA_ERR_UNSUPPORTED;
   if ((a->b_gate || a->b_up) && !aux_type(a->bias_type)) return TLA_ERR_UNSUPPORTED;
   const bool b_kc = a->w_order == TLA_COL_MAJOR;
   if (blocks ? !b_kc : a->scale_x || a->scale_gate || a->scale_up) return TLA_ERR_UNSUPPORTED;
@@ -187,7 +188,7 @@ int plan_grad(const tla_gated_grad_args* a, Plan* out, int forced) {
   out->kernel = kNoop;
   if (!a) return TLA_ERR_INVALID_ARG;
   if (const int rc = check_shape(a->groups, a->rows, a->N, a->K, a->act, a->w_order)) return rc;
-  if (!out16(a->type) || !out16(a->d_type)) return TLA_ERR_UNSUPPORTED;
+  if (!out16(a->type) || a->d_type != a->type) return TLA_ERR_UNSUPPORTED;
   if (a->groups == 0 || a->rows == 0 || a->N == 0) return TLA_OK;
   if (!a->offsets && a->groups != 1) return TLA_ERR_INVALID_ARG;
   const bool b_kc = a->w_order == TLA_COL_MAJOR;

@@ -32,9 +32,8 @@ namespace {
 // these follow each other without waiting for a result.  s[0]: the scales of the
 // plain sums or of the first half of the columns (the gate's), s[1]: of the
 // other half.  b holds FB of the FN column fragments; after(j) is called behind
-// the last use of fragment j and issues kReads LDS reads where j + FB < FN, for
-// fragment j + FB in its place.
-template <int FM, int FN, bool kTwo, int kReads, int FB, class F>
+// the last use of fragment j where j + FB < FN, to read fragment j + FB in its place.
+template <int FM, int FN, bool kTwo, int FB, class F>
 __device__ __forceinline__ void blocks_mma(f32x4 (&acc)[FM][FN], const i32x8 (&a)[FM],
                                            i32x8 (&b)[FB], const float (&s)[2][FM], F&& after) {
   constexpr int kN = FM * FN, kAhead = kN < 4 ? kN : 4;
@@ -51,14 +50,7 @@ __device__ __forceinline__ void blocks_mma(f32x4 (&acc)[FM][FN], const i32x8 (&a
       part[x % kAhead] = OpAtom<kE4M3Blocks>::block(b[x / FM % FB], a[x % FM]);
       if constexpr (x % FM == FM - 1 && x / FM + FB < FN) after(std::integral_constant<int, x / FM>{});
     }
-  });
-  static_for<kN + kAhead>([&](auto x) {
-    if constexpr (x >= kAhead) __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
-    if constexpr (x < kN) {
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-      if constexpr (x % FM == FM - 1 && x / FM + FB < FN)
-        __builtin_amdgcn_sched_group_barrier(0x100, kReads, 0);
-    }
+    __builtin_amdgcn_sched_barrier(0);  // in this order
   });
 }
 
@@ -69,52 +61,111 @@ __device__ __forceinline__ float sigmoid(float z) {
   return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * -1.44269504f));
 }
 
+// The activation of a kernel: kLinear is ReLU, or with p.act TLA_ACT_NONE nothing
+// (one code for both), the others themselves.
+enum Act : int { kLinear = TLA_ACT_RELU, kGeluAct = TLA_ACT_GELU, kSiluAct = TLA_ACT_SILU };
 template <int kAct>
-__device__ __forceinline__ float act_value(float z) {
-  if constexpr (kAct == TLA_ACT_RELU) return relu_nan(z);
-  if constexpr (kAct == TLA_ACT_GELU) return gelu_nan(z);
-  if constexpr (kAct == TLA_ACT_SILU) return z * sigmoid(z);
-  return z;
+__device__ __forceinline__ float act_value(float z, bool none) {
+  if constexpr (kAct == kGeluAct) return gelu_nan(z);
+  if constexpr (kAct == kSiluAct) return z * sigmoid(z);
+  return z < 0.f && !none ? 0.f : z;
 }
 // act(z) and act'(z); SiLU: p + z p (1 - p), p = sigmoid(z)
 template <int kAct>
-__device__ __forceinline__ void act_both(float z, float& value, float& slope) {
-  if constexpr (kAct == TLA_ACT_SILU) {
+__device__ __forceinline__ void act_both(float z, bool none, float& value, float& slope) {
+  if constexpr (kAct == kSiluAct) {
     const float s = sigmoid(z);
     value = z * s;
     slope = fmaf(value, 1.f - s, s);
   } else {
-    value = act_value<kAct>(z);
-    slope = kAct == TLA_ACT_RELU ? (z > 0.f ? 1.f : 0.f) : kAct == TLA_ACT_GELU ? gelu_slope(z) : 1.f;
+    value = act_value<kAct>(z, none);
+    slope = kAct == kGeluAct ? gelu_slope(z) : z > 0.f || none ? 1.f : 0.f;
   }
 }
-// f(integral_constant<act>)
+// f(integral_constant<Act>) for p.act
 template <class F>
 __device__ __forceinline__ void with_act(int act, F&& f) {
-  if (act == TLA_ACT_SILU) f(std::integral_constant<int, TLA_ACT_SILU>{});
-  else if (act == TLA_ACT_GELU) f(std::integral_constant<int, TLA_ACT_GELU>{});
-  else if (act == TLA_ACT_RELU) f(std::integral_constant<int, TLA_ACT_RELU>{});
-  else f(std::integral_constant<int, TLA_ACT_NONE>{});
+  if (act == TLA_ACT_SILU) f(std::integral_constant<int, kSiluAct>{});
+  else if (act == TLA_ACT_GELU) f(std::integral_constant<int, kGeluAct>{});
+  else f(std::integral_constant<int, kLinear>{});
 }
 __device__ __forceinline__ float act_any(float z, int act) {
   float y = z;
-  with_act(act, [&](auto a) { y = act_value<a>(z); });
+  with_act(act, [&](auto a) { y = act_value<a>(z, act == TLA_ACT_NONE); });
   return y;
 }
 
-// A wave's piece of a row-major 16-bit matrix in LDS (WaveRegion) seen from MFMA
-// tiles of FR rows: FR 32: lane l holds row 32 i + l % 32, columns 32 j + 8 g + 4
-// (l / 32) .. + 3; FR 16: row 16 i + l % 16, columns 16 j + 4 (l / 16) .. + 3.
+// A wave's WM x WN piece of a row-major 16-bit matrix in LDS (WaveRegion) seen from
+// MFMA tiles of FR rows: FR 32: lane l holds row 32 i + l % 32, columns 32 j + 8 g +
+// 4 (l / 32) .. + 3; FR 16: row 16 i + l % 16, columns 16 j + 4 (l / 16) .. + 3.
+// Pieces that end inside the matrix take loops that are not unrolled: the edge's
+// code is a small part of the kernel's, which the instruction cache has to hold.
 template <int FR, int WM, int WN>
 struct Piece {
   using R = WaveRegion<WM / 32, WN / 32>;
-  static constexpr int kG = FR == 32 ? 4 : 1, kBytes = WM * WN * 2;
+  static constexpr int kG = FR == 32 ? 4 : 1, kBytes = WM * WN * 2, kIters = R::kIters;
   static __device__ __forceinline__ int column(int lane, int j, int g) {
     return FR * j + 8 * g + 4 * (lane / FR);
   }
   static __device__ __forceinline__ uint2* slot(uint8_t* region, int lane, int i, int j, int g) {
     const int r = FR * i + lane % FR, c = column(lane, j, g);
     return (uint2*)(region + r * R::kRowB + R::swz(r, c / 8) * 16 + (c & 4) * 2);
+  }
+  // row and first column of the 16-byte chunk at region + 1024 t + 16 lane
+  static __device__ __forceinline__ int row(int lane, int t) { return R::kRowsPerKiB * t + lane / R::kCh; }
+  static __device__ __forceinline__ int chunk(int lane, int t) { return 8 * R::swz(row(lane, t), lane % R::kCh); }
+  static __device__ __forceinline__ bool whole(int rows, int cols) { return rows >= WM && cols >= WN; }
+  // a whole piece into registers, from there into the region
+  static __device__ __forceinline__ void fetch(const uint8_t* base, int64_t ld, i32x4 (&v)[kIters], int lane) {
+    const uint8_t* from = base + (int64_t)(lane / R::kCh) * ld * 2;
+#pragma unroll
+    for (int t = 0; t < kIters; ++t)
+      v[t] = load16_even(from + (int64_t)(R::kRowsPerKiB * t) * ld * 2 + chunk(lane, t) * 2);
+  }
+  static __device__ __forceinline__ void put(const i32x4 (&v)[kIters], uint8_t* region, int lane) {
+#pragma unroll
+    for (int t = 0; t < kIters; ++t) *(i32x4*)(region + t * 1024 + lane * 16) = v[t];
+  }
+  // rows x cols of a piece straight into the region (the rest of it: anything)
+  static __device__ __forceinline__ void load_edge(const uint8_t* base, int64_t ld, uint8_t* region,
+                                                   int lane, int rows, int cols) {
+#pragma unroll 1
+    for (int t = 0; t < kIters; ++t) {
+      const int c = chunk(lane, t);
+      const uint16_t* src = (const uint16_t*)base + (int64_t)min(row(lane, t), rows - 1) * ld;
+      uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[e / 2] |= (uint32_t)src[min(c + e, cols - 1)] << (16 * (e & 1));
+      *(i32x4*)(region + t * 1024 + lane * 16) = i32x4{(int)w[0], (int)w[1], (int)w[2], (int)w[3]};
+    }
+  }
+  // region -> rows x cols of the matrix; v16: its rows are 16-byte aligned
+  static __device__ __forceinline__ void store(uint8_t* base, int64_t ld, const uint8_t* region,
+                                               int lane, int rows, int cols, bool v16) {
+    if (whole(rows, cols)) {
+      uint8_t* to = base + (int64_t)(lane / R::kCh) * ld * 2;
+#pragma unroll
+      for (int t = 0; t < kIters; ++t) {
+        const i32x4 v = *(const i32x4*)(region + t * 1024 + lane * 16);
+        uint8_t* dst = to + (int64_t)(R::kRowsPerKiB * t) * ld * 2 + chunk(lane, t) * 2;
+        if (v16) *(i32x4*)dst = v;
+        else store16_even(dst, v);
+      }
+      return;
+    }
+#pragma unroll 1
+    for (int t = 0; t < kIters; ++t) {
+      const i32x4 v = *(const i32x4*)(region + t * 1024 + lane * 16);
+      const int r = row(lane, t), c = chunk(lane, t);
+      uint8_t* dst = base + ((int64_t)r * ld + c) * 2;
+      if (r < rows && c + 8 <= cols) {
+        store16_even(dst, v);
+      } else if (r < rows) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (c + e < cols) ((uint16_t*)dst)[e] = (uint16_t)((uint32_t)v[e >> 1] >> (16 * (e & 1)));
+      }
+    }
   }
 };
 
@@ -147,15 +198,14 @@ __device__ __forceinline__ void pair_pass(int lane, const Acc (&acc)[FM][FN], ui
 // (WN of them) of the hidden layer, the expert's rows end at r1; tiles j < FN / 2
 // are the gate's, the others the up projection's.  fp32 throughout, one rounding
 // for each output.  region: 2 WM WN 16-bit values.
-template <int FR, int WM, int WN, class Acc, int FM, int FN>
+template <int FR, int WM, int WN, int kAct, bool kBf, class Acc, int FM, int FN>
 __device__ __forceinline__ void gated_epilogue(const GroupedParams& p, int e, int r1, int row,
                                                int col, int lane, Acc (&acc)[FM][FN],
                                                uint8_t* region) {
   using P = Piece<FR, WM, WN>;
-  using R = typename P::R;
   const int rows = min(WM, r1 - row), cols = min(WN, p.N - col);
   if (rows <= 0 || cols <= 0) return;
-  const bool v16 = p.flags & kOpD16;
+  const bool v16 = p.flags & kOpD16, none = p.act == TLA_ACT_NONE;
   if (p.bias || p.bias2) {
     static_for<FN>([&](auto j) {
       const uint8_t* bias = j < FN / 2 ? p.bias : p.bias2;
@@ -169,134 +219,153 @@ __device__ __forceinline__ void gated_epilogue(const GroupedParams& p, int e, in
       }
     });
   }
-  auto run = [&](auto kb) {
-    if (p.Z) {
-      pair_pass<FR, WM, WN, kb>(lane, acc, region, [](float g, float) { return g; });
-      pair_pass<FR, WM, WN, kb>(lane, acc, region + P::kBytes, [](float, float u) { return u; });
-      wave_fence();
-      const int64_t at = ((int64_t)row * p.ldz + col) * 2;
-      R::store(p.Z + at, p.ldz, region, lane, rows, cols, v16);
-      R::store(p.Z2 + at, p.ldz, region + P::kBytes, lane, rows, cols, v16);
-      wave_fence();
-    }
-    with_act(p.act, [&](auto act) {
-      constexpr int kAct = act;
-      pair_pass<FR, WM, WN, kb>(lane, acc, region,
-                                [](float g, float u) { return act_value<kAct>(g) * u; });
-    });
+  if (p.Z) {
+    pair_pass<FR, WM, WN, kBf>(lane, acc, region, [](float g, float) { return g; });
+    pair_pass<FR, WM, WN, kBf>(lane, acc, region + P::kBytes, [](float, float u) { return u; });
     wave_fence();
-    R::store(p.D + ((int64_t)row * p.ldd + col) * 2, p.ldd, region, lane, rows, cols, v16);
-  };
-  if (p.d_type == TLA_BF16) run(std::true_type{});
-  else run(std::false_type{});
+    const int64_t at = ((int64_t)row * p.ldz + col) * 2;
+    P::store(p.Z + at, p.ldz, region, lane, rows, cols, v16);
+    P::store(p.Z2 + at, p.ldz, region + P::kBytes, lane, rows, cols, v16);
+    wave_fence();
+  }
+  pair_pass<FR, WM, WN, kBf>(lane, acc, region,
+                             [&](float g, float u) { return act_value<kAct>(g, none) * u; });
+  wave_fence();
+  P::store(p.D + ((int64_t)row * p.ldd + col) * 2, p.ldd, region, lane, rows, cols, v16);
 }
 
 // The gradient's epilogue: acc is dh; D = dh up act'(gate), D2 = dh act(gate),
 // H = act(gate) up with gate and up read from Z and Z2.  WN columns in parts of
-// half of them (or all 32): a part's gate and up go through LDS as whole rows,
-// the gradients back the same way, the hidden layer waits in the sums' registers.
-// region: WM WN 16-bit values, 2 WM WN for WN = 32.
-template <int WM, int WN, int FM, int FN>
+// half of them (or all 32): a part's gate and up come as whole rows into registers
+// (the fragments' are free) while the part before is worked on, and go through LDS;
+// the gradients go back the same way, the hidden layer waits in the sums'
+// registers.  region: WM WN 16-bit values, 2 WM WN for WN = 32.
+template <int WM, int WN, int kAct, bool kBf, int FM, int FN>
 __device__ __forceinline__ void gate_grad_epilogue(const GroupedParams& p, int r1, int row, int col,
                                                    int lane, f32x16 (&acc)[FM][FN],
                                                    uint8_t* region) {
-  constexpr int kPart = WN >= 64 ? WN / 2 : WN, FP = kPart / 32;
+  constexpr int kPart = WN >= 64 ? WN / 2 : WN, FP = kPart / 32, kParts = WN / kPart;
   using P = Piece<32, WM, kPart>;
-  using R = typename P::R;
   const int rows = min(WM, r1 - row);
-  if (rows <= 0) return;
-  const bool v16 = p.flags & kOpD16;
+  if (rows <= 0 || col >= p.N) return;
+  const bool v16 = p.flags & kOpD16, none = p.act == TLA_ACT_NONE;
   uint8_t* region2 = region + P::kBytes;
-  auto run = [&](auto kb, auto act) {
-    static_for<WN / kPart>([&](auto part) {
-      const int c = col + part * kPart, cols = min(kPart, p.N - c);
-      if (cols <= 0) return;
-      const int64_t zat = ((int64_t)row * p.ldz + c) * 2, dat = ((int64_t)row * p.ldd + c) * 2;
-      R::load(p.Z + zat, p.ldz, region, lane, rows, cols);
-      R::load(p.Z2 + zat, p.ldz, region2, lane, rows, cols);
-      wave_fence();
+  i32x4 zg[P::kIters], zu[P::kIters];
+  auto ask = [&](int part) {
+    const int c = col + part * kPart;
+    const int64_t at = ((int64_t)row * p.ldz + c) * 2;
+    if (P::whole(rows, p.N - c)) {
+      P::fetch(p.Z + at, p.ldz, zg, lane);
+      P::fetch(p.Z2 + at, p.ldz, zu, lane);
+    }
+  };
+  ask(0);
+  static_for<kParts>([&](auto part) {
+    const int c = col + part * kPart, cols = min(kPart, p.N - c);
+    if (cols <= 0) return;
+    const int64_t dat = ((int64_t)row * p.ldd + c) * 2, zat = ((int64_t)row * p.ldz + c) * 2;
+    if (P::whole(rows, cols)) {
+      P::put(zg, region, lane);
+      P::put(zu, region2, lane);
+    } else {
+      P::load_edge(p.Z + zat, p.ldz, region, lane, rows, cols);
+      P::load_edge(p.Z2 + zat, p.ldz, region2, lane, rows, cols);
+    }
+    if constexpr (part + 1 < kParts) ask(part + 1);
+    wave_fence();
+    static_for<FP>([&](auto jj) {
+      constexpr int j = part * FP + jj;
+      static_for<4>([&](auto g) {
+        static_for<FM>([&](auto i) {
+          uint2 *gate = P::slot(region, lane, i, jj, g), *up = P::slot(region2, lane, i, jj, g);
+          const uint2 wg = *gate, wu = *up;
+          const float g4[4] = {widen_lo<kBf>(wg.x), widen_hi<kBf>(wg.x), widen_lo<kBf>(wg.y),
+                               widen_hi<kBf>(wg.y)};
+          const float u4[4] = {widen_lo<kBf>(wu.x), widen_hi<kBf>(wu.x), widen_lo<kBf>(wu.y),
+                               widen_hi<kBf>(wu.y)};
+          float dg[4], du[4];
+          static_for<4>([&](auto q) {
+            float value, slope;
+            act_both<kAct>(g4[q], none, value, slope);
+            const float dh = acc[i][j][4 * g + q];
+            dg[q] = dh * (u4[q] * slope);
+            du[q] = dh * value;
+            acc[i][j][4 * g + q] = value * u4[q];
+          });
+          *gate = uint2{pack2<kBf>(dg[0], dg[1]), pack2<kBf>(dg[2], dg[3])};
+          *up = uint2{pack2<kBf>(du[0], du[1]), pack2<kBf>(du[2], du[3])};
+        });
+      });
+    });
+    wave_fence();
+    P::store(p.D + dat, p.ldd, region, lane, rows, cols, v16);
+    P::store(p.D2 + dat, p.ldd, region2, lane, rows, cols, v16);
+    wave_fence();
+    if (p.H) {
       static_for<FP>([&](auto jj) {
         constexpr int j = part * FP + jj;
         static_for<4>([&](auto g) {
           static_for<FM>([&](auto i) {
-            uint2 *gate = P::slot(region, lane, i, jj, g), *up = P::slot(region2, lane, i, jj, g);
-            const uint2 zg = *gate, zu = *up;
-            const float g4[4] = {widen_lo<kb>(zg.x), widen_hi<kb>(zg.x), widen_lo<kb>(zg.y),
-                                 widen_hi<kb>(zg.y)};
-            const float u4[4] = {widen_lo<kb>(zu.x), widen_hi<kb>(zu.x), widen_lo<kb>(zu.y),
-                                 widen_hi<kb>(zu.y)};
-            float dg[4], du[4];
-            static_for<4>([&](auto q) {
-              float value, slope;
-              act_both<act>(g4[q], value, slope);
-              const float dh = acc[i][j][4 * g + q];
-              dg[q] = dh * (u4[q] * slope);
-              du[q] = dh * value;
-              acc[i][j][4 * g + q] = value * u4[q];
-            });
-            *gate = uint2{pack2<kb>(dg[0], dg[1]), pack2<kb>(dg[2], dg[3])};
-            *up = uint2{pack2<kb>(du[0], du[1]), pack2<kb>(du[2], du[3])};
+            *P::slot(region, lane, i, jj, g) =
+                uint2{pack2<kBf>(acc[i][j][4 * g], acc[i][j][4 * g + 1]),
+                      pack2<kBf>(acc[i][j][4 * g + 2], acc[i][j][4 * g + 3])};
           });
         });
       });
       wave_fence();
-      R::store(p.D + dat, p.ldd, region, lane, rows, cols, v16);
-      R::store(p.D2 + dat, p.ldd, region2, lane, rows, cols, v16);
+      P::store(p.H + ((int64_t)row * p.ldh + c) * 2, p.ldh, region, lane, rows, cols, v16);
       wave_fence();
-      if (p.H) {
-        static_for<FP>([&](auto jj) {
-          constexpr int j = part * FP + jj;
-          static_for<4>([&](auto g) {
-            static_for<FM>([&](auto i) {
-              *P::slot(region, lane, i, jj, g) =
-                  uint2{pack2<kb>(acc[i][j][4 * g], acc[i][j][4 * g + 1]),
-                        pack2<kb>(acc[i][j][4 * g + 2], acc[i][j][4 * g + 3])};
-            });
-          });
-        });
-        wave_fence();
-        R::store(p.H + ((int64_t)row * p.ldh + c) * 2, p.ldh, region, lane, rows, cols, v16);
-        wave_fence();
-      }
-    });
-  };
-  with_act(p.act, [&](auto act) {
-    if (p.d_type == TLA_BF16) run(std::true_type{}, act);
-    else run(std::false_type{}, act);
+    }
   });
 }
 
 // The block-scaled product's epilogue: D = act(sum + bias).
-template <int WM, int WN, int FM, int FN>
+template <int WM, int WN, int kAct, bool kBf, int FM, int FN>
 __device__ __forceinline__ void blocks_epilogue(const GroupedParams& p, int e, int r1, int row,
                                                 int col, int lane, f32x4 (&acc)[FM][FN],
                                                 uint8_t* region) {
   using P = Piece<16, WM, WN>;
-  using R = typename P::R;
   const int rows = min(WM, r1 - row), cols = min(WN, p.N - col);
   if (rows <= 0 || cols <= 0) return;
+  const bool none = p.act == TLA_ACT_NONE;
   if (p.bias) {
     static_for<FN>([&](auto j) {
       const f32x4 b = bias4(p, p.bias, e, col + P::column(lane, j, 0));
       static_for<FM>([&](auto i) { acc[i][j] += b; });
     });
   }
-  auto run = [&](auto kb) {
-    with_act(p.act, [&](auto act) {
-      static_for<FN>([&](auto j) {
-        static_for<FM>([&](auto i) {
-          float y[4];
-          static_for<4>([&](auto q) { y[q] = act_value<act>(acc[i][j][(int)q]); });
-          *P::slot(region, lane, i, j, 0) = uint2{pack2<kb>(y[0], y[1]), pack2<kb>(y[2], y[3])};
-        });
-      });
+  static_for<FN>([&](auto j) {
+    static_for<FM>([&](auto i) {
+      float y[4];
+      static_for<4>([&](auto q) { y[q] = act_value<kAct>(acc[i][j][(int)q], none); });
+      *P::slot(region, lane, i, j, 0) = uint2{pack2<kBf>(y[0], y[1]), pack2<kBf>(y[2], y[3])};
     });
-    wave_fence();
-    R::store(p.D + ((int64_t)row * p.ldd + col) * 2, p.ldd, region, lane, rows, cols,
-             p.flags & kOpD16);
+  });
+  wave_fence();
+  P::store(p.D + ((int64_t)row * p.ldd + col) * 2, p.ldd, region, lane, rows, cols, p.flags & kOpD16);
+}
+
+// A wave's epilogue in the role and operand code of its kernel.  16-bit roles: the
+// outputs have the operands' type.  The two-group kernel is compiled for each
+// activation (kAct > 0), the others branch.
+template <int kCode, int kRole, int kAct, int FR, int WM, int WN, class Acc, int FM, int FN>
+__device__ __forceinline__ void role_epilogue(const GroupedParams& p, int e, int r1, int row, int col,
+                                              int lane, Acc (&acc)[FM][FN], uint8_t* region) {
+  auto run = [&](auto act, auto bf) {
+    if constexpr (kRole == kGated)
+      gated_epilogue<FR, WM, WN, act, bf>(p, e, r1, row, col, lane, acc, region);
+    else if constexpr (kRole == kGateGrad)
+      gate_grad_epilogue<WM, WN, act, bf>(p, r1, row, col, lane, acc, region);
+    else
+      blocks_epilogue<WM, WN, act, bf>(p, e, r1, row, col, lane, acc, region);
   };
-  if (p.d_type == TLA_BF16) run(std::true_type{});
-  else run(std::false_type{});
+  auto typed = [&](auto act) {
+    if constexpr (kCode == kBF16 || kCode == kF16) run(act, std::bool_constant<kCode == kBF16>{});
+    else if (p.d_type == TLA_BF16) run(act, std::true_type{});
+    else run(act, std::false_type{});
+  };
+  if constexpr (kAct > 0) typed(std::integral_constant<int, kAct>{});
+  else with_act(p.act, typed);
 }
 
 }  // namespace

@@ -41,7 +41,7 @@ __global__ __launch_bounds__(256) void gated_small_kernel(const GroupedParams p,
     const float dh = g, gate = load_elem(p.Z, p.d_type, z), up = load_elem(p.Z2, p.d_type, z);
     with_act(p.act, [&](auto act) {
       float value, slope;
-      act_both<act>(gate, value, slope);
+      act_both<act>(gate, p.act == TLA_ACT_NONE, value, slope);
       ((uint16_t*)p.D)[d] = to_bits(dh * (up * slope), p.d_type);
       ((uint16_t*)p.D2)[d] = to_bits(dh * value, p.d_type);
       if (p.H) ((uint16_t*)p.H)[(int64_t)row * p.ldh + n] = to_bits(value * up, p.d_type);

@@ -462,10 +462,9 @@ __global__ __launch_bounds__(64 * kWM * kWN) void grouped_direct_kernel(const Gr
   }
   if constexpr (kForm == kGrad)
     wgrad_epilogue<FM, FN>(p, e, m0 + wm0, n0 + wn0, lane, acc, region);
-  else if constexpr (kRole == kGated)
-    gated_epilogue<32, WM, WN / 2>(p, e, m_end, m0 + wm0, n0 + wb0, lane, acc, region);
-  else if constexpr (kRole == kGateGrad)
-    gate_grad_epilogue<WM, WN>(p, m_end, m0 + wm0, n0 + wn0, lane, acc, region);
+  else if constexpr (kRole != kPlain)
+    role_epilogue<kCode, kRole, 0, 32, WM, kTwo ? WN / 2 : WN>(p, e, m_end, m0 + wm0, n0 + wb0, lane,
+                                                               acc, region);
   else
     grouped_epilogue<kCode, FM, FN>(p, e, m_end, m0 + wm0, n0 + wn0, lane, acc, region);
 }

@@ -263,10 +263,9 @@ __global__ __launch_bounds__(kThreads, kBView == kBElem ? 1 : 2) void grouped_ge
   }
   if constexpr (kWgrad)
     wgrad_epilogue<FM, FN>(p, e, m0 + wm0, n0 + wn0, lane, acc, region);
-  else if constexpr (kRole == kGated)
-    gated_epilogue<32, WM, WN / 2>(p, e, m_end, m0 + wm0, n0 + wb0, lane, acc, region);
-  else if constexpr (kRole == kGateGrad)
-    gate_grad_epilogue<WM, WN>(p, m_end, m0 + wm0, n0 + wn0, lane, acc, region);
+  else if constexpr (kRole != kPlain)
+    role_epilogue<kCode, kRole, 0, 32, WM, kTwo ? WN / 2 : WN>(p, e, m_end, m0 + wm0, n0 + wb0, lane,
+                                                               acc, region);
   else
     grouped_epilogue<kCode, FM, FN>(p, e, m_end, m0 + wm0, n0 + wn0, lane, acc, region);
 }

@@ -64,7 +64,7 @@ struct TileSpan {
 // The tile program.  kHalf: 128 x 256 instead of 256 x 256, for blocks of at
 // most 128 rows: both groups share the rows and take half the columns each, so
 // every wave multiplies 64 x 64 (16 MFMAs a k-tile, not 32) and none idles.
-template <int kCode, int kForm, bool kHalf, int kRole>
+template <int kCode, int kForm, bool kHalf, int kRole, int kAct>
 __device__ __forceinline__ void two_group_tile(const GroupedParams& p, const TileSpan& ts,
                                                uint8_t* smem) {
   constexpr bool kShift = kForm == kNKShift;
@@ -446,7 +446,7 @@ __device__ __forceinline__ void two_group_tile(const GroupedParams& p, const Til
     __builtin_amdgcn_sched_barrier(0);
     if constexpr (kBlocks) {
       if (busy)
-        blocks_mma<FM, FN, kTwo, kSub>(acc, a[0], b[0], scale, [&](auto j) {
+        blocks_mma<FM, FN, kTwo>(acc, a[0], b[0], scale, [&](auto j) {
           read_frag(kt, std::integral_constant<int, FM + j + FB>{});
         });
       advance_b(kt);
@@ -589,12 +589,9 @@ __device__ __forceinline__ void two_group_tile(const GroupedParams& p, const Til
   }
   if constexpr (kForm == kGrad)
     wgrad_epilogue<FM, FN>(p, e, m0 + wm0, n0 + wn0, lane, acc, region);
-  else if constexpr (kRole == kGated)
-    gated_epilogue<FR, WM, WN / 2>(p, e, m_end, m0 + wm0, n0 + wb0, lane, acc, region);
-  else if constexpr (kRole == kGateGrad)
-    gate_grad_epilogue<WM, WN>(p, m_end, m0 + wm0, n0 + wn0, lane, acc, region);
-  else if constexpr (kBlocks)
-    blocks_epilogue<WM, WN>(p, e, m_end, m0 + wm0, n0 + wn0, lane, acc, region);
+  else if constexpr (kRole != kPlain || kBlocks)
+    role_epilogue<kCode, kRole, kAct, FR, WM, kTwo ? WN / 2 : WN>(p, e, m_end, m0 + wm0, n0 + wb0, lane,
+                                                                 acc, region);
   else
     grouped_epilogue<kCode, FM, FN>(p, e, m_end, m0 + wm0, n0 + wn0, lane, acc, region);
 }
@@ -693,7 +690,7 @@ __device__ __forceinline__ bool two_group_lookup(const GroupedParams& p, int bid
   return false;
 }
 
-template <int kCode, int kForm, int kRole = kPlain>
+template <int kCode, int kForm, int kRole = kPlain, int kAct = 0>
 __global__ __launch_bounds__(512) void grouped_two_group_kernel(const GroupedParams p) {
   constexpr int EB = type_bytes(kCode);
   __shared__ __attribute__((aligned(1024))) uint8_t smem[kTwoGroupLds];
@@ -711,7 +708,7 @@ __global__ __launch_bounds__(512) void grouped_two_group_kernel(const GroupedPar
     ts.K = hi - lo;
     ts.A = p.A + (int64_t)lo * p.lda * EB;
     ts.B = p.B + (int64_t)lo * p.ldb * EB;
-    two_group_tile<kCode, kForm, false, kRole>(p, ts, smem);
+    two_group_tile<kCode, kForm, false, kRole, kAct>(p, ts, smem);
   } else {
     HalfTile t;
     if (!two_group_lookup(p, blockIdx.x, t)) return;
@@ -724,12 +721,12 @@ __global__ __launch_bounds__(512) void grouped_two_group_kernel(const GroupedPar
     ts.A = p.A;
     ts.B = p.B + (int64_t)ts.e * p.stride_b * EB;
     if constexpr (kRole == kGated) ts.B2 = p.B2 + (int64_t)ts.e * p.stride_b * EB;
-    if (t.half) two_group_tile<kCode, kForm, true, kRole>(p, ts, smem);
-    else two_group_tile<kCode, kForm, false, kRole>(p, ts, smem);
+    if (t.half) two_group_tile<kCode, kForm, true, kRole, kAct>(p, ts, smem);
+    else two_group_tile<kCode, kForm, false, kRole, kAct>(p, ts, smem);
   }
 }
 
-template <int kCode, int kForm, int kRole = kPlain>
+template <int kCode, int kForm, int kRole = kPlain, int kAct = 0>
 int launch(const GroupedParams& p0, hipStream_t stream) {
   GroupedParams p = p0;
   p.tiles_n = kRole == kGated ? (p.N + 127) / 128 : (p.N + 255) / 256;
@@ -741,9 +738,17 @@ int launch(const GroupedParams& p0, hipStream_t stream) {
                             : row_tiles_bound(p.rows, p.groups, 256) * p.tiles_n + 256;
   if (grid <= 0) return TLA_OK;
   if (!grid_fits(grid, 512)) return TLA_ERR_UNSUPPORTED;
-  hipLaunchKernelGGL((grouped_two_group_kernel<kCode, kForm, kRole>), dim3((unsigned)grid), dim3(512), 0,
+  hipLaunchKernelGGL((grouped_two_group_kernel<kCode, kForm, kRole, kAct>), dim3((unsigned)grid), dim3(512), 0,
                      stream, p);
   return hipGetLastError() == hipSuccess ? TLA_OK : TLA_ERR_HIP;
+}
+
+// The kernel of the problem's activation
+template <int kCode, int kForm, int kRole>
+int launch_act(const GroupedParams& p, hipStream_t s) {
+  if (p.act == TLA_ACT_SILU) return launch<kCode, kForm, kRole, kSiluAct>(p, s);
+  if (p.act == TLA_ACT_GELU) return launch<kCode, kForm, kRole, kGeluAct>(p, s);
+  return launch<kCode, kForm, kRole, kLinear>(p, s);
 }
 
 }  // namespace

@@ -109,10 +109,12 @@ inline bool few_rows_narrow(int64_t rows, int64_t groups, int64_t N) {
 int launch_grouped_few_rows(const GroupedParams& p, int type, int mt, hipStream_t stream);
 
 // The gated product (role kGated) and its gradient (kGateGrad) on the same
-// kernels, with the same conditions; 16-bit operands.
+// kernels, with the same conditions; 16-bit operands, outputs of their type.
 int launch_gated_general(const GroupedParams& p, int type, bool b_kc, int role, hipStream_t stream);
-int launch_gated_two_group_nk(const GroupedParams& p, int type, int role, hipStream_t stream);
-int launch_gated_two_group_kn(const GroupedParams& p, int type, int role, hipStream_t stream);
+int launch_two_group_gated_nk(const GroupedParams& p, int type, hipStream_t stream);
+int launch_two_group_gated_kn(const GroupedParams& p, int type, hipStream_t stream);
+int launch_two_group_grad_nk(const GroupedParams& p, int type, hipStream_t stream);
+int launch_two_group_grad_kn(const GroupedParams& p, int type, hipStream_t stream);
 int launch_gated_direct_nk(const GroupedParams& p, int type, int shape, int role, hipStream_t stream);
 int launch_gated_direct_kn(const GroupedParams& p, int type, int role, hipStream_t stream);
 int launch_gated_few_rows(const GroupedParams& p, int type, int mt, hipStream_t stream);

@@ -121,11 +121,20 @@ struct QuantArgs {
   int kbs, groups, shift;  // blocks in a row; workgroups along a row; log2 of a workgroup's blocks along it
 };
 
+// Workgroup b runs on XCD b % 8: each XCD gets a run of neighbours, so that lines
+// which two blocks share are read into one L2 (16384 x 8191 bf16, whose rows begin
+// anywhere in a line: TIME).
+__device__ __forceinline__ unsigned in_runs(unsigned b, unsigned n) {
+  const unsigned per = n / 8, rest = n % 8, xcd = b & 7;
+  return xcd * per + min(xcd, rest) + (b >> 3);
+}
+
 // 1 x 128: a workgroup's sixteen blocks are 2^shift neighbours of 16 / 2^shift rows.
 template <int kCode>
 __global__ __launch_bounds__(256) void quantize_row_blocks_kernel(const QuantArgs a) {
   const int tid = threadIdx.x, unit = tid >> 4;
-  const int band = blockIdx.x / (unsigned)a.groups, group = blockIdx.x % (unsigned)a.groups;
+  const unsigned id = in_runs(blockIdx.x, gridDim.x);
+  const int band = id / (unsigned)a.groups, group = id % (unsigned)a.groups;
   const int64_t row = ((int64_t)band << (4 - a.shift)) + (unit >> a.shift);
   const int kb = (group << a.shift) + (unit & ((1 << a.shift) - 1));
   if (row >= a.M || kb >= a.kbs) return;
@@ -145,8 +154,9 @@ __global__ __launch_bounds__(256) void quantize_row_blocks_kernel(const QuantArg
 template <int kCode>
 __global__ __launch_bounds__(256) void quantize_square_blocks_kernel(const QuantArgs a) {
   const int tid = threadIdx.x;
-  const int64_t band = blockIdx.x / (unsigned)a.kbs;
-  const int kb = blockIdx.x % (unsigned)a.kbs;
+  const unsigned id = in_runs(blockIdx.x, gridDim.x);
+  const int64_t band = id / (unsigned)a.kbs;
+  const int kb = id % (unsigned)a.kbs;
   const int64_t row0 = band * 128 + (tid >> 4), c = (int64_t)kb * 128 + 8 * (tid & 15);
   RowVec<kCode> v[8];
   uint32_t m = 0;
