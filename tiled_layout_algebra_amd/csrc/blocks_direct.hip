@@ -97,8 +97,8 @@ __global__ __launch_bounds__(64 * kWM * kWN) void blocks_direct_kernel(const Gro
     const i32x4 lo = *(const i32x4*)(smem + at + c0), hi = *(const i32x4*)(smem + at + (c0 ^ 16u));
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
   };
-  f32x4 acc[FM][FN];
-  static_for<FM>([&](auto i) { static_for<FN>([&](auto j) { acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f}; }); });
+  BlockSums<FM, FN, kTwo> sums;
+  sums.init();
 
   auto tile = [&](int kt, auto S) {
     using Fill = std::integral_constant<int, (S + kStages - 1) % kStages>;
@@ -119,7 +119,8 @@ __global__ __launch_bounds__(64 * kWM * kWN) void blocks_direct_kernel(const Gro
       constexpr int at = kTwo ? j % FH * 16 * kRowBytes + j / FH * (SLAB_B / 2) : j * 16 * kRowBytes;
       b[j] = frag(fb + S * STAGE + SLAB_A + at);
     });
-    blocks_mma<FM, FN, kTwo>(acc, a, b, s, [](auto) {});
+    sums.mma(a, b, s, [](auto) {});
+    sums.finish(s);
   };
   if (KT > 0) {
     // the first tile's scales before its copies, so that the loop's first wait covers them
@@ -135,7 +136,7 @@ __global__ __launch_bounds__(64 * kWM * kWN) void blocks_direct_kernel(const Gro
   __syncthreads();  // the stages become the waves' epilogue regions
   uint8_t* region = smem + wave * WM * WN * 2;
   role_epilogue<kE4M3Blocks, kTwo ? kGated : kPlain, 0, 16, WM, kTwo ? WN / 2 : WN>(
-      p, e, m_end, m0 + wm0, n0 + wb0, lane, acc, region);
+      p, e, m_end, m0 + wm0, n0 + wb0, lane, sums.acc, region);
 }
 
 template <int BM, int kStages, int kWM, int kWN, bool kTwo>

@@ -27,32 +27,50 @@ struct OpAtom<kE4M3Blocks> {
 
 namespace {
 
-// One k-tile (a block of 128) of a wave's MFMA tiles: acc += scale part, the
-// sums of a tile kAhead instructions behind its matrix instruction, so that
-// these follow each other without waiting for a result.  s[0]: the scales of the
-// plain sums or of the first half of the columns (the gate's), s[1]: of the
-// other half.  b holds FB of the FN column fragments; after(j) is called behind
-// the last use of fragment j where j + FB < FN, to read fragment j + FB in its place.
-template <int FM, int FN, bool kTwo, int FB, class F>
-__device__ __forceinline__ void blocks_mma(f32x4 (&acc)[FM][FN], const i32x8 (&a)[FM],
-                                           i32x8 (&b)[FB], const float (&s)[2][FM], F&& after) {
-  constexpr int kN = FM * FN, kAhead = kN < 4 ? kN : 4;
-  f32x4 part[kAhead];
-  static_for<kN + kAhead>([&](auto x) {
-    if constexpr (x >= kAhead) {
-      constexpr int y = x - kAhead, i = y % FM, j = y / FM;
-      const float c = s[kTwo && j >= FN / 2][i];
-      static_for<4>([&](auto q) {
-        acc[i][j][(int)q] = fmaf(part[y % kAhead][(int)q], c, acc[i][j][(int)q]);
-      });
-    }
-    if constexpr (x < kN) {
+// The sums of a wave's MFMA tiles over blocks of 128 of K: acc += scale part, a
+// tile's sum kAhead instructions behind its matrix instruction, so that these
+// follow each other without waiting for a result.  s[0]: the scales of the plain
+// sums or of the first half of the columns (the gate's), s[1]: of the other half.
+// mma: a k-tile's matrix instructions and all but the last kAhead sums; b holds FB
+// of the FN column fragments, and after(j) is called behind the last use of fragment
+// j where j + FB < FN, to read fragment j + FB in its place.  finish: those last
+// sums, which may wait (with their scales) until the matrix cores are another
+// wave's.
+template <int FM, int FN, bool kTwo>
+struct BlockSums {
+  static constexpr int kN = FM * FN, kAhead = 3;
+  f32x4 acc[FM][FN], part[kAhead];
+  __device__ __forceinline__ void init() {
+    static_for<FM>([&](auto i) { static_for<FN>([&](auto j) { acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f}; }); });
+  }
+  template <int y>
+  __device__ __forceinline__ void add(const float (&s)[2][FM]) {
+    constexpr int i = y % FM, j = y / FM;
+    const float c = s[kTwo && j >= FN / 2][i];
+    static_for<4>([&](auto q) {
+      acc[i][j][(int)q] = fmaf(part[y % kAhead][(int)q], c, acc[i][j][(int)q]);
+    });
+  }
+  template <int FB, class F>
+  __device__ __forceinline__ void mma(const i32x8 (&a)[FM], i32x8 (&b)[FB], const float (&s)[2][FM],
+                                      F&& after) {
+    static_for<kN>([&](auto x) {
+      if constexpr (x >= kAhead) add<x - kAhead>(s);
       part[x % kAhead] = OpAtom<kE4M3Blocks>::block(b[x / FM % FB], a[x % FM]);
       if constexpr (x % FM == FM - 1 && x / FM + FB < FN) after(std::integral_constant<int, x / FM>{});
-    }
-    __builtin_amdgcn_sched_barrier(0);  // in this order
-  });
-}
+      __builtin_amdgcn_sched_barrier(0);  // in this order
+    });
+  }
+  __device__ __forceinline__ void finish(const float (&s)[2][FM]) {
+    static_for<kAhead>([&](auto x) { add<kN - kAhead + x>(s); });
+  }
+  // keeps the matrix instructions in front of what follows
+  __device__ __forceinline__ void pin() {
+#if defined(__HIP_DEVICE_COMPILE__)
+    static_for<kAhead>([&](auto x) { asm volatile("" : "+v"(part[x])); });
+#endif
+  }
+};
 
 // sigmoid(z) = 1 / (1 + 2^(-z log2 e)) by the hardware's exp2 and reciprocal
 // (one unit each); the exponent's rounding makes it off by (|z| + 4) 2^-24 of
@@ -95,11 +113,13 @@ __device__ __forceinline__ float act_any(float z, int act) {
   return y;
 }
 
+// Orders a wave's LDS accesses of different types
+__device__ __forceinline__ void wave_fence() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
+
 // A wave's WM x WN piece of a row-major 16-bit matrix in LDS (WaveRegion) seen from
 // MFMA tiles of FR rows: FR 32: lane l holds row 32 i + l % 32, columns 32 j + 8 g +
 // 4 (l / 32) .. + 3; FR 16: row 16 i + l % 16, columns 16 j + 4 (l / 16) .. + 3.
-// Pieces that end inside the matrix take loops that are not unrolled: the edge's
-// code is a small part of the kernel's, which the instruction cache has to hold.
+// WM <= 64.
 template <int FR, int WM, int WN>
 struct Piece {
   using R = WaveRegion<WM / 32, WN / 32>;
@@ -114,57 +134,51 @@ struct Piece {
   // row and first column of the 16-byte chunk at region + 1024 t + 16 lane
   static __device__ __forceinline__ int row(int lane, int t) { return R::kRowsPerKiB * t + lane / R::kCh; }
   static __device__ __forceinline__ int chunk(int lane, int t) { return 8 * R::swz(row(lane, t), lane % R::kCh); }
-  static __device__ __forceinline__ bool whole(int rows, int cols) { return rows >= WM && cols >= WN; }
-  // a whole piece into registers, from there into the region
-  static __device__ __forceinline__ void fetch(const uint8_t* base, int64_t ld, i32x4 (&v)[kIters], int lane) {
+  // where element c of row r lies in the region
+  static __device__ __forceinline__ uint16_t* elem(uint8_t* region, int r, int c) {
+    return (uint16_t*)(region + r * R::kRowB + R::swz(r, c / 8) * 16 + (c & 7) * 2);
+  }
+  // rows x cols of a piece into registers (whole chunks of them) ...
+  static __device__ __forceinline__ void fetch(const uint8_t* base, int64_t ld, i32x4 (&v)[kIters],
+                                               int lane, int rows, int cols) {
     const uint8_t* from = base + (int64_t)(lane / R::kCh) * ld * 2;
 #pragma unroll
-    for (int t = 0; t < kIters; ++t)
-      v[t] = load16_even(from + (int64_t)(R::kRowsPerKiB * t) * ld * 2 + chunk(lane, t) * 2);
+    for (int t = 0; t < kIters; ++t) {
+      v[t] = i32x4{0, 0, 0, 0};
+      if (row(lane, t) < rows && chunk(lane, t) + 8 <= cols)
+        v[t] = load16_even(from + (int64_t)(R::kRowsPerKiB * t) * ld * 2 + chunk(lane, t) * 2);
+    }
   }
-  static __device__ __forceinline__ void put(const i32x4 (&v)[kIters], uint8_t* region, int lane) {
+  // ... and from there into the region, with the elements of the chunk that the
+  // last column cuts, a lane a row
+  static __device__ __forceinline__ void put(const uint8_t* base, int64_t ld, const i32x4 (&v)[kIters],
+                                             uint8_t* region, int lane, int rows, int cols) {
 #pragma unroll
     for (int t = 0; t < kIters; ++t) *(i32x4*)(region + t * 1024 + lane * 16) = v[t];
-  }
-  // rows x cols of a piece straight into the region (the rest of it: anything)
-  static __device__ __forceinline__ void load_edge(const uint8_t* base, int64_t ld, uint8_t* region,
-                                                   int lane, int rows, int cols) {
+    if (cols < WN && cols % 8 != 0 && lane < rows) {
+      wave_fence();
 #pragma unroll 1
-    for (int t = 0; t < kIters; ++t) {
-      const int c = chunk(lane, t);
-      const uint16_t* src = (const uint16_t*)base + (int64_t)min(row(lane, t), rows - 1) * ld;
-      uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-      for (int e = 0; e < 8; ++e) w[e / 2] |= (uint32_t)src[min(c + e, cols - 1)] << (16 * (e & 1));
-      *(i32x4*)(region + t * 1024 + lane * 16) = i32x4{(int)w[0], (int)w[1], (int)w[2], (int)w[3]};
+      for (int c = cols & ~7; c < cols; ++c)
+        *elem(region, lane, c) = ((const uint16_t*)base)[(int64_t)lane * ld + c];
     }
   }
   // region -> rows x cols of the matrix; v16: its rows are 16-byte aligned
-  static __device__ __forceinline__ void store(uint8_t* base, int64_t ld, const uint8_t* region,
-                                               int lane, int rows, int cols, bool v16) {
-    if (whole(rows, cols)) {
-      uint8_t* to = base + (int64_t)(lane / R::kCh) * ld * 2;
+  static __device__ __forceinline__ void store(uint8_t* base, int64_t ld, uint8_t* region, int lane,
+                                               int rows, int cols, bool v16) {
+    uint8_t* to = base + (int64_t)(lane / R::kCh) * ld * 2;
 #pragma unroll
-      for (int t = 0; t < kIters; ++t) {
-        const i32x4 v = *(const i32x4*)(region + t * 1024 + lane * 16);
-        uint8_t* dst = to + (int64_t)(R::kRowsPerKiB * t) * ld * 2 + chunk(lane, t) * 2;
+    for (int t = 0; t < kIters; ++t) {
+      const i32x4 v = *(const i32x4*)(region + t * 1024 + lane * 16);
+      uint8_t* dst = to + (int64_t)(R::kRowsPerKiB * t) * ld * 2 + chunk(lane, t) * 2;
+      if (row(lane, t) < rows && chunk(lane, t) + 8 <= cols) {
         if (v16) *(i32x4*)dst = v;
         else store16_even(dst, v);
       }
-      return;
     }
+    if (cols < WN && cols % 8 != 0 && lane < rows) {
 #pragma unroll 1
-    for (int t = 0; t < kIters; ++t) {
-      const i32x4 v = *(const i32x4*)(region + t * 1024 + lane * 16);
-      const int r = row(lane, t), c = chunk(lane, t);
-      uint8_t* dst = base + ((int64_t)r * ld + c) * 2;
-      if (r < rows && c + 8 <= cols) {
-        store16_even(dst, v);
-      } else if (r < rows) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (c + e < cols) ((uint16_t*)dst)[e] = (uint16_t)((uint32_t)v[e >> 1] >> (16 * (e & 1)));
-      }
+      for (int c = cols & ~7; c < cols; ++c)
+        ((uint16_t*)base)[(int64_t)lane * ld + c] = *elem(region, lane, c);
     }
   }
 };
@@ -176,8 +190,6 @@ __device__ __forceinline__ f32x4 bias4(const GroupedParams& p, const uint8_t* bi
   static_for<4>([&](auto q) { x[(int)q] = load_elem(bias, p.bias_type, at + min(n + q, p.N - 1)); });
   return x;
 }
-
-__device__ __forceinline__ void wave_fence() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
 
 // One pass over pairs of sums: f(gate, up) packed into a region.
 template <int FR, int WM, int WN, bool kBf, class Acc, int FM, int FN, class F>
@@ -234,44 +246,44 @@ __device__ __forceinline__ void gated_epilogue(const GroupedParams& p, int e, in
   P::store(p.D + ((int64_t)row * p.ldd + col) * 2, p.ldd, region, lane, rows, cols, v16);
 }
 
+// What the gradient's epilogue reads: a part's gate and up as whole rows, in
+// registers.  Parts are half a wave's columns, or all 32.
+template <int WM, int WN>
+struct GateParts {
+  static constexpr int kPart = WN >= 64 ? WN / 2 : WN, kParts = WN / kPart;
+  using P = Piece<32, WM, kPart>;
+  i32x4 g[P::kIters], u[P::kIters];
+  __device__ __forceinline__ void ask(const GroupedParams& p, int r1, int row, int col, int lane, int part) {
+    const int c = col + part * kPart, rows = min(WM, r1 - row), cols = min(kPart, p.N - c);
+    const int64_t at = ((int64_t)row * p.ldz + c) * 2;
+    P::fetch(p.Z + at, p.ldz, g, lane, rows, cols);
+    P::fetch(p.Z2 + at, p.ldz, u, lane, rows, cols);
+  }
+};
+
 // The gradient's epilogue: acc is dh; D = dh up act'(gate), D2 = dh act(gate),
-// H = act(gate) up with gate and up read from Z and Z2.  WN columns in parts of
-// half of them (or all 32): a part's gate and up come as whole rows into registers
-// (the fragments' are free) while the part before is worked on, and go through LDS;
-// the gradients go back the same way, the hidden layer waits in the sums'
-// registers.  region: WM WN 16-bit values, 2 WM WN for WN = 32.
+// H = act(gate) up with gate and up read from Z and Z2.  z holds the first part;
+// the next one comes while a part is worked on.  A part goes through LDS into the
+// MFMA layout, the gradients go back the same way, the hidden layer waits in the
+// sums' registers.  region: WM WN 16-bit values, 2 WM WN for WN = 32.
 template <int WM, int WN, int kAct, bool kBf, int FM, int FN>
 __device__ __forceinline__ void gate_grad_epilogue(const GroupedParams& p, int r1, int row, int col,
                                                    int lane, f32x16 (&acc)[FM][FN],
-                                                   uint8_t* region) {
-  constexpr int kPart = WN >= 64 ? WN / 2 : WN, FP = kPart / 32, kParts = WN / kPart;
-  using P = Piece<32, WM, kPart>;
+                                                   GateParts<WM, WN>& z, uint8_t* region) {
+  using G = GateParts<WM, WN>;
+  using P = typename G::P;
+  constexpr int kPart = G::kPart, FP = kPart / 32, kParts = G::kParts;
   const int rows = min(WM, r1 - row);
   if (rows <= 0 || col >= p.N) return;
   const bool v16 = p.flags & kOpD16, none = p.act == TLA_ACT_NONE;
   uint8_t* region2 = region + P::kBytes;
-  i32x4 zg[P::kIters], zu[P::kIters];
-  auto ask = [&](int part) {
-    const int c = col + part * kPart;
-    const int64_t at = ((int64_t)row * p.ldz + c) * 2;
-    if (P::whole(rows, p.N - c)) {
-      P::fetch(p.Z + at, p.ldz, zg, lane);
-      P::fetch(p.Z2 + at, p.ldz, zu, lane);
-    }
-  };
-  ask(0);
   static_for<kParts>([&](auto part) {
     const int c = col + part * kPart, cols = min(kPart, p.N - c);
     if (cols <= 0) return;
     const int64_t dat = ((int64_t)row * p.ldd + c) * 2, zat = ((int64_t)row * p.ldz + c) * 2;
-    if (P::whole(rows, cols)) {
-      P::put(zg, region, lane);
-      P::put(zu, region2, lane);
-    } else {
-      P::load_edge(p.Z + zat, p.ldz, region, lane, rows, cols);
-      P::load_edge(p.Z2 + zat, p.ldz, region2, lane, rows, cols);
-    }
-    if constexpr (part + 1 < kParts) ask(part + 1);
+    P::put(p.Z + zat, p.ldz, z.g, region, lane, rows, cols);
+    P::put(p.Z2 + zat, p.ldz, z.u, region2, lane, rows, cols);
+    if constexpr (part + 1 < kParts) z.ask(p, r1, row, col, lane, part + 1);
     wave_fence();
     static_for<FP>([&](auto jj) {
       constexpr int j = part * FP + jj;
@@ -345,20 +357,8 @@ __device__ __forceinline__ void blocks_epilogue(const GroupedParams& p, int e, i
   P::store(p.D + ((int64_t)row * p.ldd + col) * 2, p.ldd, region, lane, rows, cols, p.flags & kOpD16);
 }
 
-// A wave's epilogue in the role and operand code of its kernel.  16-bit roles: the
-// outputs have the operands' type.  The two-group kernel is compiled for each
-// activation (kAct > 0), the others branch.
-template <int kCode, int kRole, int kAct, int FR, int WM, int WN, class Acc, int FM, int FN>
-__device__ __forceinline__ void role_epilogue(const GroupedParams& p, int e, int r1, int row, int col,
-                                              int lane, Acc (&acc)[FM][FN], uint8_t* region) {
-  auto run = [&](auto act, auto bf) {
-    if constexpr (kRole == kGated)
-      gated_epilogue<FR, WM, WN, act, bf>(p, e, r1, row, col, lane, acc, region);
-    else if constexpr (kRole == kGateGrad)
-      gate_grad_epilogue<WM, WN, act, bf>(p, r1, row, col, lane, acc, region);
-    else
-      blocks_epilogue<WM, WN, act, bf>(p, e, r1, row, col, lane, acc, region);
-  };
+template <int kCode, int kAct, class F>
+__device__ __forceinline__ void with_act_and_type(const GroupedParams& p, F&& run) {
   auto typed = [&](auto act) {
     if constexpr (kCode == kBF16 || kCode == kF16) run(act, std::bool_constant<kCode == kBF16>{});
     else if (p.d_type == TLA_BF16) run(act, std::true_type{});
@@ -366,6 +366,28 @@ __device__ __forceinline__ void role_epilogue(const GroupedParams& p, int e, int
   };
   if constexpr (kAct > 0) typed(std::integral_constant<int, kAct>{});
   else with_act(p.act, typed);
+}
+
+// A wave's epilogue in the role and operand code of its kernel.  16-bit roles: the
+// outputs have the operands' type.  The two-group kernel is compiled for each
+// activation (kAct > 0), the others branch.
+template <int kCode, int kRole, int kAct, int FR, int WM, int WN, class Acc, int FM, int FN>
+__device__ __forceinline__ void role_epilogue(const GroupedParams& p, int e, int r1, int row, int col,
+                                              int lane, Acc (&acc)[FM][FN], uint8_t* region) {
+  with_act_and_type<kCode, kAct>(p, [&](auto act, auto bf) {
+    if constexpr (kRole == kGated)
+      gated_epilogue<FR, WM, WN, act, bf>(p, e, r1, row, col, lane, acc, region);
+    else
+      blocks_epilogue<WM, WN, act, bf>(p, e, r1, row, col, lane, acc, region);
+  });
+}
+template <int kCode, int kAct, int WM, int WN, int FM, int FN>
+__device__ __forceinline__ void grad_epilogue(const GroupedParams& p, int r1, int row, int col, int lane,
+                                              f32x16 (&acc)[FM][FN], GateParts<WM, WN>& z,
+                                              uint8_t* region) {
+  with_act_and_type<kCode, kAct>(p, [&](auto act, auto bf) {
+    gate_grad_epilogue<WM, WN, act, bf>(p, r1, row, col, lane, acc, z, region);
+  });
 }
 
 }  // namespace

@@ -434,6 +434,9 @@ __global__ __launch_bounds__(64 * kWM * kWN) void grouped_direct_kernel(const Gr
     });
   };
 
+  // the gradient's first gate and up values, under the loop
+  GateParts<kRole == kGateGrad ? WM : 32, kRole == kGateGrad ? WN : 32> z;
+  if constexpr (kRole == kGateGrad) z.ask(p, m_end, m0 + wm0, n0 + wn0, lane, 0);
   if (KT > 0) {
     static_for<kStages - 1>([&](auto t) {
       static_for<kLoads>([&](auto q) { copy(t, t, q); });
@@ -462,6 +465,8 @@ __global__ __launch_bounds__(64 * kWM * kWN) void grouped_direct_kernel(const Gr
   }
   if constexpr (kForm == kGrad)
     wgrad_epilogue<FM, FN>(p, e, m0 + wm0, n0 + wn0, lane, acc, region);
+  else if constexpr (kRole == kGateGrad)
+    grad_epilogue<kCode, 0>(p, m_end, m0 + wm0, n0 + wn0, lane, acc, z, region);
   else if constexpr (kRole != kPlain)
     role_epilogue<kCode, kRole, 0, 32, WM, kTwo ? WN / 2 : WN>(p, e, m_end, m0 + wm0, n0 + wb0, lane,
                                                                acc, region);

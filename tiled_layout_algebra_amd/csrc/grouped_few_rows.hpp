@@ -150,50 +150,65 @@ __global__ __launch_bounds__(64 * kWaves) void grouped_few_rows_kernel(const Gro
     });
   };
 
+  // Loads run kU steps ahead of the matrix instructions: unit v's are asked for
+  // again as soon as its step (kBlocks: its two) has been taken.  (All kU loaded,
+  // then all used: TIME.)
   const int whole = min(s1, (int)(kbytes / 64));  // steps inside K
-  int s = s0;
-  if constexpr (kBlocks) {
-    for (; s + kU <= whole; s += kU) {
-      Chunk<kDword> a[kU][MT], b[kU][NT];
-      Scales x[kU / 2];
-      static_for<kU>([&](auto u) {
-        static_for<NT>([&](auto j) { b[u][j].load(pb[j] + (int64_t)(s + u) * 64); });
-        static_for<MT>([&](auto i) { a[u][i].load(pa[i] + (int64_t)(s + u) * 64); });
-        if constexpr (u % 2 == 0) x[u / 2] = scales((s + u) / 2);
-      });
-      static_for<kU / 2>([&](auto v) {
-        Acc part[MT][NT];
-        static_for<MT>([&](auto i) { static_for<NT>([&](auto j) { part[i][j] = Acc{}; }); });
-        static_for<2>([&](auto h) {
-          constexpr int u = 2 * v + h;
-          i32x4 bb[NT];
-          static_for<NT>([&](auto j) { bb[j] = b[u][j].get(sb[kTwo && j >= NH]); });
-          static_for<MT>([&](auto i) {
-            const i32x4 aa = a[u][i].get(sa);
-            static_for<NT>([&](auto j) { S::mma(part[i][j], bb[j], aa); });
-          });
-        });
-        add_block(part, x[v]);
-      });
-    }
-  }
-  for (; !kBlocks && s + kU <= whole; s += kU) {
-    Chunk<kDword> a[kU][MT], b[kU][NT];
-    static_for<kU>([&](auto u) {
-      static_for<NT>([&](auto j) { b[u][j].load(pb[j] + (int64_t)(s + u) * 64); });
-      static_for<MT>([&](auto i) { a[u][i].load(pa[i] + (int64_t)(s + u) * 64); });
+  constexpr int kSlots = kU / kUnit;
+  Chunk<kDword> a[kU][MT], b[kU][NT];
+  Scales x[kBlocks ? kSlots : 1];
+  auto load = [&](int s, auto v) {
+    static_for<kUnit>([&](auto h) {
+      constexpr int u = kUnit * v + h;
+      static_for<NT>([&](auto j) { b[u][j].load(pb[j] + (int64_t)(s + h) * 64); });
+      static_for<MT>([&](auto i) { a[u][i].load(pa[i] + (int64_t)(s + h) * 64); });
     });
-    static_for<kU>([&](auto u) {
+    if constexpr (kBlocks) x[v] = scales(s / 2);
+  };
+  auto use = [&](auto v) {
+    Acc part[MT][NT];
+    if constexpr (kBlocks)
+      static_for<MT>([&](auto i) { static_for<NT>([&](auto j) { part[i][j] = Acc{}; }); });
+    static_for<kUnit>([&](auto h) {
+      constexpr int u = kUnit * v + h;
       i32x4 bb[NT];
       static_for<NT>([&](auto j) { bb[j] = b[u][j].get(sb[kTwo && j >= NH]); });
       static_for<MT>([&](auto i) {
         const i32x4 aa = a[u][i].get(sa);
-        static_for<NT>([&](auto j) { S::mma(acc[i][j], bb[j], aa); });
+        static_for<NT>([&](auto j) {
+          if constexpr (kBlocks) S::mma(part[i][j], bb[j], aa);
+          else S::mma(acc[i][j], bb[j], aa);
+        });
       });
     });
+    if constexpr (kBlocks) add_block(part, x[v]);
+  };
+  int s = s0;
+  if (s + kU <= whole) {
+    static_for<kSlots>([&](auto v) { load(s + kUnit * v, v); });
+    for (; s + 2 * kU <= whole; s += kU) {
+      static_for<kSlots>([&](auto v) {
+        use(v);
+        load(s + kU + kUnit * v, v);
+        __builtin_amdgcn_sched_barrier(0);  // (or the registers of v double)
+      });
+    }
+    static_for<kSlots>([&](auto v) { use(v); });
+    s += kU;
   }
+  // what is left of the whole steps, in halves of kU
+  static_for<3>([&](auto h) {
+    constexpr int n = kU >> (h + 1);
+    if constexpr (n >= kUnit) {
+      if (s + n <= whole) {
+        static_for<n / kUnit>([&](auto v) { load(s + kUnit * v, v); });
+        static_for<n / kUnit>([&](auto v) { use(v); });
+        s += n;
+      }
+    }
+  });
   for (; s < s1; ++s) {
-    // the rest one step at a time; a lane's bytes past K are zeros, gathered
+    // the last step; a lane's bytes past K are zeros, gathered
     // where they begin inside its sixteen
     const int left = (int)min(kbytes - (int64_t)s * 64, (int64_t)64) - 16 * (lane >> 4);
     auto get = [&](const uint8_t* base) {

@@ -257,12 +257,16 @@ __global__ __launch_bounds__(kThreads, kBView == kBElem ? 1 : 2) void grouped_ge
   }
   __syncthreads();  // the stages become the waves' epilogue regions
   uint8_t* region = smem + wave * WM * 64 * FN;
+  GateParts<WM, WN> z;
+  if constexpr (kRole == kGateGrad) z.ask(p, m_end, m0 + wm0, n0 + wn0, lane, 0);
   if constexpr (kWgrad) {
     if (sum_b) sums.template write<FN>(p.dbias + (int64_t)e * p.N, n0 + wn0, p.N, lane);
     if (sum_a) sums.template write<FM>(p.dbias + (int64_t)e * p.M, m0 + wm0, p.M, lane);
   }
   if constexpr (kWgrad)
     wgrad_epilogue<FM, FN>(p, e, m0 + wm0, n0 + wn0, lane, acc, region);
+  else if constexpr (kRole == kGateGrad)
+    grad_epilogue<kCode, 0>(p, m_end, m0 + wm0, n0 + wn0, lane, acc, z, region);
   else if constexpr (kRole != kPlain)
     role_epilogue<kCode, kRole, 0, 32, WM, kTwo ? WN / 2 : WN>(p, e, m_end, m0 + wm0, n0 + wb0, lane,
                                                                acc, region);

@@ -381,6 +381,13 @@ __device__ __forceinline__ void two_group_tile(const GroupedParams& p, const Til
       c += kShift ? 2 : (r % (FM + FN) < FM) ? (kAT ? 2 : kSub) : (kBT ? 2 : kSub);
     return c;
   };
+  BlockSums<kBlocks ? FM : 1, kBlocks ? FN : 1, kTwo> block_sums;
+  typename Atom::Acc plain_sums[kBlocks ? 1 : FM][kBlocks ? 1 : FN];
+  auto& acc = [&]() -> auto& {
+    if constexpr (kBlocks) return block_sums.acc;
+    else return plain_sums;
+  }();
+  static_for<FM>([&](auto i) { static_for<FN>([&](auto j) { acc[i][j] = typename Atom::Acc{}; }); });
   // kBlocks: the scales of a block of k.  Lane l asks for row wm0 + l's and, by
   // its parity, for the gate's (or only) and the up projection's of the wave's
   // columns, a period before they are used: two loads in front of the period's
@@ -392,6 +399,11 @@ __device__ __forceinline__ void two_group_tile(const GroupedParams& p, const Til
     sa_at = p.sa + (int64_t)min(m0 + wm0 + lane, m_end - 1) * p.sa_row;
     sb_at = (kTwo && (lane & 1) ? p.sb2 : p.sb) + (int64_t)e * p.stride_sb +
             (int64_t)(min(n0 + wb0, p.N - 1) >> 7) * p.sb_col;
+  }
+  if constexpr (kBlocks) {
+    // the first k-tile finds nothing to finish
+    static_for<block_sums.kAhead>([&](auto x) { block_sums.part[x] = f32x4{0.f, 0.f, 0.f, 0.f}; });
+    static_for<FM>([&](auto i) { scale[0][i] = scale[1][i] = 0.f; });
   }
   auto ask_scales = [&](int kt) {
     if constexpr (kBlocks) {
@@ -415,7 +427,9 @@ __device__ __forceinline__ void two_group_tile(const GroupedParams& p, const Til
   auto memory_phase = [&](int kt, int ct, int slot, bool live, auto copies) {
     constexpr int kPer = kReads / copies, kRem = kReads % copies;
     if constexpr (kBlocks) {
+      // (the k-tile before's last sums, under the other group's MFMAs)
       __builtin_amdgcn_sched_barrier(0);
+      block_sums.finish(scale);
       place_scales();
       ask_scales(kt + 1);
     }
@@ -436,8 +450,6 @@ __device__ __forceinline__ void two_group_tile(const GroupedParams& p, const Til
     if constexpr (!kBlocks) advance_b(kt);
     __builtin_amdgcn_sched_barrier(0);
   };
-  typename Atom::Acc acc[FM][FN];
-  static_for<FM>([&](auto i) { static_for<FN>([&](auto j) { acc[i][j] = typename Atom::Acc{}; }); });
   LineSums<kCode, FN> sums;
   if constexpr (kForm == kGrad) sums.init();
   // one k-tile of MFMAs, fenced off from the scheduler on both sides so that
@@ -445,10 +457,11 @@ __device__ __forceinline__ void two_group_tile(const GroupedParams& p, const Til
   auto compute = [&](int kt) {
     __builtin_amdgcn_sched_barrier(0);
     if constexpr (kBlocks) {
-      if (busy)
-        blocks_mma<FM, FN, kTwo>(acc, a[0], b[0], scale, [&](auto j) {
-          read_frag(kt, std::integral_constant<int, FM + j + FB>{});
-        });
+      // (also without a row: a branch would join the partial sums by moves, which
+      // wait for them)
+      block_sums.mma(a[0], b[0], scale, [&](auto j) {
+        read_frag(kt, std::integral_constant<int, FM + j + FB>{});
+      });
       advance_b(kt);
     } else if (busy) {
       static_for<KSTEPS * FM * FN>([&](auto idx) {
@@ -471,6 +484,7 @@ __device__ __forceinline__ void two_group_tile(const GroupedParams& p, const Til
     for (int i = 0; i < FM; ++i)
 #pragma unroll
       for (int j = 0; j < FN; ++j) asm volatile("" ::"v"(acc[i][j]));
+    if constexpr (kBlocks) block_sums.pin();
 #endif
   };
   auto wait_lgkmcnt0 = [&]() { __builtin_amdgcn_s_waitcnt(0xC07F); };
@@ -578,6 +592,7 @@ __device__ __forceinline__ void two_group_tile(const GroupedParams& p, const Til
       }
       wait_vmcnt<0>();  // the last (record-less) copies
     }
+    if constexpr (kBlocks) block_sums.finish(scale);
   }
   // Every LDS read of the main loop finished before the last barrier and no
   // copy is in flight, so the slots are free for the epilogue: group 0
@@ -589,7 +604,11 @@ __device__ __forceinline__ void two_group_tile(const GroupedParams& p, const Til
   }
   if constexpr (kForm == kGrad)
     wgrad_epilogue<FM, FN>(p, e, m0 + wm0, n0 + wn0, lane, acc, region);
-  else if constexpr (kRole != kPlain || kBlocks)
+  else if constexpr (kRole == kGateGrad) {
+    GateParts<WM, WN> z;
+    z.ask(p, m_end, m0 + wm0, n0 + wn0, lane, 0);
+    grad_epilogue<kCode, kAct>(p, m_end, m0 + wm0, n0 + wn0, lane, acc, z, region);
+  } else if constexpr (kRole != kPlain || kBlocks)
     role_epilogue<kCode, kRole, kAct, FR, WM, kTwo ? WN / 2 : WN>(p, e, m_end, m0 + wm0, n0 + wb0, lane,
                                                                  acc, region);
   else

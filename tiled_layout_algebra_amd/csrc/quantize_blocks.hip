@@ -7,11 +7,11 @@
 // reduction and written as one byte.  1 x 128: sixteen lanes share a block, eight
 // values each.  128 x 128: a workgroup has a block, 16 lanes a row, 8 rows a lane.
 //
-// Exact rounding without a division: with i the rounded 1 / s, x i (1 - 2^-22) and
-// x i (1 + 2^-22), rounding errors included, lie on either side of x / s.  Rounding
-// is monotone, so where both convert to one code that is the quotient's; where
-// they do not, the sign of x - m s, m the midpoint of the two codes, decides: the
-// fused multiply-add has it exactly.
+// Exact rounding without a division: with i the hardware's reciprocal of s (one
+// unit off at most), x i (1 - 2^-21) and x i (1 + 2^-21), rounding errors included,
+// lie on either side of x / s.  Rounding is monotone, so where both convert to one
+// code that is the quotient's; where they do not, the sign of x - m s, m the
+// midpoint of the two codes, decides: the fused multiply-add has it exactly.
 #include "quantize_common.hpp"
 
 namespace tla {
@@ -24,24 +24,54 @@ struct BlockScale {
   float s, lo, hi, mul;
   bool zero, tiny;  // zero: every code is 0 (s is 0, infinite or NaN)
 };
+// a / 448 correctly rounded: from the product q with the rounded reciprocal, whose
+// remainder a - 448 q is exact, one correction (checked over every significand on
+// the host); below 2^-91 the remainder could underflow.
+__device__ __forceinline__ float over448(float a) {
+  constexpr float r = 1.f / 448.f;
+  const float q = a * r, y = fmaf(fmaf(-448.f, q, a), r, q);
+  return a >= 0x1p-91f && a <= 3.40282347e38f ? y : a / 448.f;
+}
 __device__ __forceinline__ BlockScale block_scale(float amax, float& s) {
   BlockScale d;
-  s = amax / 448.f;
+  s = over448(amax);
   d.zero = !(s > 0.f && s <= 3.40282347e38f);
   d.tiny = s < 0x1p-100f;
   d.mul = d.tiny ? 0x1p64f : 1.f;
   d.s = s * d.mul;
-  const float inv = 1.f / d.s;
-  d.lo = fmaf(inv, -0x1p-22f, inv);
-  d.hi = fmaf(inv, 0x1p-22f, inv);
+  const float inv = __builtin_amdgcn_rcpf(d.s);
+  d.lo = fmaf(inv, -0x1p-21f, inv);
+  d.hi = fmaf(inv, 0x1p-21f, inv);
   return d;
 }
 
+// The largest of 16 neighbouring lanes' values, in each of them
+__device__ __forceinline__ uint32_t max16(uint32_t m) {
+  auto turn = [&](auto n) {  // rotated by n lanes within the sixteen
+    m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x120 + n, 0xF, 0xF, false));
+  };
+  turn(std::integral_constant<int, 8>{});
+  turn(std::integral_constant<int, 4>{});
+  turn(std::integral_constant<int, 2>{});
+  turn(std::integral_constant<int, 1>{});
+  return m;
+}
+
+__device__ __forceinline__ int any_int() {  // a register as it is
+  int x;
+#if defined(__HIP_DEVICE_COMPILE__)
+  asm volatile("" : "=v"(x));
+#else
+  x = 0;
+#endif
+  return x;
+}
 __device__ __forceinline__ uint32_t codes2(float a, float b) {
-  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false) & 0xFFFFu;
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(a, b, any_int(), false) & 0xFFFFu;
 }
 __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
-  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false), true);
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(
+      c, d, __builtin_amdgcn_cvt_pk_fp8_f32(a, b, any_int(), false), true);
 }
 // The exactly rounded code of one value
 __device__ __forceinline__ uint32_t settle(float x, const BlockScale& d) {
@@ -84,31 +114,46 @@ __device__ __forceinline__ uint2 block_codes8(const RowVec<kCode>& v, const Bloc
   return uint2{w[0], w[1]};
 }
 
-// eight values of a row from column c, zeros from column K on
-template <int kCode>
-__device__ __forceinline__ void load8(RowVec<kCode>& v, const uint8_t* row, int64_t c, int64_t K) {
+
+// Eight values of each of kN rows from a column on, zeros from column K on: without a
+// branch where the whole wavefront is inside (its loads then go out together).
+template <int kCode, int kN, class C, class F>
+__device__ __forceinline__ void load_rows(RowVec<kCode> (&v)[kN], int64_t K, C&& col, F&& row) {
   constexpr int kEB = type_bytes(kCode);
-  if (c + 8 <= K) {
-    v.load(row, c);
+  bool inside = true;
+#pragma unroll
+  for (int i = 0; i < kN; ++i) inside &= col(i) + 8 <= K;
+  if (__all(inside)) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) v[i].load(row(i), col(i));
     return;
   }
-  uint32_t w[kEB * 2] = {};
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    if (c + e < K) {
-      if constexpr (kCode == kF32) w[e] = ((const uint32_t*)row)[c + e];
-      else w[e / 2] |= (uint32_t)((const uint16_t*)row)[c + e] << (16 * (e & 1));
+  for (int i = 0; i < kN; ++i) {
+    uint32_t w[kEB * 2] = {};
+    const uint8_t* x = row(i);
+    const int64_t c = col(i);
+    if (c + 8 <= K) {
+      v[i].load(x, c);
+      continue;
     }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if (c + e < K) {
+        if constexpr (kCode == kF32) w[e] = ((const uint32_t*)x)[c + e];
+        else w[e / 2] |= (uint32_t)((const uint16_t*)x)[c + e] << (16 * (e & 1));
+      }
+    }
+    v[i].load((const uint8_t*)w, 0);
   }
-  v.load((const uint8_t*)w, 0);
 }
 __device__ __forceinline__ void store8(uint8_t* q, int64_t c, int64_t K, uint2 w) {
   typedef uint32_t u32x2_a1 __attribute__((ext_vector_type(2), aligned(1)));
   if (c + 8 <= K) {
-    *(u32x2_a1*)(q + c) = u32x2_a1{w.x, w.y};
+    __builtin_nontemporal_store(u32x2_a1{w.x, w.y}, (u32x2_a1*)(q + c));
     return;
   }
-#pragma unroll
+#pragma unroll 1
   for (int e = 0; e < 8; ++e)
     if (c + e < K) q[c + e] = (uint8_t)((e < 4 ? w.x : w.y) >> (8 * (e & 3)));
 }
@@ -129,65 +174,81 @@ __device__ __forceinline__ unsigned in_runs(unsigned b, unsigned n) {
   return xcd * per + min(xcd, rest) + (b >> 3);
 }
 
-// 1 x 128: a workgroup's sixteen blocks are 2^shift neighbours of 16 / 2^shift rows.
-template <int kCode>
+// 1 x 128: a workgroup has 16 kUnits blocks, 2^shift neighbours of each of its rows
+// (whole rows of up to 64 blocks: the workgroup's loads, all in front of its stores,
+// run through memory in order); a lane has eight values of kUnits of them.
+template <int kCode, int kUnits>
 __global__ __launch_bounds__(256) void quantize_row_blocks_kernel(const QuantArgs a) {
   const int tid = threadIdx.x, unit = tid >> 4;
   const unsigned id = in_runs(blockIdx.x, gridDim.x);
   const int band = id / (unsigned)a.groups, group = id % (unsigned)a.groups;
-  const int64_t row = ((int64_t)band << (4 - a.shift)) + (unit >> a.shift);
-  const int kb = (group << a.shift) + (unit & ((1 << a.shift) - 1));
-  if (row >= a.M || kb >= a.kbs) return;
-  const int64_t c = (int64_t)kb * 128 + 8 * (tid & 15);
-  RowVec<kCode> v;
-  load8<kCode>(v, a.X + row * a.ldx * type_bytes(kCode), c, a.K);
-  uint32_t m = v.amax();
+  const int mask = (1 << a.shift) - 1;
+  const int64_t row0 = (int64_t)band * (16 * kUnits >> a.shift);
+  auto row_of = [&](int i) { return row0 + ((unit + 16 * i) >> a.shift); };
+  auto block_of = [&](int i) { return (group << a.shift) + ((unit + 16 * i) & mask); };
+  auto col_of = [&](int i) { return (int64_t)block_of(i) * 128 + 8 * (tid & 15); };
+  RowVec<kCode> v[kUnits];
+  load_rows<kCode>(v, a.K, col_of, [&](int i) {
+    return a.X + min(row_of(i), a.M - 1) * a.ldx * type_bytes(kCode);
+  });
 #pragma unroll
-  for (int d = 8; d; d >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d));
-  float s;
-  const BlockScale d = block_scale(from_bits<kCode>(m), s);
-  if ((tid & 15) == 0) a.scale[row * a.s_row + kb * a.s_kb] = s;
-  store8(a.Q + row * a.ldq, c, a.K, block_codes8<kCode>(v, d));
+  for (int i = 0; i < kUnits; ++i) {
+    const uint32_t m = max16(v[i].amax());
+    float s;
+    const BlockScale d = block_scale(from_bits<kCode>(m), s);
+    const int64_t row = row_of(i);
+    const int kb = block_of(i);
+    if (row < a.M && kb < a.kbs) {
+      if ((tid & 15) == 0) a.scale[row * a.s_row + kb * a.s_kb] = s;
+      store8(a.Q + row * a.ldq, col_of(i), a.K, block_codes8<kCode>(v[i], d));
+    }
+  }
 }
 
-// 128 x 128: a workgroup a block.
+// 128 x 128: a workgroup a block.  (Four neighbouring blocks and 1024 threads, whose
+// loads are 1 KiB of a row: 134 us instead of TIME for 16384 x 8191 bf16.)
 template <int kCode>
-__global__ __launch_bounds__(256) void quantize_square_blocks_kernel(const QuantArgs a) {
+__global__ __launch_bounds__(512) void quantize_square_blocks_kernel(const QuantArgs a) {
   const int tid = threadIdx.x;
   const unsigned id = in_runs(blockIdx.x, gridDim.x);
   const int64_t band = id / (unsigned)a.kbs;
   const int kb = id % (unsigned)a.kbs;
   const int64_t row0 = band * 128 + (tid >> 4), c = (int64_t)kb * 128 + 8 * (tid & 15);
-  RowVec<kCode> v[8];
+  RowVec<kCode> v[4];
   uint32_t m = 0;
+  load_rows<kCode>(v, a.K, [&](int) { return c; }, [&](int i) {
+    return a.X + min(row0 + 32 * i, a.M - 1) * a.ldx * type_bytes(kCode);
+  });
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    load8<kCode>(v[i], a.X + min(row0 + 16 * i, a.M - 1) * a.ldx * type_bytes(kCode), c, a.K);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, v[i].amax());  // (rows past the last are that row again)
-#pragma unroll
-  for (int d = 32; d; d >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d));
-  __shared__ uint32_t part[4];
+  for (int i = 0; i < 4; ++i) m = max(m, v[i].amax());  // (rows past the last are that row again)
+  m = max16(m);
+  m = max(m, (uint32_t)__shfl_xor((int)m, 16));
+  m = max(m, (uint32_t)__shfl_xor((int)m, 32));
+  __shared__ uint32_t part[8];
   if ((tid & 63) == 0) part[tid >> 6] = m;
   __syncthreads();
-  m = max(max(part[0], part[1]), max(part[2], part[3]));
+  for (int w = 0; w < 8; ++w) m = max(m, part[w]);
   float s;
   const BlockScale d = block_scale(from_bits<kCode>(m), s);
   if (tid == 0) a.scale[band * a.s_row + kb * a.s_kb] = s;
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (row0 + 16 * i < a.M) store8(a.Q + (row0 + 16 * i) * a.ldq, c, a.K, block_codes8<kCode>(v[i], d));
+  for (int i = 0; i < 4; ++i)
+    if (row0 + 32 * i < a.M) store8(a.Q + (row0 + 32 * i) * a.ldq, c, a.K, block_codes8<kCode>(v[i], d));
 }
 
 // In launches of fewer than 2^32 threads, bands of rows at a time.
 template <int kCode>
 int launch(QuantArgs a, int block_rows, hipStream_t s) {
-  const int64_t most = kMaxThreads / 256;  // workgroups
+  const int64_t most = kMaxThreads / 512;  // workgroups
   a.kbs = (int)((a.K + 127) / 128);
+  // 1 x 128: four blocks a lane where that still gives each compute unit eight
+  // workgroups, else one
+  const bool deep = a.M * (int64_t)a.kbs >= 2048 * 64;
+  const int units = deep ? 64 : 16;
   a.shift = 0;
-  while (a.shift < 4 && (1 << a.shift) < a.kbs) ++a.shift;
+  while ((1 << a.shift) < units && (1 << a.shift) < a.kbs) ++a.shift;
   a.groups = block_rows == 1 ? (a.kbs + (1 << a.shift) - 1) >> a.shift : a.kbs;
-  const int64_t rows = block_rows == 1 ? 16 >> a.shift : 128;  // of a workgroup
+  const int64_t rows = block_rows == 1 ? units >> a.shift : 128;  // of a workgroup
   const int64_t bands = (a.M + rows - 1) / rows, step = most / a.groups;
   if (step < 1) return TLA_ERR_UNSUPPORTED;
   const int64_t M = a.M;
@@ -199,10 +260,12 @@ int launch(QuantArgs a, int block_rows, hipStream_t s) {
     x.scale += b * (block_rows == 1 ? rows : 1) * a.s_row;
     x.M = M - b * rows;
     const dim3 grid((unsigned)(n * a.groups));
-    if (block_rows == 1)
-      hipLaunchKernelGGL((quantize_row_blocks_kernel<kCode>), grid, dim3(256), 0, s, x);
+    if (block_rows != 1)
+      hipLaunchKernelGGL((quantize_square_blocks_kernel<kCode>), grid, dim3(512), 0, s, x);
+    else if (deep)
+      hipLaunchKernelGGL((quantize_row_blocks_kernel<kCode, 4>), grid, dim3(256), 0, s, x);
     else
-      hipLaunchKernelGGL((quantize_square_blocks_kernel<kCode>), grid, dim3(256), 0, s, x);
+      hipLaunchKernelGGL((quantize_row_blocks_kernel<kCode, 1>), grid, dim3(256), 0, s, x);
     if (hipGetLastError() != hipSuccess) return TLA_ERR_HIP;
   }
   return TLA_OK;
