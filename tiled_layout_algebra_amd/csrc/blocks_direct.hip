@@ -91,10 +91,11 @@ __global__ __launch_bounds__(64 * kWM * kWN) void blocks_direct_kernel(const Gro
   };
 
   const uint32_t fa = (uint32_t)((wm0 + (lane & 15)) * kRowBytes), fb = (uint32_t)((wb0 + (lane & 15)) * kRowBytes);
-  // logical chunks 2 (lane / 16) and the one after it; the swizzle repeats in 16 rows
-  const uint32_t c0 = Swz::chunk(lane & 15, 2 * (lane >> 4)) * 16;
+  // logical chunks lane / 16 and the fourth after it, as the two-group kernel's
+  // (whose comment says why); the swizzle repeats in 16 rows
+  const uint32_t c0 = Swz::chunk(lane & 15, lane >> 4) * 16;
   auto frag = [&](uint32_t at) {
-    const i32x4 lo = *(const i32x4*)(smem + at + c0), hi = *(const i32x4*)(smem + at + (c0 ^ 16u));
+    const i32x4 lo = *(const i32x4*)(smem + at + c0), hi = *(const i32x4*)(smem + at + (c0 ^ 64u));
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
   };
   BlockSums<FM, FN, kTwo> sums;

@@ -89,7 +89,7 @@ __global__ __launch_bounds__(64 * kWaves) void grouped_few_rows_kernel(const Gro
   constexpr bool kTwo = kRole == kGated;
   constexpr int NH = kTwo ? NT / 2 : NT;
   constexpr int EB = type_bytes(kCode), BM = 16 * MT, BN = 16 * NH;
-  constexpr int kU = MT + NT <= 3 ? 8 : 4;  // steps in flight
+  constexpr int kU = MT + NT <= 2 ? 8 : 4;  // steps in flight
   __shared__ Acc part[kWaves][MT * NT][64];
 
   RowTile t;
@@ -152,7 +152,9 @@ __global__ __launch_bounds__(64 * kWaves) void grouped_few_rows_kernel(const Gro
 
   // Loads run kU steps ahead of the matrix instructions: unit v's are asked for
   // again as soon as its step (kBlocks: its two) has been taken.  (All kU loaded,
-  // then all used: TIME.)
+  // then all used, twice as many: bf16, 128 rows on 32 experts of 2048 x 4096 112 us
+  // instead of 106; and the steps left over one at a time: one row, 8192 x 1050 e4m3
+  // 14.4 instead of 9.7.)
   const int whole = min(s1, (int)(kbytes / 64));  // steps inside K
   constexpr int kSlots = kU / kUnit;
   Chunk<kDword> a[kU][MT], b[kU][NT];

@@ -235,10 +235,15 @@ __device__ __forceinline__ void two_group_tile(const GroupedParams& p, const Til
   // swizzle XORs the chunk index, so the second chunk sits at the first
   // one's address XOR 16 (every other term of the address is a multiple of
   // 128), formed in the loop rather than held.
+  // kBlocks: lane l holds chunks l / 16 and l / 16 + 4 (XOR 64).  A 16-byte LDS read
+  // takes lanes 0 .. 3, 12 .. 15 and 20 .. 27 at a time, rows 4 .. 11 of them
+  // sixteen lanes on: with chunks 2 (l / 16) and the next one these hit the banks
+  // of the others' (bank conflicts 46 % of the LDS's cycles), with neighbours they
+  // do not.  Both operands share the order, so the sums are the same.
   static_assert(kSub == 1 || (Atom::kLaneBytes == 32 && kStepBytes % 32 == 0), "chunk pairs");
   uint32_t fa[kAT ? 1 : KSTEPS], fb[kBT ? 1 : KSTEPS];
   static_for<KSTEPS>([&](auto ks) {
-    const int c = (ks * kStepBytes + lane / FR * Atom::kLaneBytes) / 16;
+    const int c = kBlocks ? lane / FR : (ks * kStepBytes + lane / FR * Atom::kLaneBytes) / 16;
     const int ra = wm0 + lane % FR, rbw = wb0 + lane % FR;
     if constexpr (!kAT) fa[ks] = (uint32_t)(ra * kRowBytes + Swz::chunk(ra, c) * 16);
     if constexpr (!kBT)
@@ -286,7 +291,7 @@ __device__ __forceinline__ void two_group_tile(const GroupedParams& p, const Til
     if constexpr (kSub == 1) {
       return *(const i32x4*)(smem + base + imm);
     } else {
-      uint32_t base_hi = base ^ 16u;
+      uint32_t base_hi = base ^ (kBlocks ? 64u : 16u);
       asm volatile("" : "+v"(base_hi));  // keep the XOR in the loop
       const i32x4 lo = *(const i32x4*)(smem + base + imm);
       const i32x4 hi = *(const i32x4*)(smem + base_hi + imm);
