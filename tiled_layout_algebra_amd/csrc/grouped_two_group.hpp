@@ -418,19 +418,22 @@ __device__ __forceinline__ void two_group_tile(const GroupedParams& p, const Til
       raw_b = sb_at[(int64_t)k * p.sb_kb];
     }
   };
-  float of_row[kTwo ? 2 : 1];
-  auto take_scales = [&]() {  // row wm0 + lane's, from what was asked for
+  // the scales of this lane's rows, 16 i + l % 16, from those that lanes 16 i + l %
+  // 16 asked for: sixteen lanes' values spread over the others by swaps of halves
+  auto place_scales = [&]() {
+    static_assert(!kBlocks || FM == 4, "sixteen lanes a tile");
     static_for<kTwo ? 2 : 1>([&](auto h) {
-      of_row[h] = raw_a * __builtin_bit_cast(float, __builtin_amdgcn_readlane(
-                                                        __builtin_bit_cast(int, raw_b), h));
-    });
-  };
-  auto place_scales = [&]() {  // the rows' of this lane's tiles
-    static_for<kTwo ? 2 : 1>([&](auto h) {
-      static_for<FM>([&](auto i) {
-        scale[h][i] = __builtin_bit_cast(float, __builtin_amdgcn_ds_bpermute(
-                                                    4 * (FR * i + lane % FR),
-                                                    __builtin_bit_cast(int, of_row[h])));
+      const uint32_t s = __builtin_bit_cast(
+          uint32_t, raw_a * __builtin_bit_cast(float, __builtin_amdgcn_readlane(
+                                                          __builtin_bit_cast(int, raw_b), h)));
+      typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+      const u32x2 half = __builtin_amdgcn_permlane32_swap(s, s, false, false);
+      static_for<2>([&](auto x) {
+        const uint32_t two = half[(int)x];
+        const u32x2 row = __builtin_amdgcn_permlane16_swap(two, two, false, false);
+        const uint32_t first = row[0], second = row[1];
+        scale[h][2 * x] = __builtin_bit_cast(float, first);
+        scale[h][2 * x + 1] = __builtin_bit_cast(float, second);
       });
     });
   };
@@ -440,7 +443,7 @@ __device__ __forceinline__ void two_group_tile(const GroupedParams& p, const Til
       // (the k-tile before's last sums, under the other group's MFMAs)
       __builtin_amdgcn_sched_barrier(0);
       block_sums.finish(scale);
-      take_scales();
+      place_scales();
       ask_scales(kt + 1);
     }
     __builtin_amdgcn_sched_barrier(0);
@@ -457,8 +460,7 @@ __device__ __forceinline__ void two_group_tile(const GroupedParams& p, const Til
       __builtin_amdgcn_sched_group_barrier(0x100, read_insts(first, n), 0);
     });
     place();
-    if constexpr (kBlocks) place_scales();
-    else advance_b(kt);
+    if constexpr (!kBlocks) advance_b(kt);
     __builtin_amdgcn_sched_barrier(0);
   };
   LineSums<kCode, FN> sums;
