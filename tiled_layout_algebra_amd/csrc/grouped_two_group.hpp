@@ -282,10 +282,10 @@ __device__ __forceinline__ void two_group_tile(const GroupedParams& p, const Til
     const int n = wb0 + 16 * (qw & 1) + 4 * (a4 & 3);
     fb[0] = (uint32_t)(B_BASE + k * kRowBT + (((n >> 3) ^ (4 * (k & 3))) * 16) + (n & 7) * 2);
   }
-  // kBlocks: six of B's fragments at a time (kTwo, with twice the scales: five), the
-  // others read between the MFMAs: 256 registers do not hold the sums, both
-  // operands and the partial sums (four at a time: 477 us for 8192^3 instead of 456)
-  constexpr int FB = kBlocks && FN > 6 ? (kTwo ? 5 : 6) : FN;
+  // kBlocks: six of B's fragments at a time, the others read between the MFMAs: 256
+  // registers do not hold the sums, both operands and the partial sums (four at a
+  // time: 477 us for 8192^3 instead of 456)
+  constexpr int FB = kBlocks && FN > 6 ? 6 : FN;
   Frag a[KSTEPS][FM], b[KSTEPS][FB];
   uint32_t xa[kShift ? KSTEPS : 1][FM], xb[kShift ? KSTEPS : 1][FN];
   auto lds_frag = [&](uint32_t base, int imm) -> Frag {
