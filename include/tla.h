@@ -435,9 +435,15 @@ int tla_gemm_blocks(const tla_gemm_blocks_args *args, void *stream);
  * that infinity or NaN.  Q: row-major, pitch ldq >= K, any alignment; its padding
  * is not written.  M or K == 0 is a no-op; M and K at most 2^31 - 4096.
  */
-int tla_quantize_blocks(int64_t M, int64_t K, const void *X, int32_t x_type, int64_t ldx,
-                        int32_t block_rows, void *Q, int64_t ldq, float *scale, int32_t s_order,
-                        int64_t lds, void *stream);
+typedef struct {
+  int64_t M, K;
+  const void *X; int32_t x_type; int64_t ldx;
+  int32_t block_rows;
+  void *Q; int64_t ldq;
+  float *scale; int32_t s_order; int64_t lds;
+} tla_quantize_blocks_args;
+
+int tla_quantize_blocks(const tla_quantize_blocks_args *args, void *stream);
 
 /* These products on the kernel asked for (ids of tla_grouped_gemm_run_variant, 0
  * to 6, of which the gradient has 0 to 3 and e4m3 1 to 6), with the same

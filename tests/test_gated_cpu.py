@@ -132,13 +132,15 @@ QUANT = dict(M=64, K=256, X=FAKE, x_type=tla.BF16, ldx=256, block_rows=1, Q=FAKE
     (dict(K=0, X=None, scale=None), tla.OK),
 ])
 def test_quantizer_refusals(kw, status):
-    a = dict(QUANT, **kw)
-    assert tla.lib().tla_quantize_blocks(*a.values(), None) == status
+    a = tla.QuantizeBlocksArgs(**dict(QUANT, **kw))
+    assert tla.lib().tla_quantize_blocks(ctypes.byref(a), None) == status
+    assert tla.lib().tla_quantize_blocks(None, None) == I
 
 
 def test_packed_arguments_are_the_structures():
     for pack, args in ((tla._PACK_GATED, tla.GatedGemmArgs), (tla._PACK_GATED_GRAD, tla.GatedGradArgs),
-                       (tla._PACK_BLOCKS, tla.GemmBlocksArgs)):
+                       (tla._PACK_BLOCKS, tla.GemmBlocksArgs),
+                       (tla._PACK_QUANT_BLOCKS, tla.QuantizeBlocksArgs)):
         values = [i + 1 for i in range(len(args._fields_))]
         a = args.from_buffer_copy(pack.pack(*values).ljust(ctypes.sizeof(args), b"\0"))
         assert [getattr(a, name) for name, _ in args._fields_] == values

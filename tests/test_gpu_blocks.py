@@ -37,6 +37,32 @@ def test_gated_every_kernel(variant, shape):
           x_order=shape % 2, w_order=shape % 3 % 2, seed=shape).call(variant=VARIANTS[variant]).verify()
 
 
+@pytest.mark.parametrize("variant", ["two_group", "direct128", "direct64"])
+def test_many_tiles(variant):
+    """Several tiles each way, experts that end inside one, the last block short."""
+    v = VARIANTS[variant]
+    Blocks([700, 0, 389, 130], 712, 664, bias=True).call(variant=v).verify()
+    Gated([700, 0, 389, 130], 392, 664, tla.E4M3).call(variant=v).verify()
+
+
+@pytest.mark.parametrize("variant", KERNELS)
+def test_more_experts_than_lanes(variant):
+    Blocks([3 if e % 7 == 2 else 0 for e in range(150)], 40, 136).call(variant=VARIANTS[variant]).verify()
+
+
+@pytest.mark.parametrize("variant", ["two_group", "direct128", "few16"])
+def test_a_large_term_beside_small_ones(variant):
+    """One product a million times the others of its block: what the 8-bit matrix
+    instruction drops of them stays within its 2^-14 of the block's magnitudes, and
+    the few-row kernel drops nothing."""
+    b = Blocks([40], 48, 256)
+    b.A[:], b.B[:] = 0.01, 0.01
+    b.A[:, 5], b.B[:, 5] = 448.0, 448.0
+    b.B[:, 5, ::2] = -448.0
+    b.sa[:], b.sb[:] = 1.0, 1.0
+    b.call(variant=VARIANTS[variant]).verify()
+
+
 @pytest.mark.parametrize("rows,K,pad,shift", [(3, 77, 0, 0), (90, 301, 1, 1), (20, 128, 3, 2), (5, 1, 0, 1),
                                               (2, 129, 0, 3)])
 def test_rows_at_any_byte(rows, K, pad, shift):

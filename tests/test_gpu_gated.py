@@ -58,6 +58,58 @@ def test_grad_every_kernel(variant, order, shape):
 
 
 @pytest.mark.parametrize("order", [NK, KN])
+@pytest.mark.parametrize("variant", ["general", "two_group", "direct128"])
+def test_many_tiles(variant, order):
+    """Several tiles each way, experts that end inside one, the last k-tile short."""
+    v = VARIANTS[variant]
+    Gated([700, 0, 389, 130], 712, 328, tla.BF16, order=order, keep=True).call(variant=v).verify()
+    Grad([700, 0, 389, 130], 712, 328, tla.F16, order=order, act=tla.ACT_GELU).call(variant=v).verify()
+
+
+@pytest.mark.parametrize("order", [NK, KN])
+def test_many_experts_and_short_lines(order):
+    """More experts than lanes, most of them empty, on every kernel."""
+    counts = [3 if e % 7 == 2 else 0 for e in range(150)]
+    for v in ((0, 1, 2, 3, 6) if order == NK else (0, 1, 2)):
+        Gated(counts, 32, 64, tla.BF16, order=order).call(variant=v).verify()
+    Gated(counts, 5, 6, tla.BF16, order=order, bias=(True, True), lost=2).call().verify()
+    Grad(counts, 5, 6, tla.BF16, order=order, lost=2).call().verify()
+
+
+@pytest.mark.parametrize("variant", ["general", "two_group", "direct64"])
+def test_offsets_past_32_bits(variant):
+    """Rows 8 MiB apart: the last ones' offsets pass 2^32 bytes in every buffer."""
+    rows, N, K, ld = 520, 64, 64, (1 << 22) + 8
+    v = VARIANTS[variant]
+    gen = torch.Generator().manual_seed(4)
+    W = (torch.randn(2, N, K, generator=gen) / 8).bfloat16()
+    X = torch.randn(rows, K, generator=gen).bfloat16()
+    pitch = ld if variant == "general" else (1 << 22) - 8
+    Xd, H, Z, Z2 = (torch.empty(rows * pitch, dtype=torch.bfloat16, device="cuda") for _ in range(4))
+    Xd.view(rows, pitch)[:, :K] = X.cuda()
+    Wd = W.cuda()
+    tla.gated_gemm(1, rows, N, K, None, Xd, tla.BF16, pitch, Wd[0], Wd[1], NK, K, 0, H, tla.BF16, pitch,
+                   Z_gate=Z, Z_up=Z2, ldz=pitch, variant=v)
+    dY = Xd  # [rows, K]
+    D, D2 = (torch.empty(rows * pitch, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    tla.gated_gemm_grad(1, rows, N, K, None, dY, tla.BF16, pitch, Wd[0], NK, K, 0, Z, Z2, pitch, D, D2,
+                        tla.BF16, pitch, variant=v)
+    torch.cuda.synchronize()
+    part = lambda t: t.view(rows, pitch)[:, :N].cpu().double()  # noqa: E731
+    g, u = X.double() @ W[0].double().t(), X.double() @ W[1].double().t()
+    e = 2.0 ** -24 * (K + 4) * (X.double().abs() @ W.double().abs().amax(0).t())
+    check(part(Z), g, e + g.abs() * 2.0 ** -8, "Z_gate")
+    check(part(Z2), u, e + u.abs() * 2.0 ** -8, "Z_up")
+    h = oga.act(g, 3) * u
+    check(part(H), h, 1.13 * e * (u.abs() + e) + e * g.abs() + h.abs() * 2.0 ** -8 + 1e-6, "H")
+    zg, zu = part(Z), part(Z2)
+    dg = g * zu * oga.act_slope(zg, 3)
+    check(part(D), dg, e * (zu.abs() + 1) + dg.abs() * 2.0 ** -8 + 1e-6, "dZ_gate")
+    check(part(D2), g * oga.act(zg, 3), e * (zg.abs() + 1) + (g * oga.act(zg, 3)).abs() * 2.0 ** -8 + 1e-6,
+          "dZ_up")
+
+
+@pytest.mark.parametrize("order", [NK, KN])
 @pytest.mark.parametrize("N,K,pad,shift", [(99, 77, 0, 0), (99, 77, 1, 1), (64, 80, 3, 1),
                                            (7, 5, 0, 0), (3, 40, 1, 1), (40, 3, 2, 1), (1, 1, 0, 0)])
 def test_rows_at_any_element(order, N, K, pad, shift):

@@ -117,3 +117,29 @@ def test_shared_buffers_and_graph():
         torch.cuda.synchronize()
         want, scale = oga.quantize_blocks(X.cpu(), 1)
         assert torch.equal(Q.cpu().double(), want) and torch.equal(S.cpu().t(), scale)
+
+
+@pytest.mark.parametrize("block_rows", [1, 128])
+def test_offsets_past_32_bits(block_rows):
+    """Rows 128 MiB apart, codes 64 MiB apart, scales far apart."""
+    M, K, ldx, ldq, lds = 70, 300, 1 << 25, 1 << 26, 1 << 24
+    gen = torch.Generator().manual_seed(8)
+    x = torch.randn(M, K, generator=gen)
+    X = torch.empty(M * ldx, device="cuda")
+    X.view(M, ldx)[:, :K] = x.cuda()
+    Q = torch.empty(M * ldq, dtype=torch.uint8, device="cuda")
+    S = torch.empty(M * lds, device="cuda")
+    tla.quantize_blocks(M, K, X, tla.F32, ldx, block_rows, Q, ldq, S, tla.ROW_MAJOR, lds)
+    torch.cuda.synchronize()
+    want, scale = oga.quantize_blocks(x, block_rows)
+    got = Q.view(M, ldq)[:, :K].cpu().contiguous().view(torch.float8_e4m3fn).double()
+    assert torch.equal(got, want)
+    assert torch.equal(S.view(M, lds)[:scale.shape[0], :3].cpu(), scale)
+
+
+@pytest.mark.parametrize("kind", [tla.F16, tla.BF16, tla.F32])
+@pytest.mark.parametrize("block_rows", [1, 128])
+def test_many_blocks(kind, block_rows):
+    """Enough blocks for several a lane, a row's last block short."""
+    gen = torch.Generator().manual_seed(2)
+    verify(torch.randn(2100, 8200, generator=gen), kind, block_rows)

@@ -115,11 +115,11 @@ def lib() -> ctypes.CDLL:
         L.tla_grouped_gemm_wgrad.argtypes = [ctypes.POINTER(GroupedWgradArgs), P]
         L.tla_gemm_i8.argtypes = [ctypes.POINTER(GemmI8Args), P]
         L.tla_quantize_rows.argtypes = [I64, I64, P, I32, I64, P, I64, P, P]
+        L.tla_quantize_blocks.argtypes = [ctypes.POINTER(QuantizeBlocksArgs), P]
         for name, args in (("gated_gemm", GatedGemmArgs), ("gated_gemm_grad", GatedGradArgs),
                            ("gemm_blocks", GemmBlocksArgs)):
             getattr(L, "tla_" + name).argtypes = [ctypes.POINTER(args), P]
             getattr(L, "tla_%s_run_variant" % name).argtypes = [ctypes.POINTER(args), I32, P]
-        L.tla_quantize_blocks.argtypes = [I64, I64, P, I32, I64, I32, P, I64, P, I32, I64, P]
         L.tla_status_string.argtypes = [ctypes.c_int]
         L.tla_status_string.restype = ctypes.c_char_p
         for name in EXPORTED:
@@ -487,6 +487,16 @@ class GemmBlocksArgs(ctypes.Structure):
     ]
 
 
+class QuantizeBlocksArgs(ctypes.Structure):
+    _fields_ = [
+        ("M", ctypes.c_int64), ("K", ctypes.c_int64), ("X", ctypes.c_void_p),
+        ("x_type", ctypes.c_int32), ("ldx", ctypes.c_int64), ("block_rows", ctypes.c_int32),
+        ("Q", ctypes.c_void_p), ("ldq", ctypes.c_int64), ("scale", ctypes.c_void_p),
+        ("s_order", ctypes.c_int32), ("lds", ctypes.c_int64),
+    ]
+
+
+_PACK_QUANT_BLOCKS = struct.Struct("2qPiqiPqPiq")
 _PACK_GATED = struct.Struct("4qPPiqPPiqqPiqPPiPPqPiqPPiqqi")
 _PACK_GATED_GRAD = struct.Struct("4qPPiqPiqqPPqPPiqPqi")
 _PACK_BLOCKS = struct.Struct("4qPPqPiqPqqPiqqPiqPii")
@@ -548,11 +558,9 @@ def gemm_blocks(groups, rows, N, K, offsets, A, lda, scale_a, sa_order, ldsa, B,
 def quantize_blocks(M, K, X, x_type, ldx, block_rows, Q, ldq, scale, s_order, lds, stream=None):
     """e4m3 codes Q and a scale for each block_rows (1 or 128) x 128 block of X
     (tla_quantize_blocks)."""
-    rc = lib().tla_quantize_blocks(M, K, _ptr(X, "X"), x_type, ldx, block_rows, _ptr(Q, "Q"), ldq,
-                                   _ptr(scale, "scale", "float32", pitched=True), s_order, lds,
-                                   _stream(stream, X, Q, scale))
-    if rc != OK:
-        raise TlaError(rc, "tla_quantize_blocks")
+    a = _PACK_QUANT_BLOCKS.pack(M, K, _ptr(X, "X"), x_type, ldx, block_rows, _ptr(Q, "Q"), ldq,
+                                _ptr(scale, "scale", "float32", pitched=True), s_order, lds)
+    _packed_call("tla_quantize_blocks", a, _stream(stream, X, Q, scale))
 
 
 # -------------------------------------------------------------- transpose

@@ -323,20 +323,20 @@ int tla_gemm_blocks_run_variant(const tla_gemm_blocks_args* a, int32_t variant, 
   return variant_ok(variant) ? call(plan_blocks, a, variant, stream) : TLA_ERR_INVALID_ARG;
 }
 
-int tla_quantize_blocks(int64_t M, int64_t K, const void* X, int32_t x_type, int64_t ldx,
-                        int32_t block_rows, void* Q, int64_t ldq, float* scale, int32_t s_order,
-                        int64_t lds, void* stream) {
-  if (M < 0 || K < 0 || (block_rows != 1 && block_rows != 128) || !order_ok(s_order))
+int tla_quantize_blocks(const tla_quantize_blocks_args* a, void* stream) {
+  if (!a || a->M < 0 || a->K < 0 || (a->block_rows != 1 && a->block_rows != 128) ||
+      !order_ok(a->s_order))
     return TLA_ERR_INVALID_ARG;
-  if (!aux_type(x_type) || M > kMaxExtent || K > kMaxExtent) return TLA_ERR_UNSUPPORTED;
-  if (M == 0 || K == 0) return TLA_OK;
-  const int64_t rows = block_rows == 1 ? M : blocks_of(M);
-  if (!X || !Q || ldx < K || ldq < K || !aligned_to(X, type_bytes(x_type)) ||
-      !scales_ok(scale, s_order, lds, rows, blocks_of(K)))
+  if (!aux_type(a->x_type) || a->M > kMaxExtent || a->K > kMaxExtent) return TLA_ERR_UNSUPPORTED;
+  if (a->M == 0 || a->K == 0) return TLA_OK;
+  const int64_t rows = a->block_rows == 1 ? a->M : blocks_of(a->M);
+  if (!a->X || !a->Q || a->ldx < a->K || a->ldq < a->K || !aligned_to(a->X, type_bytes(a->x_type)) ||
+      !scales_ok(a->scale, a->s_order, a->lds, rows, blocks_of(a->K)))
     return TLA_ERR_INVALID_ARG;
-  const bool row = s_order == TLA_ROW_MAJOR;
-  return launch_quantize_blocks(M, K, X, x_type, ldx, block_rows, (uint8_t*)Q, ldq, scale,
-                                row ? lds : 1, row ? 1 : lds, (hipStream_t)stream);
+  const bool row = a->s_order == TLA_ROW_MAJOR;
+  return launch_quantize_blocks(a->M, a->K, a->X, a->x_type, a->ldx, a->block_rows, (uint8_t*)a->Q,
+                                a->ldq, a->scale, row ? a->lds : 1, row ? 1 : a->lds,
+                                (hipStream_t)stream);
 }
 
 }  // extern "C"

@@ -14,12 +14,16 @@ __global__ __launch_bounds__(256) void gated_small_kernel(const GroupedParams p,
   const int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (x >= (int64_t)p.rows * p.N) return;
   const int row = (int)(x / p.N), n = (int)(x % p.N);
+  // the last expert that starts at or before the row
   int e = 0, lo, hi;
-  for (; e < p.groups; ++e) {
-    expert_rows(p, e, lo, hi);
-    if (lo <= row && row < hi) break;
+  for (int above = p.groups; above - e > 1;) {
+    const int mid = e + (above - e) / 2;
+    expert_rows(p, mid, lo, hi);
+    if (lo <= row) e = mid;
+    else above = mid;
   }
-  if (e == p.groups) return;  // a row of no expert
+  expert_rows(p, e, lo, hi);
+  if (row < lo || row >= hi) return;  // a row of no expert
   const uint8_t* a = p.A + (int64_t)row * p.lda * 2;
   const int64_t first = (int64_t)e * p.stride_b + (b_kc ? n * p.ldb : n), step = b_kc ? 1 : p.ldb;
   float g = 0.f, u = 0.f;
