@@ -17,15 +17,16 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libtla.so")
-SOURCES = ["api.cpp", "algebra.cpp", "gemm.hip", "gemm_general.hip", "gemm_pingpong.hip",
-           "conv_slab.hip", "transpose.hip", "layout_eval.hip", "operators_api.cpp",
-           "grouped_direct.hip", "grouped_direct_rows.hip", "grouped_direct_shift.hip",
-           "grouped_few_rows.hip", "grouped_general.hip", "grouped_two_group.hip", "grouped_two_group_8bit.hip",
-           "grouped_two_group_rows.hip", "grouped_two_group_shift.hip", "quantize.hip",
-           "gated_api.cpp", "gated_direct.hip", "gated_few_rows.hip", "gated_general.hip",
+# the longest compilations first, so that none of them is left to run alone
+SOURCES = ["gemm_general.hip", "grouped_two_group_shift.hip", "gemm_pingpong.hip",
+           "grouped_general.hip", "grouped_two_group_8bit.hip", "grouped_two_group_rows.hip",
+           "grouped_two_group.hip", "gemm.hip", "grouped_direct_shift.hip", "grouped_direct.hip",
+           "blocks_two_group.hip", "gated_two_group_grad_nk.hip", "gated_two_group_grad_kn.hip",
            "gated_two_group_gated_nk.hip", "gated_two_group_gated_kn.hip",
-           "gated_two_group_grad_nk.hip", "gated_two_group_grad_kn.hip", "blocks_direct.hip",
-           "blocks_few_rows.hip", "blocks_two_group.hip", "quantize_blocks.hip"]
+           "grouped_direct_rows.hip", "grouped_few_rows.hip", "gated_direct.hip",
+           "gated_general.hip", "conv_slab.hip", "blocks_direct.hip", "blocks_few_rows.hip",
+           "gated_few_rows.hip", "quantize.hip", "quantize_blocks.hip", "transpose.hip",
+           "layout_eval.hip", "api.cpp", "algebra.cpp", "operators_api.cpp", "gated_api.cpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
@@ -68,7 +69,7 @@ def build(verbose: bool = True, only_changed: bool = False) -> str:
     older than the source or any header) and link libtla.so."""
     os.makedirs(BUILD, exist_ok=True)
     todo = [s for s in SOURCES if not only_changed or _stale(s)]
-    with ThreadPoolExecutor(max_workers=max(len(todo), 1)) as ex:
+    with ThreadPoolExecutor(max_workers=min(max(len(todo), 1), os.cpu_count() or 1, 16)) as ex:
         list(ex.map(_compile, todo))
     objs = [os.path.join(BUILD, os.path.splitext(s)[0] + ".o") for s in SOURCES]
     tmp = LIB + ".tmp%d" % os.getpid()

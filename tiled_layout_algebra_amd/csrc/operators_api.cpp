@@ -121,7 +121,14 @@ double two_group_rounds(const tla_grouped_gemm_args* a, bool halves) {
 // and in bf16 for 32 experts of 2048 x 4096: 128 rows 110 (few 16), 123
 // (64x128), 4096 rows 174 (64x128), 144 (128x128), 147 (256x256); for 8
 // experts of 4096 x 4096 with 2000 rows 129, 123, 89.
-Kernel choose(const tla_grouped_gemm_args* a, int eb, bool b_kc, unsigned allowed) {
+// What differs for the operators on these kernels (gated_api.cpp): `own`, MB/us of
+// the weights at which a few-row kernel takes an expert's first block of rows and
+// each further one, and us a k-tile of the block-scaled kernels of 64 and 128 rows.
+struct Rates {
+  bool own = false, blocks = false;
+  double few[3][2] = {{5.0, 5.0}, {3.3, 3.3}, {2.2, 2.2}};
+};
+Kernel choose(const tla_grouped_gemm_args* a, int eb, bool b_kc, unsigned allowed, const Rates& r) {
   const double live = (double)(a->rows < a->groups ? a->rows : a->groups);
   const double matrix = (double)a->N * (double)a->K * eb * 1e-6;  // MB
   const double weights = live * matrix / 5.0;
@@ -143,13 +150,25 @@ Kernel choose(const tla_grouped_gemm_args* a, int eb, bool b_kc, unsigned allowe
   auto rounds = [](double t) { return (double)(int64_t)((t + 255.0) / 256.0); };
   // each block of rows reads the weights again, at the rate the matrix
   // instructions and A's rows leave
-  consider(kFewRows1, 4.0 + row_blocks(a, 16) * matrix / 5.0);
-  consider(kFewRows2, 4.3 + row_blocks(a, 32) * matrix / 3.3);
-  consider(kFewRows4, 5.0 + row_blocks(a, 64) * matrix / 2.2);
+  auto few = [&](double least, int64_t bm, const double (&rate)[2]) {
+    if (!r.own) return least + row_blocks(a, (double)bm) * matrix / rate[0];
+    // one expert's blocks are a whole number
+    const double n = a->groups == 1 ? (double)((a->rows + bm - 1) / bm) : row_blocks(a, (double)bm);
+    const double once = n < live ? n : live;
+    return least + matrix * (once / rate[0] + (n - once) / rate[1]);
+  };
+  consider(kFewRows1, few(4.0, 16, r.few[0]));
+  consider(kFewRows2, few(4.3, 32, r.few[1]));
+  consider(kFewRows4, few(5.0, 64, r.few[2]));
   const double t64 = tiles(64, 128), t128 = tiles(128, 128);
   auto at_least = [](double least, double us) { return us > least ? us : least; };
-  consider(kDirect64, 4.2 + kt * at_least(0.3, (eb == 1 ? 0.0015 : 0.0019) * t64));
-  consider(kDirect128, 4.5 + kt * (t128 <= 128.0 ? 0.4 : t128 <= 256.0 ? 0.54 : 0.62 * rounds(t128)));
+  if (r.blocks) {
+    consider(kDirect64, 4.2 + kt * at_least(0.45, 0.0018 * t64));
+    consider(kDirect128, 4.5 + kt * (t128 <= 256.0 ? 0.72 : at_least(1.15, 1.15 / 512.0 * t128)));
+  } else {
+    consider(kDirect64, 4.2 + kt * at_least(0.3, (eb == 1 ? 0.0015 : 0.0019) * t64));
+    consider(kDirect128, 4.5 + kt * (t128 <= 128.0 ? 0.4 : t128 <= 256.0 ? 0.54 : 0.62 * rounds(t128)));
+  }
   const double mixed = two_group_rounds(a, false), halved = two_group_rounds(a, true);
   const double two = mixed < halved ? mixed : halved;
   consider(kTwoGroup, at_least(4.0 + 1.2 * weights, 5.0 + kt * 1.6 * two));
@@ -228,7 +247,7 @@ int plan_product(const tla_grouped_gemm_args* a, Plan* out) {
   if (!launches(kGeneral, a)) return TLA_ERR_UNSUPPORTED;
   out->type = a->type;
   out->b_kc = b_kc;
-  out->kernel = choose(a, eb, b_kc, kAnyKernel);
+  out->kernel = choose(a, eb, b_kc, kAnyKernel, Rates{});
   return TLA_OK;
 }
 
@@ -274,8 +293,26 @@ int run_product(const tla_grouped_gemm_args* a, hipStream_t stream, int forced =
 
 namespace tla {
 
+// Measured, 4096 x 4096 (us; few 16, 32, 64, then 64 x 128, 128 x 128, 256 x 256):
+//   block-scaled         24 rows  10.4   8.2  10.3   18.7  27  32
+//                        48       14    14.3  11.5   18.7  27  32
+//                        96       24    19    24     18.6  27  32
+//                       800                          26.7  28  33
+//                      1600                                41  34
+//   gated, block-scaled  24       14    10.7  12     19     27  33
+//                        48       19    20    14.5   19     27  33
+//                        96       35    30    27     19     27  34
+//   gated, bf16          24       24    16.5  18     23     25  40
+//                        48       35    31    22.7   23     26  41
+//                       400                          35-38      58
 Kernel choose_product(const tla_grouped_gemm_args* a, int eb, bool b_kc, unsigned allowed) {
-  return choose(a, eb, b_kc, allowed);
+  Rates rates;
+  rates.own = true;
+  rates.blocks = eb == 1;
+  const double few[3][2] = {{5.0, 5.0}, {4.5, 2.8}, {3.0, 1.8}};
+  for (int i = 0; i < 3; ++i)
+    for (int j = 0; j < 2; ++j) rates.few[i][j] = few[i][j];
+  return choose(a, eb, b_kc, allowed, rates);
 }
 bool product_halves(const tla_grouped_gemm_args* a) {
   return two_group_rounds(a, true) < two_group_rounds(a, false);
