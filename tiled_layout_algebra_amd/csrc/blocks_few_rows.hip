@@ -1,5 +1,6 @@
 // blocks_few_rows.hip -- launches of the kernel for few rows
-// (grouped_few_rows.hpp): e4m3 with block scales, plain and gated.
+// (grouped_few_rows.hpp): e4m3 with block scales, plain and gated.  Bound by the weights'
+// way from memory (figures there).
 #include "grouped_few_rows.hpp"
 
 namespace tla {

@@ -1,6 +1,12 @@
 // gated_common.hpp -- what the kernels of the gated feed-forward products and
 // of the block-scaled e4m3 product share: the block-scaled matrix-core atom and
 // the epilogues.
+//
+//   forward   g = sum + bias, u = sum + bias, H = act(g) u
+//   backward  dh = sum;  dgate = dh u act'(g),  dup = dh act(g),  H = act(g) u
+//   SiLU      z s(z), derivative s(z) (1 + z (1 - s(z))), s(z) = 1 / (1 + e^-z)
+//   GELU      the polynomials of grouped_common.hpp
+// All in fp32 from the fp32 sums; each result is rounded once, when it is written.
 #pragma once
 
 #include "grouped_common.hpp"

@@ -1,6 +1,7 @@
 // gated_few_rows.hip -- launches of the kernel for few rows
 // (grouped_few_rows.hpp): the gated product in 16 bits.  A workgroup has 16
-// columns of both projections.
+// columns of both projections.  Bound by the weights' way from memory (figures in
+// grouped_few_rows.hpp).
 #include "grouped_few_rows.hpp"
 
 namespace tla {

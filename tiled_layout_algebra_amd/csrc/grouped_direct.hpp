@@ -16,7 +16,9 @@
 // 2048 x 4096 151 us (128 x 128; 537 MB of weights: 3.6 TB/s), 2048 rows 117 us
 // (64 x 128; 4.6 TB/s), int8 512 rows x 4096 x 4096 17 us; kNKShift, 4096 rows 2048 x
 // 4095 241 us (its dword loads and copies across two lines cost the difference);
-// 777 rows' fp32 gradients on 16 experts of 512 x 1024 12 us (33.5 MB written).
+// 777 rows' fp32 gradients on 16 experts of 512 x 1024 12 us (33.5 MB written).  The
+// gated forms (Role, as in grouped_two_group.hpp; half as many columns of the result):
+// bf16, 4096 x 4096, 96 rows or fewer 23 us (64 x 128), 400 rows 35-38 (128 x 128).
 #pragma once
 
 #include "gated_common.hpp"

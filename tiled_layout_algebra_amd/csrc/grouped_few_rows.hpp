@@ -13,11 +13,15 @@
 // Weights of 8 bits are read as they are: int8 goes to the integer
 // instruction, e4m3 is widened to f16, which holds it exactly.
 //
-// Bound by memory.  Measured: bf16, 128 rows on 32 experts of 2048 x 4096 110 us
-// (537 MB of weights: 4.9 TB/s; a large copy reaches 6.7, reads and writes together),
-// two rows on two experts of 4096 x 4096 12-13.6 us (67 MB: 5 TB/s and more); one
+// Bound by memory.  Measured: bf16, 128 rows on 32 experts of 2048 x 4096 106 us
+// (537 MB of weights: 5.1 TB/s; a large copy reaches 6.7, reads and writes together),
+// two rows on two experts of 4096 x 4096 12-13 us (67 MB: 5 TB/s and more); one
 // row x 4096 x 4096 6.3 us in int8 and in e4m3, of which about 4 are a launch's; 128
-// e4m3 rows on the 32 experts 43 us.
+// e4m3 rows on the 32 experts 43 us.  Gated (the NT fragments are as many of the gate's
+// columns and the same of up's), one bf16 row x 8192 x 4096, SiLU: 26.9 us a call, 22.8
+// on the card (134 MB: 5.9 TB/s).  Block scales (kBlocks: two steps of 64 are a block, whose
+// partial sums are scaled into the sums): one row x 4096 x 4096 7.2 us, 128 rows on the
+// 32 experts 52-55 (253 MB: 4.9 TB/s).
 #pragma once
 
 #include "gated_common.hpp"

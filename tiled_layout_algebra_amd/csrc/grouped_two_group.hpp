@@ -27,6 +27,17 @@
 //             operations a fragment, under the other group's MFMAs).  A k-tile
 //             uses 96 of the window's 128 bytes, so that dword is always in it:
 //             three MFMA steps a period instead of four.
+//   Role      kGated: half of B's slab is columns of the gate's projection, half the
+//             same columns of up's, so that a lane holds both sums of an element and
+//             the epilogue has act(gate) up without meeting another lane; a tile is
+//             256 x 128 of the result.  kGateGrad: a plain product whose epilogue
+//             reads gate and up and writes both gradients (and the hidden values):
+//             the product itself is never stored.
+//   e4m3 with block scales  a k-tile is a block of 128 of K.  The matrix instruction
+//             starts from zero and its result is scaled into the sums by vector
+//             multiply-adds, which run under the other group's MFMAs.  Scales travel
+//             with the fragments' lanes and are spread by register swaps (by LDS
+//             permutes: 456 us for 8192^3 instead of 442).
 //
 // Bound by the matrix cores (busy 0.72 of the time in the int8 case below, at
 // the clock that leaves).  Measured, calls in a row on the same buffers; boxes
@@ -38,7 +49,14 @@
 // pre-activation or in fp32, and every compute unit does so at once); 8192^3 with
 // bias and GELU 472 us = 2330 TOP/s in int8, 411 us = 2670 TFLOP/s in e4m3; kNKShift
 // on 8 experts of 4096 x 4095 720 us.  A round of tiles that fills part of the card
-// costs most of a whole one: see two_group_lookup.
+// costs most of a whole one: see two_group_lookup.  kGated, bf16, 8192 rows x 8192
+// columns x 4096, SiLU, gate and up kept: 820-845 us = 1320 TFLOP/s, of which the 400
+// MB written are 60 (MFMA busy 0.78).  kGateGrad at the same sizes, SiLU, hidden
+// written: 538 us; a tile's epilogue moves 640 KiB, and every compute unit does so at
+// once (busy 0.56).  Every other unit begun half a tile ahead, so that epilogues meet
+// products: 616 instead of 579 then, its half tiles cost more.  Block scales: 8192^3
+// 440 us = 2500 TFLOP/s, e4m3 without scales 390 on that box, at 1.66 GHz both by the
+// card's power (busy 0.65); gated, 2048 x 8192 x 4096, 120 us, two rounds of tiles.
 #pragma once
 
 #include "gated_common.hpp"
@@ -422,20 +440,22 @@ __device__ __forceinline__ void two_group_tile(const GroupedParams& p, const Til
   // 16 asked for: sixteen lanes' values spread over the others by swaps of halves
   auto place_scales = [&]() {
     static_assert(!kBlocks || FM == 4, "sixteen lanes a tile");
-    static_for<kTwo ? 2 : 1>([&](auto h) {
-      const uint32_t s = __builtin_bit_cast(
-          uint32_t, raw_a * __builtin_bit_cast(float, __builtin_amdgcn_readlane(
-                                                          __builtin_bit_cast(int, raw_b), h)));
-      typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
-      const u32x2 half = __builtin_amdgcn_permlane32_swap(s, s, false, false);
-      static_for<2>([&](auto x) {
-        const uint32_t two = half[(int)x];
-        const u32x2 row = __builtin_amdgcn_permlane16_swap(two, two, false, false);
-        const uint32_t first = row[0], second = row[1];
-        scale[h][2 * x] = __builtin_bit_cast(float, first);
-        scale[h][2 * x + 1] = __builtin_bit_cast(float, second);
+    if constexpr (kBlocks) {
+      static_for<kTwo ? 2 : 1>([&](auto h) {
+        const uint32_t s = __builtin_bit_cast(
+            uint32_t, raw_a * __builtin_bit_cast(float, __builtin_amdgcn_readlane(
+                                                            __builtin_bit_cast(int, raw_b), h)));
+        typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+        const u32x2 half = __builtin_amdgcn_permlane32_swap(s, s, false, false);
+        static_for<2>([&](auto x) {
+          const uint32_t two = half[(int)x];
+          const u32x2 row = __builtin_amdgcn_permlane16_swap(two, two, false, false);
+          const uint32_t first = row[0], second = row[1];
+          scale[h][2 * x] = __builtin_bit_cast(float, first);
+          scale[h][2 * x + 1] = __builtin_bit_cast(float, second);
+        });
       });
-    });
+    }
   };
   auto memory_phase = [&](int kt, int ct, int slot, bool live, auto copies) {
     constexpr int kPer = kReads / copies, kRem = kReads % copies;

@@ -6,6 +6,9 @@
 // Memory-bound: each value is read once, kept in registers over its block's
 // reduction and written as one byte.  1 x 128: sixteen lanes share a block, eight
 // values each.  128 x 128: a workgroup has a block, 16 lanes a row, 8 rows a lane.
+// Measured: 16384 x 8192 bf16 (403 MB) 84 us in 1 x 128 and 81 in 128 x 128, 4.8 and
+// 5.0 TB/s of a large copy's 6.6; 8191 columns, whose rows begin anywhere in a line, 92
+// and 93; 8192 x 8192 fp32 62 us; 64 x 4096 3.5 us on the card, a launch.
 //
 // Exact rounding without a division: with i the hardware's reciprocal of s (one
 // unit off at most), x i (1 - 2^-21) and x i (1 + 2^-21), rounding errors included,
@@ -168,7 +171,7 @@ struct QuantArgs {
 
 // Workgroup b runs on XCD b % 8: each XCD gets a run of neighbours, so that lines
 // which two blocks share are read into one L2 (16384 x 8191 bf16, whose rows begin
-// anywhere in a line: TIME).
+// anywhere in a line, in blocks of 128 x 128: 131 us without, 93 with).
 __device__ __forceinline__ unsigned in_runs(unsigned b, unsigned n) {
   const unsigned per = n / 8, rest = n % 8, xcd = b & 7;
   return xcd * per + min(xcd, rest) + (b >> 3);
@@ -206,7 +209,7 @@ __global__ __launch_bounds__(256) void quantize_row_blocks_kernel(const QuantArg
 }
 
 // 128 x 128: a workgroup a block.  (Four neighbouring blocks and 1024 threads, whose
-// loads are 1 KiB of a row: 134 us instead of TIME for 16384 x 8191 bf16.)
+// loads are 1 KiB of a row: 134 us instead of 93 for 16384 x 8191 bf16.)
 template <int kCode>
 __global__ __launch_bounds__(512) void quantize_square_blocks_kernel(const QuantArgs a) {
   const int tid = threadIdx.x;
