@@ -433,7 +433,8 @@ int tla_gemm_blocks(const tla_gemm_blocks_args *args, void *stream);
  * the last blocks may be short.  A block of zeros, or one whose scale rounds to
  * 0, gets zero codes; so does a block with an infinity or a NaN, whose scale is
  * that infinity or NaN.  Q: row-major, pitch ldq >= K, any alignment; its padding
- * is not written.  M or K == 0 is a no-op; M and K at most 2^31 - 4096.
+ * is not written.  M or K == 0 is a no-op; M and K at most 2^31 - 4096, with
+ * block_rows 128 K at most 2^30 - 128.
  */
 typedef struct {
   int64_t M, K;

@@ -130,6 +130,7 @@ QUANT = dict(M=64, K=256, X=FAKE, x_type=tla.BF16, ldx=256, block_rows=1, Q=FAKE
     (dict(lds=63), I), (dict(s_order=tla.ROW_MAJOR, lds=1), I), (dict(X=FAKE + 1), I),
     (dict(x_type=tla.F32, X=FAKE + 2), I), (dict(scale=FAKE + 2), I), (dict(M=0, X=None), tla.OK),
     (dict(K=0, X=None, scale=None), tla.OK),
+    (dict(K=2 ** 30 - 127, ldx=2 ** 30, ldq=2 ** 30, block_rows=128), U),
 ])
 def test_quantizer_refusals(kw, status):
     a = tla.QuantizeBlocksArgs(**dict(QUANT, **kw))

@@ -63,6 +63,31 @@ def test_serving_step_by_step(counts, width, hidden):
     check(y, z, e + half_step(z.abs() + e, tla.BF16), "y")
 
 
+def test_rows_of_no_expert():
+    """No rows at all, and experts that end before the last row: what is there equals
+    the same layer's results on those rows alone, and gradients without a row are zero."""
+    from tiled_layout_algebra_amd.gated_layer import GatedLayer
+    gen = torch.Generator().manual_seed(2)
+    W = torch.randn(2, 2 * 72, 136, generator=gen).bfloat16().cuda()
+    W2 = torch.randn(2, 136, 72, generator=gen).bfloat16().cuda()
+    layer = GatedLayer(W, W2).quantize()
+    x, dy = (torch.randn(9, 136, generator=gen).bfloat16().cuda() for _ in range(2))
+
+    def run(x, dy, off):
+        off = torch.tensor(off, dtype=torch.int32).cuda()
+        y, saved = layer.forward(x, off)
+        return y, layer.backward(dy, saved), layer.serve(x, off)[0]
+
+    y, grads, few = run(x[:0], dy[:0], [0, 0, 0])
+    assert y.shape == few.shape == grads[0].shape == (0, 136)
+    assert not grads[1].any() and not grads[2].any()
+    some, all_ = run(x[:5], dy[:5], [0, 0, 5]), run(x, dy, [0, 0, 5])
+    assert torch.equal(some[0], all_[0][:5]) and torch.equal(some[2], all_[2][:5])
+    assert torch.equal(some[1][0], all_[1][0][:5])
+    for a, b in zip(some[1][1:], all_[1][1:]):
+        assert torch.equal(a, b) and not b[0].any()
+
+
 def test_command():
     import subprocess
     import sys
