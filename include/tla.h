@@ -376,7 +376,7 @@ int tla_gated_gemm(const tla_gated_gemm_args *args, void *stream);
  * where they are halves of a buffer), the weight and bias gradients
  * tla_grouped_gemm_wgrad.
  * type F16 or BF16, of everything (d_type: the same).  Outputs must not overlap each other or an input.
- * K == 0 gives dh = 0.  The rest as above, with N columns in the extents.
+ * K == 0 gives dh = 0.  The rest as above.
  */
 typedef struct {
   int64_t groups, rows, N, K;
@@ -406,8 +406,9 @@ int tla_gated_gemm_grad(const tla_gated_grad_args *args, void *stream);
  * A block's products are summed by the 8-bit matrix instruction, which loses
  * what lies below about 2^-14.3 of the largest; that sum times both scales is
  * added in fp32.  With few rows they are summed exactly instead.
- * Extents, offsets, padding, aliasing and no-ops as for tla_grouped_gemm; rows
- * that do not start on dwords run at the few-row kernel's rate.
+ * Extents (2 N in the place of N), offsets, padding, aliasing and no-ops as for
+ * tla_grouped_gemm; rows that do not start on dwords run at the few-row kernel's
+ * rate.
  */
 typedef struct {
   int64_t groups, rows, N, K;
