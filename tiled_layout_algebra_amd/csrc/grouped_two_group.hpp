@@ -60,14 +60,12 @@
 #pragma once
 
 #include "gated_common.hpp"
+#include "two_group_lds.hpp"
 
 namespace tla {
 namespace {
 
 enum Form : int { kNK = 0, kKN = 1, kGrad = 2, kNKShift = 3 };
-
-// LDS bytes of the workgroup
-constexpr int kTwoGroupLds = 5 * 256 * 128;
 
 // Where a workgroup's tile lies: rows m0 .. of the expert, which end at m_end;
 // columns n0 ..; the operands' bases, and the length of the sum.  Product: rows
@@ -104,7 +102,7 @@ __device__ __forceinline__ void two_group_tile(const GroupedParams& p, const Til
   constexpr int kSub = Atom::kLaneBytes / 16;   // 16-byte reads per fragment
   constexpr int kStepBytes = Atom::kK * EB;
   constexpr int SLAB = BN * kRowBytes;          // 32 KiB: one operand, one k-tile
-  constexpr int B_BASE = 2 * SLAB;              // LDS: [A0 A1 | B0 B1 B2]
+  constexpr int B_BASE = kTwoGroupB;            // LDS: [A0 A1 | B0 B1 B2]
   constexpr int kCopies = SLAB / (256 * 16);    // 16-byte copies per thread per slab
   constexpr int kCopiesA = BM * kRowBytes / (256 * 16);
   constexpr int kRowBT = kRole == kGated ? 256 : 512;  // bytes of a k row in B's slab
@@ -112,7 +110,7 @@ __device__ __forceinline__ void two_group_tile(const GroupedParams& p, const Til
   static_assert(!kShift || (kSub == 1 && kStepBytes == 32), "a dword follows every fragment");
   static_assert((1 << Slab<kRowBytes>::kRowShift) * kChunks <= 32,
                 "the swizzle repeats within 32 rows");
-  static_assert(5 * SLAB == kTwoGroupLds && 5 * SLAB <= 160 * 1024, "LDS budget");
+  static_assert(SLAB == kTwoGroupSlab && kTwoGroupLds <= 160 * 1024, "LDS budget");
   static_assert(!kHalf || kForm != kGrad, "blocks of rows");
   static_assert(!kBT || EB == 2, "slabs of k rows: 16-bit operands");
 
@@ -627,10 +625,12 @@ __device__ __forceinline__ void two_group_tile(const GroupedParams& p, const Til
     }
     if constexpr (kBlocks) block_sums.finish(scale);
   }
-  // Every LDS read of the main loop finished before the last barrier and no
-  // copy is in flight, so the slots are free for the epilogue: group 0
-  // starts while group 1 still multiplies the last k-tile.
-  uint8_t* region = smem + wave * WM * WN * 2;
+  // The epilogue's regions lie where nothing is read or copied any more: group 0
+  // starts while group 1 still multiplies the last k-tile, a wave of group 1 while
+  // the group's others do.
+  constexpr bool kLate = FB < FN;  // fragments of B are read between the MFMAs
+  static_assert(!kLate || 2 * WM * WN * 2 <= SLAB, "two regions in a B slot");
+  uint8_t* region = smem + two_group_region(wave, WM * WN * 2, kLate, KT);
   if constexpr (kForm == kGrad) {
     if (sum_b) sums.template write<FN>(p.dbias + (int64_t)e * p.N, n0 + wn0, p.N, lane);
     if (sum_a) sums.template write<FM>(p.dbias + (int64_t)e * p.M, m0 + wm0, p.M, lane);
