@@ -608,7 +608,8 @@ __device__ __forceinline__ void two_group_tile(const GroupedParams& p, const Til
       for (int kt = 0; kt < KT; ++kt) {
         memory_phase(kt, kt + 2, (kt + 2) % 3, kt + 2 < KT, CopiesB{});
         wait_lgkmcnt0();
-        wait_vmcnt<kCopies + kScaleLoads>();         // B of kt+1 landed
+        if (kt + 1 < KT) wait_vmcnt<kCopies + kScaleLoads>();  // B of kt+1 landed
+        else wait_vmcnt<0>();  // behind this barrier no copy, record-less or not, lands in a region
         barrier();
         if constexpr (kForm != kGrad) {
           // while group 0 clears the last k-tile's A, before it reads it
@@ -621,7 +622,6 @@ __device__ __forceinline__ void two_group_tile(const GroupedParams& p, const Til
         pin();
         if (kt + 1 < KT) barrier();
       }
-      wait_vmcnt<0>();  // the last (record-less) copies
     }
     if constexpr (kBlocks) block_sums.finish(scale);
   }
