@@ -71,3 +71,28 @@ def test_grouped(kind, order, variant, lengths):
             tla.grouped_gemm(*c.keep[0], **c.keep[1], variant=variant)
             torch.cuda.synchronize()
             assert torch.equal(first.view(torch.int16), c.D.view(torch.int16))
+
+
+@pytest.mark.parametrize("kind,orders,lengths", [
+    (tla.BF16, (tla.ROW_MAJOR, tla.COL_MAJOR), SHORTER), (tla.F16, (tla.ROW_MAJOR, tla.ROW_MAJOR), SHORTER),
+    (tla.BF16, (tla.COL_MAJOR, tla.ROW_MAJOR), SHORTER), (tla.E4M3, (tla.ROW_MAJOR, tla.COL_MAJOR), (384, 512, 640))])
+def test_ungrouped(kind, orders, lengths):
+    """The same program without groups (variant 0), 264 tiles."""
+    M, N = 5904, 2816
+    t = {tla.BF16: torch.bfloat16, tla.F16: torch.float16, tla.E4M3: torch.float8_e4m3fn}[kind]
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    for K in lengths:
+        A, B = (torch.randn(*s, generator=gen, device="cuda").to(t) for s in ((M, K), (N, K)))
+        want, size = A.double() @ B.double().t(), A.double().abs() @ B.double().abs().t()
+        bound = size * ((K + 4) * 2.0 ** -24 + (2.0 ** -14 if kind == tla.E4M3 else 0.0)) + want.abs() * 2.0 ** -8
+        a, b = (x if o == major else x.view(torch.int16).t().contiguous().view(t)
+                for x, o, major in ((A, orders[0], tla.ROW_MAJOR), (B, orders[1], tla.COL_MAJOR)))
+        first = None
+        for _ in range(4):
+            D = torch.full((M, N), 7.0, dtype=torch.bfloat16, device="cuda")
+            tla.gemm_epilogue(M, N, K, a, kind, orders[0], a.shape[1], b, kind, orders[1], b.shape[1], D, tla.BF16,
+                              tla.ROW_MAJOR, N, act=tla.ACT_NONE, variant=0)
+            torch.cuda.synchronize()
+            assert ((D.double() - want).abs() <= bound).all()
+            assert first is None or torch.equal(first.view(torch.int16), D.view(torch.int16))
+            first = D

@@ -335,7 +335,8 @@ __global__ __launch_bounds__(512) void gemm_pingpong_kernel(const GemmParams p) 
       for (int kt = 0; kt < KT; ++kt) {
         memory_phase(kt, kt + 2, (kt + 2) % 3, kt + 2 < KT);
         wait_lgkmcnt0();
-        wait_vmcnt<kCopies>();                       // B of kt+1 landed
+        if (kt + 1 < KT) wait_vmcnt<kCopies>();      // B of kt+1 landed
+        else wait_vmcnt<0>();  // behind this barrier no copy, record-less or not, lands in a region
         barrier();
         compute();
 #pragma unroll
@@ -344,7 +345,6 @@ __global__ __launch_bounds__(512) void gemm_pingpong_kernel(const GemmParams p) 
           for (int j = 0; j < FN; ++j) asm volatile("" ::"v"(acc[i][j]));
         if (kt + 1 < KT) barrier();
       }
-      wait_vmcnt<0>();  // the last (record-less) copies
     }
   }
   // Every LDS read of the main loop finished before the last barrier and no
