@@ -120,6 +120,16 @@ __device__ __forceinline__ float act_any(float z, int act) {
   return y;
 }
 
+// v, which the compiler has to take for different in each lane: a load at this offset
+// is a vector load, in order with the others in vmcnt, where one that is the same for
+// all lanes may become a scalar load, which vmcnt does not count.
+__device__ __forceinline__ int64_t per_lane(int64_t v) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  asm volatile("" : "+v"(v));
+#endif
+  return v;
+}
+
 // Orders a wave's LDS accesses of different types
 __device__ __forceinline__ void wave_fence() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
 

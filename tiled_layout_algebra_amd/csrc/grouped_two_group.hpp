@@ -419,8 +419,9 @@ __device__ __forceinline__ void two_group_tile(const GroupedParams& p, const Til
   float raw_a = 0.f, raw_b = 0.f, scale[2][FM];
   if constexpr (kBlocks) {
     sa_at = p.sa + (int64_t)min(m0 + wm0 + lane, m_end - 1) * p.sa_row;
-    sb_at = (kTwo && (lane & 1) ? p.sb2 : p.sb) + (int64_t)e * p.stride_sb +
-            (int64_t)(min(n0 + wb0, p.N - 1) >> 7) * p.sb_col;
+    // (per_lane: the waits for copies count both loads)
+    sb_at = (kTwo && (lane & 1) ? p.sb2 : p.sb) +
+            per_lane((int64_t)e * p.stride_sb + (int64_t)(min(n0 + wb0, p.N - 1) >> 7) * p.sb_col);
   }
   if constexpr (kBlocks) {
     // the first k-tile finds nothing to finish
