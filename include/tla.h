@@ -403,9 +403,11 @@ int tla_gated_gemm_grad(const tla_gated_grad_args *args, void *stream);
  * stride_sb elements apart.  The last block of K and of N may be short.  D F16
  * or BF16; bias (groups x N, dense, or NULL) F16, BF16 or F32; act any of
  * tla_act.
- * A block's products are summed by the 8-bit matrix instruction, which loses
- * what lies below about 2^-14.3 of the largest; that sum times both scales is
- * added in fp32.  With few rows they are summed exactly instead.
+ * From K = 512 on a block's products are summed by the 8-bit matrix instruction,
+ * which loses what lies below about 2^-14.3 of the largest; that sum times both
+ * scales is added in fp32.  With few rows they are summed exactly instead, and
+ * with K < 512 in fp32 for any number of rows (by name, variant 1 takes the
+ * matrix instruction for every K).
  * Extents (2 N in the place of N), offsets, padding, aliasing and no-ops as for
  * tla_grouped_gemm; rows that do not start on dwords run at the few-row kernel's
  * rate.

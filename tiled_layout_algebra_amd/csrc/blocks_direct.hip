@@ -8,6 +8,12 @@
 // loads in front of the copies: a lane's rows' (col-major scales: 16 neighbours
 // together) and the one or two of the workgroup's columns.
 //
+// kWide (K < 512): the fragments are widened to f16 and every product and sum is fp32,
+// as in the other e4m3 products of that length: what the 8-bit instruction drops of
+// terms of like sizes lies under fp32's own rounding bound in long sums only.  8192 rows x 4096 x 384 43 us (without 35), gated 82 (52 in
+// the two-group kernel, which has no such form); 300 rows 7.0 (6.1), 9 (8.7).  The
+// few-row kernel, which sums the same way, takes 361 and 326 for the 8192 rows.
+//
 // Bound by its copies: a workgroup's k-tile takes 0.45 us alone on a compute unit with 64
 // rows, 0.72 with 128.  Measured, 4096 x 4096 weights, 32 k-tiles: 96 rows 18.6 us (64
 // x 128), 800 rows 26.7 and 28 (128 x 128); gated, 48 rows 19 and 27.
@@ -16,7 +22,7 @@
 namespace tla {
 namespace {
 
-template <int BM, int kStages, int kWM, int kWN, bool kTwo>
+template <int BM, int kStages, int kWM, int kWN, bool kTwo, bool kWide>
 __global__ __launch_bounds__(64 * kWM * kWN) void blocks_direct_kernel(const GroupedParams p) {
   constexpr int BN = 128, kRowBytes = 128, NT = 64 * kWM * kWN;
   using Swz = typename Slab<kRowBytes>::Swz;
@@ -124,8 +130,12 @@ __global__ __launch_bounds__(64 * kWM * kWN) void blocks_direct_kernel(const Gro
       constexpr int at = kTwo ? j % FH * 16 * kRowBytes + j / FH * (SLAB_B / 2) : j * 16 * kRowBytes;
       b[j] = frag(fb + S * STAGE + SLAB_A + at);
     });
-    sums.mma(a, b, s, [](auto) {});
-    sums.finish(s);
+    if constexpr (kWide) {
+      sums.mma_wide(a, b, s);
+    } else {
+      sums.mma(a, b, s, [](auto) {});
+      sums.finish(s);
+    }
   };
   if (KT > 0) {
     // the first tile's scales before its copies, so that the loop's first wait covers them
@@ -144,16 +154,22 @@ __global__ __launch_bounds__(64 * kWM * kWN) void blocks_direct_kernel(const Gro
       p, e, m_end, m0 + wm0, n0 + wb0, lane, sums.acc, region);
 }
 
-template <int BM, int kStages, int kWM, int kWN, bool kTwo>
-int launch(const GroupedParams& p0, hipStream_t stream) {
+template <int BM, int kStages, int kWM, int kWN, bool kTwo, bool kWide>
+int launch_form(const GroupedParams& p0, hipStream_t stream) {
   GroupedParams p = p0;
   p.tiles_n = kTwo ? (p.N + 63) / 64 : (p.N + 127) / 128;
   const int64_t grid = row_tiles_bound(p.rows, p.groups, BM) * p.tiles_n;
   if (grid <= 0) return TLA_OK;
   if (!grid_fits(grid, 64 * kWM * kWN)) return TLA_ERR_UNSUPPORTED;
-  hipLaunchKernelGGL((blocks_direct_kernel<BM, kStages, kWM, kWN, kTwo>), dim3((unsigned)grid),
+  hipLaunchKernelGGL((blocks_direct_kernel<BM, kStages, kWM, kWN, kTwo, kWide>), dim3((unsigned)grid),
                      dim3(64 * kWM * kWN), 0, stream, p);
   return hipGetLastError() == hipSuccess ? TLA_OK : TLA_ERR_HIP;
+}
+
+template <int BM, int kStages, int kWM, int kWN, bool kTwo>
+int launch(const GroupedParams& p, hipStream_t s) {
+  return p.K < kMinKE4m3 ? launch_form<BM, kStages, kWM, kWN, kTwo, true>(p, s)
+                         : launch_form<BM, kStages, kWM, kWN, kTwo, false>(p, s);
 }
 
 }  // namespace

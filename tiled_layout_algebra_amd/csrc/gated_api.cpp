@@ -53,6 +53,8 @@ int finish(Plan* out, int forced) {
   if (p.B2 && !aligned_to(p.B2, 4)) out->allowed &= ~kTiles;
   const int eb = type_bytes(out->type);
   if (forced >= 0) out->allowed &= 1u << forced;
+  // short sums are fp32 throughout: of the tile kernels only the direct ones have that form
+  else if (blocks && a.K < kMinKE4m3) out->allowed &= ~(1u << kTwoGroup);
   // (the few-row kernel takes any block-scaled problem; with K = 0 every kernel
   // but the general one stands back)
   if (a.K == 0 && blocks && out->allowed & 1u << kFewRows1) out->kernel = kFewRows1;
@@ -146,7 +148,7 @@ int plan_gated(const tla_gated_gemm_args* a, Plan* out, int forced) {
   s.K = a->K;
   s.offsets = a->offsets;
   s.A = a->X;
-  s.type = blocks ? TLA_I8 : a->type;  // (blocks of any K take the matrix instruction)
+  s.type = blocks ? TLA_I8 : a->type;  // (for the estimates; short sums: finish)
   s.lda = a->ldx;
   s.B = a->W_gate;
   s.b_order = a->w_order;
@@ -267,7 +269,7 @@ int plan_blocks(const tla_gemm_blocks_args* a, Plan* out, int forced) {
   s.K = a->K;
   s.offsets = a->offsets;
   s.A = a->A;
-  s.type = TLA_I8;  // (blocks of any K take the matrix instruction)
+  s.type = TLA_I8;  // (for the estimates; short sums: finish)
   s.lda = a->lda;
   s.B = a->B;
   s.b_order = TLA_COL_MAJOR;

@@ -68,6 +68,27 @@ struct BlockSums {
       __builtin_amdgcn_sched_barrier(0);  // in this order
     });
   }
+  // The whole k-tile with e4m3 widened to f16, which holds every e4m3 value: here each
+  // product and sum is fp32, where the 8-bit instruction drops what lies far below a
+  // block's largest term.
+  __device__ __forceinline__ void mma_wide(const i32x8 (&a)[FM], const i32x8 (&b)[FN],
+                                           const float (&s)[2][FM]) {
+    i32x4 wa[FM][4];
+    static_for<FM>([&](auto i) { static_for<4>([&](auto q) { wa[i][q] = E4m3AsF16::widen(a[i], q); }); });
+    static_for<FN>([&](auto j) {
+      i32x4 wb[4];
+      static_for<4>([&](auto q) { wb[q] = E4m3AsF16::widen(b[j], q); });
+      static_for<FM>([&](auto i) {
+        f32x4 x = {0.f, 0.f, 0.f, 0.f};
+        static_for<4>([&](auto q) {
+          x = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, wb[q]),
+                                                     __builtin_bit_cast(f16x8, wa[i][q]), x, 0, 0, 0);
+        });
+        const float c = s[kTwo && j >= FN / 2][i];
+        static_for<4>([&](auto q) { acc[i][j][(int)q] = fmaf(x[(int)q], c, acc[i][j][(int)q]); });
+      });
+    });
+  }
   __device__ __forceinline__ void finish(const float (&s)[2][FM]) {
     static_for<kAhead>([&](auto x) { add<kN - kAhead + x>(s); });
   }
