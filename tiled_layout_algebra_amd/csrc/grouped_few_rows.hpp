@@ -84,7 +84,7 @@ template <>
 struct Step16<kE4M3Blocks> : Step16<kE4M3> {};
 
 template <int kCode, int MT, int NT, int kWaves, bool kDword, int kRole = kPlain>
-__global__ __launch_bounds__(64 * kWaves) void grouped_few_rows_kernel(const GroupedParams p) {
+__global__ __launch_bounds__(64 * kWaves) void grouped_few_rows_kernel(const GroupedParams p, int first) {
   using S = Step16<kCode>;
   typedef typename S::Acc Acc;
   constexpr bool kBlocks = kCode == kE4M3Blocks;
@@ -97,7 +97,7 @@ __global__ __launch_bounds__(64 * kWaves) void grouped_few_rows_kernel(const Gro
   __shared__ Acc part[kWaves][MT * NT][64];
 
   RowTile t;
-  if (!row_tile<BM>(p, blockIdx.x, t)) return;
+  if (!row_tile<BM>(p, first + (int)blockIdx.x, t)) return;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n0 = t.tn * BN;
@@ -293,6 +293,8 @@ __global__ __launch_bounds__(64 * kWaves) void grouped_few_rows_kernel(const Gro
   }
 }
 
+constexpr int64_t kMaxTiles = (int64_t(1) << 31) - 4096;  // counted in 32 bits
+
 template <int kCode, int MT, int NT, int kWaves, int kRole = kPlain>
 int launch(const GroupedParams& p0, hipStream_t stream) {
   constexpr int EB = type_bytes(kCode);
@@ -301,16 +303,22 @@ int launch(const GroupedParams& p0, hipStream_t stream) {
   p.tiles_n = (p.N + kCols - 1) / kCols;
   const int64_t grid = row_tiles_bound(p.rows, p.groups, 16 * MT) * p.tiles_n;
   if (grid <= 0) return TLA_OK;
-  if (!grid_fits(grid, 64 * kWaves)) return TLA_ERR_UNSUPPORTED;
+  if (grid > kMaxTiles) return TLA_ERR_UNSUPPORTED;
   const bool dword = aligned(p.A, 4) && aligned(p.B, 4) && (kRole != kGated || aligned(p.B2, 4)) && p.lda * EB % 4 == 0 &&
                      p.ldb * EB % 4 == 0 && (p.groups == 1 || p.stride_b * EB % 4 == 0);
-  if (dword)
-    hipLaunchKernelGGL((grouped_few_rows_kernel<kCode, MT, NT, kWaves, true, kRole>), dim3((unsigned)grid),
-                       dim3(64 * kWaves), 0, stream, p);
-  else
-    hipLaunchKernelGGL((grouped_few_rows_kernel<kCode, MT, NT, kWaves, false, kRole>),
-                       dim3((unsigned)grid), dim3(64 * kWaves), 0, stream, p);
-  return hipGetLastError() == hipSuccess ? TLA_OK : TLA_ERR_HIP;
+  // launches of fewer than 2^32 threads, each a multiple of the eight XCDs (the last: what is left)
+  constexpr int64_t kStep = kMaxThreads / (64 * kWaves) / 8 * 8;
+  for (int64_t first = 0; first < grid; first += kStep) {
+    const dim3 blocks((unsigned)(grid - first < kStep ? grid - first : kStep)), threads(64 * kWaves);
+    if (dword)
+      hipLaunchKernelGGL((grouped_few_rows_kernel<kCode, MT, NT, kWaves, true, kRole>), blocks, threads, 0,
+                         stream, p, (int)first);
+    else
+      hipLaunchKernelGGL((grouped_few_rows_kernel<kCode, MT, NT, kWaves, false, kRole>), blocks, threads, 0,
+                         stream, p, (int)first);
+    if (hipGetLastError() != hipSuccess) return TLA_ERR_HIP;
+  }
+  return TLA_OK;
 }
 
 }  // namespace

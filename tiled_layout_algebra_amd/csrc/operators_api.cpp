@@ -47,18 +47,25 @@ bool k_rows_fit(int64_t k, int64_t ld, int eb) {
   return ld <= (kLimit - 1) / ((k > 64 ? k : 64) * eb);
 }
 
-// Whether a launch holds the kernel's workgroups.
-bool launches(Kernel k, const tla_grouped_gemm_args* a) {
+// Whether a launch holds the kernel's workgroups.  bands: the few-row kernel's may go
+// out in several launches, while 32 bits count them (16 columns each at the least), for
+// products that may have no other kernel (gated_api.cpp); where the grouped products'
+// do not fit, the general kernel takes the call.
+bool launches(Kernel k, const tla_grouped_gemm_args* a, bool bands) {
+  auto blocks = [&](int64_t bm, int64_t bn) {
+    return row_tiles_bound(a->rows, a->groups, bm) * ((a->N + bn - 1) / bn);
+  };
   auto fits = [&](int64_t bm, int64_t bn, int threads, int64_t more) {
-    return grid_fits(row_tiles_bound(a->rows, a->groups, bm) * ((a->N + bn - 1) / bn) + more, threads);
+    return grid_fits(blocks(bm, bn) + more, threads);
   };
   const bool narrow = few_rows_narrow(a->rows, a->groups, a->N);
-  const int64_t few_n = narrow ? 16 : 32;
-  const int few_threads = narrow ? 512 : 256;
+  auto few = [&](int64_t bm) {
+    return bands ? blocks(bm, 16) <= kMaxExtent : fits(bm, narrow ? 16 : 32, narrow ? 512 : 256, 0);
+  };
   switch (k) {
-    case kFewRows1: return fits(16, few_n, few_threads, 0);
-    case kFewRows2: return fits(32, few_n, few_threads, 0);
-    case kFewRows4: return fits(64, few_n, few_threads, 0);
+    case kFewRows1: return few(16);
+    case kFewRows2: return few(32);
+    case kFewRows4: return few(64);
     case kDirect64: case kDirect64Shift: return fits(64, 128, 256, 0);
     case kDirect128: case kDirect128Shift: return fits(128, 128, 512, 0);
     // half tiles throughout, or whole ones and fewer than 256 halves
@@ -68,9 +75,9 @@ bool launches(Kernel k, const tla_grouped_gemm_args* a) {
 }
 
 // Whether a kernel takes the problem.
-bool takes(Kernel k, const tla_grouped_gemm_args* a, int eb, bool b_kc) {
+bool takes(Kernel k, const tla_grouped_gemm_args* a, int eb, bool b_kc, bool bands = false) {
   if (k == kGeneral) return true;
-  if (a->K == 0 || !launches(k, a)) return false;
+  if (a->K == 0 || !launches(k, a, bands)) return false;
   if (k == kFewRows1 || k == kFewRows2 || k == kFewRows4) return b_kc;
   if (a->type == TLA_E4M3 && a->K < kMinKE4m3) return false;
   // 32-bit offsets within a tile's rows
@@ -131,7 +138,7 @@ Kernel choose(const tla_grouped_gemm_args* a, int eb, bool b_kc, unsigned allowe
   Kernel best = kNoop;
   double best_us = 1e30;
   auto consider = [&](Kernel k, double us) {
-    if (!(allowed >> k & 1) || !takes(k, a, eb, b_kc)) return;
+    if (!(allowed >> k & 1) || !takes(k, a, eb, b_kc, r.own)) return;
     us = us > weights + 4.0 ? us : weights + 4.0;
     if (us < best_us) {
       best = k;
@@ -239,7 +246,7 @@ int plan_product(const tla_grouped_gemm_args* a, Plan* out) {
       (!a->bias || aligned_to(a->bias, 4 * bb)))
     p.flags |= kOpVec4;
   // no other kernel needs fewer threads than the one that takes everything
-  if (!launches(kGeneral, a)) return TLA_ERR_UNSUPPORTED;
+  if (!launches(kGeneral, a, false)) return TLA_ERR_UNSUPPORTED;
   out->type = a->type;
   out->b_kc = b_kc;
   out->kernel = choose(a, eb, b_kc, kAnyKernel, Rates{});
