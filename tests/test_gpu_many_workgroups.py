@@ -47,3 +47,24 @@ def test_no_k_and_many_elements(gated):
     torch.cuda.synchronize()
     for lo in range(0, rows, 16384):
         assert (out[lo:lo + 16384] == want).all()
+
+
+@pytest.mark.parametrize("K", [0, 3])
+def test_short_sums_and_many_elements(K):
+    """16 bits, lines shorter than a chunk: 2^32 elements and more."""
+    rows, N = 131075, 32776
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    X, W = (torch.randn(*s, generator=gen, device="cuda").bfloat16() for s in ((rows, K), (2 * N, K)))
+    b, up = (torch.randn(N, generator=gen, device="cuda").bfloat16() for _ in range(2))
+    H = torch.full((rows, N), float("nan"), dtype=torch.bfloat16, device="cuda")
+    tla.gated_gemm(1, rows, N, K, None, X, tla.BF16, K, W, W[N:], NK, K, 0, H, tla.BF16, N, b_gate=b, b_up=up,
+                   act=tla.ACT_RELU)
+    torch.cuda.synchronize()
+    for lo in range(0, rows, 8192):
+        assert not H[lo:lo + 8192].isnan().any()
+    for r in (0, 1, 65535, 131039, 131040, rows - 1):  # (row 131040 and column 0: element 2^32 and a little)
+        x = X[r].double()
+        g, u = W[:N].double() @ x + b.double(), W[N:].double() @ x + up.double()
+        e = (K + 4) * 2.0 ** -24 * (W.double().abs() @ x.abs()).view(2, N).amax(0) + 2.0 ** -24 * (b.abs() + up.abs())
+        want = g.clamp(min=0) * u
+        assert ((H[r].double() - want).abs() <= e * (g.abs() + u.abs() + e) + want.abs() * 2.0 ** -8 * 1.01 + 1e-30).all()

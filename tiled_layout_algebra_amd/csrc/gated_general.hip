@@ -7,13 +7,9 @@
 namespace tla {
 namespace {
 
-// One thread an element of the hidden layer, the sums in order.  Extents below
-// eight elements only, where no kernel's tiles would be a tenth full.
+// The element at row, n of the hidden layer, the sums in order.
 template <int kRole>
-__global__ __launch_bounds__(256) void gated_small_kernel(const GroupedParams p, int type, bool b_kc) {
-  const int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (x >= (int64_t)p.rows * p.N) return;
-  const int row = (int)(x / p.N), n = (int)(x % p.N);
+__device__ __forceinline__ void gated_small(const GroupedParams& p, int type, bool b_kc, int row, int n) {
   // the last expert that starts at or before the row
   int e = 0, lo, hi;
   for (int above = p.groups; above - e > 1;) {
@@ -53,10 +49,19 @@ __global__ __launch_bounds__(256) void gated_small_kernel(const GroupedParams p,
   }
 }
 
+// A thread an element, or, past the largest grid, several.  Extents below eight
+// elements only, where no kernel's tiles would be a tenth full, and K = 0.
+template <int kRole>
+__global__ __launch_bounds__(256) void gated_small_kernel(const GroupedParams p, int type, bool b_kc) {
+  const int64_t all = (int64_t)p.rows * p.N, step = (int64_t)gridDim.x * 256;
+  for (int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x; x < all; x += step)
+    gated_small<kRole>(p, type, b_kc, (int)(x / p.N), (int)(x % p.N));
+}
+
 template <int kRole>
 int launch_small(const GroupedParams& p, int type, bool b_kc, hipStream_t s) {
-  const int64_t grid = ((int64_t)p.rows * p.N + 255) / 256;
-  if (!grid_fits(grid, 256)) return TLA_ERR_UNSUPPORTED;
+  const int64_t need = ((int64_t)p.rows * p.N + 255) / 256, most = kMaxThreads / 256;
+  const int64_t grid = need < most ? need : most;
   hipLaunchKernelGGL((gated_small_kernel<kRole>), dim3((unsigned)grid), dim3(256), 0, s, p, type, b_kc);
   return hipGetLastError() == hipSuccess ? TLA_OK : TLA_ERR_HIP;
 }
