@@ -1,0 +1,28 @@
+"""The layers refuse offsets of another length than their experts need, before any
+kernel could read past them."""
+import pytest
+import torch
+
+
+def layers():
+    from tiled_layout_algebra_amd.expert_layer import ExpertLayer
+    from tiled_layout_algebra_amd.gated_layer import GatedLayer
+    t = lambda *shape: torch.zeros(*shape, dtype=torch.bfloat16)  # noqa: E731
+    for experts in (1, 3):
+        e = ExpertLayer(t(experts, 8, 16), t(experts, 16), t(experts, 16, 8))
+        g = GatedLayer(t(experts, 32, 8), t(experts, 8, 16))
+        for call in (e.forward, e.decode, g.forward, g.serve):
+            yield experts, call
+
+
+def test_offsets_of_another_length():
+    x = torch.zeros(5, 8, dtype=torch.bfloat16)
+    for experts, call in layers():
+        for n in (0, experts, experts + 2):
+            with pytest.raises(ValueError, match="offsets must hold"):
+                call(x, torch.zeros(n, dtype=torch.int32))
+        with pytest.raises(ValueError, match="offsets must hold"):
+            call(x, torch.zeros(experts + 1, 1, dtype=torch.int32))
+        if experts > 1:
+            with pytest.raises(ValueError, match="offsets must hold"):
+                call(x, None)

@@ -26,6 +26,12 @@ def _check(t, what, shape):
         raise ValueError("%s must be a contiguous bfloat16 tensor of shape %s" % (what, list(shape)))
 
 
+def _check_offsets(offsets, experts):
+    """The kernels read experts + 1 values (None: a single expert)."""
+    if experts != 1 if offsets is None else tuple(offsets.shape) != (experts + 1,):
+        raise ValueError("offsets must hold %d values" % (experts + 1))
+
+
 class ExpertLayer:
     """Weights W1 [experts, width, hidden], b1 [experts, hidden] and W2
     [experts, hidden, width], contiguous bf16 CUDA tensors, stored [K, N] for
@@ -43,6 +49,7 @@ class ExpertLayer:
         expert, offsets int32 [experts + 1]."""
         import torch
         _check(x, "x", (x.shape[0], self.width))
+        _check_offsets(offsets, self.experts)
         g, w, h, rows = self.experts, self.width, self.hidden, x.shape[0]
         act, z = (torch.empty(rows, h, dtype=x.dtype, device=x.device) for _ in range(2))
         y = torch.empty(rows, w, dtype=x.dtype, device=x.device)
@@ -94,6 +101,7 @@ class ExpertLayer:
         """y in int8: tokens quantized, both products with their scales."""
         import torch
         _check(x, "x", (x.shape[0], self.width))
+        _check_offsets(offsets, self.experts)
         g, w, h, rows = self.experts, self.width, self.hidden, x.shape[0]
         for k, n, (W, s), bias, act in ((w, h, self.q1, self.b1, tla.ACT_GELU),
                                         (h, w, self.q2, None, tla.ACT_NONE)):

@@ -28,6 +28,12 @@ def _check(t, what, shape):
         raise ValueError("%s must be a contiguous bfloat16 tensor of shape %s" % (what, list(shape)))
 
 
+def _check_offsets(offsets, experts):
+    """The kernels read experts + 1 values (None: a single expert)."""
+    if experts != 1 if offsets is None else tuple(offsets.shape) != (experts + 1,):
+        raise ValueError("offsets must hold %d values" % (experts + 1))
+
+
 def _up(n, to):
     return -(-n // to) * to
 
@@ -61,6 +67,7 @@ class GatedLayer:
         expert, offsets int32 [experts + 1]."""
         import torch
         _check(x, "x", (x.shape[0], self.width))
+        _check_offsets(offsets, self.experts)
         g, w, h, rows = self.experts, self.width, self.hidden, x.shape[0]
         act = torch.empty(rows, h, dtype=x.dtype, device=x.device)
         z = torch.empty(rows, 2 * h, dtype=x.dtype, device=x.device)
@@ -113,6 +120,7 @@ class GatedLayer:
         """y and the hidden layer, both products in e4m3."""
         import torch
         _check(x, "x", (x.shape[0], self.width))
+        _check_offsets(offsets, self.experts)
         g, w, h, rows = self.experts, self.width, self.hidden, x.shape[0]
         act = torch.empty(rows, h, dtype=x.dtype, device=x.device)
         y = torch.empty_like(x)
