@@ -1,5 +1,5 @@
-"""The layers refuse offsets of another length than their experts need, before any
-kernel could read past them."""
+"""The layers refuse what their calls would misread: offsets of another length than the
+experts need, before any kernel could read past them, and tokens of another form.""" 
 import pytest
 import torch
 
@@ -26,3 +26,11 @@ def test_offsets_of_another_length():
         if experts > 1:
             with pytest.raises(ValueError, match="offsets must hold"):
                 call(x, None)
+
+
+def test_tokens_that_would_be_misread():
+    from tiled_layout_algebra_amd.gated_layer import quantize_tokens
+    for x in (torch.zeros(4, 8), torch.zeros(4, 8, dtype=torch.float16),
+              torch.zeros(4, 16, dtype=torch.bfloat16)[:, ::2], torch.zeros(8, 4, dtype=torch.bfloat16).t()):
+        with pytest.raises(ValueError, match="x must be a contiguous bfloat16"):
+            quantize_tokens(x)

@@ -42,6 +42,7 @@ def quantize_tokens(x):
     """e4m3 codes [rows, width rounded up to 16] of a contiguous bf16 tensor and
     their scales [blocks of 128, rows], as gated_gemm and gemm_blocks read them."""
     import torch
+    _check(x, "x", tuple(x.shape))
     rows, width = x.shape
     pitch = _up(width, 16)
     q = torch.empty(rows, pitch, dtype=torch.float8_e4m3fn, device=x.device)
