@@ -338,11 +338,11 @@ int tla_quantize_rows(int64_t M, int64_t K, const void *X, int32_t x_type, int64
  * type F16 or BF16: any order, pitch and alignment to the element; the scales
  * are NULL.  type E4M3, with block scales as in tla_gemm_blocks: scale_x of X's
  * rows, scale_gate and scale_up of each 128 x 128 block, TLA_COL_MAJOR weights
- * only.  H, Z: row-major, h_type: type, or for E4M3 F16 or BF16.  Biases (groups x N, dense, or
- * NULL) F16, BF16 or F32.  act: any of tla_act.  Sums and the epilogue are fp32,
- * each output is rounded once.  SiLU is z times the sigmoid, so SiLU(-inf) is
- * NaN; the sigmoid is off by at most (|z| + 4) 2^-24 of its value and is 0 below
- * 2^-126, GELU as said for tla_grouped_gemm.
+ * only.  H, Z: row-major, h_type: type, or for E4M3 F16 or BF16.  Biases (groups
+ * x N, dense, or NULL) F16, BF16 or F32.  act: any of tla_act.  Sums (e4m3: as
+ * said there) and the epilogue are fp32, each output is rounded once.  SiLU is z times the sigmoid, so SiLU(-inf) is
+ * NaN; the sigmoid is off by at most (1.25 |z| + 5) 2^-24 of its value and is 0
+ * below 2^-126, GELU as said for tla_grouped_gemm.
  *
  * groups, rows or N == 0 is a no-op, K == 0 gives g = b_gate, u = b_up.  Offsets,
  * extents (2 N in the place of N), padding, aliasing and rows of no expert as for
@@ -369,8 +369,9 @@ int tla_gated_gemm(const tla_gated_gemm_args *args, void *stream);
  * hidden layer, the down projection read in the other order:
  *   dh[r, n] = sum_k dY[r, k] W_e(k, n)             (never stored)
  *   dZ_gate = dh u act'(g),  dZ_up = dh act(g),  H = act(g) u unless NULL
- * with g = Z_gate, u = Z_up as the forward pass kept them.  act' of tla_grouped_gemm; SiLU': p + z p (1 - p), p the sigmoid; 1
- * without an activation.  H lets a program drop the hidden layer after the
+ * with g = Z_gate, u = Z_up as the forward pass kept them.  act' of
+ * tla_grouped_gemm; SiLU': p + z p (1 - p), p the sigmoid, so NaN at an infinity;
+ * 1 without an activation.  H lets a program drop the hidden layer after the
  * forward pass; it is what the down projection's weight gradient reads.
  * The rest of the backward pass: dX = dZ_gate Wg^T + dZ_up Wu^T (one product
  * where they are halves of a buffer), the weight and bias gradients
@@ -405,9 +406,9 @@ int tla_gated_gemm_grad(const tla_gated_grad_args *args, void *stream);
  * tla_act.
  * From K = 512 on a block's products are summed by the 8-bit matrix instruction,
  * which loses what lies below about 2^-14.3 of the largest; that sum times both
- * scales is added in fp32.  With few rows they are summed exactly instead, and
- * with K < 512 in fp32 for any number of rows (by name, variant 1 takes the
- * matrix instruction for every K).
+ * scales, which are multiplied first, is added in fp32.  With few rows, and with
+ * K < 512 for any number of them, every product and sum is fp32 instead (by name,
+ * variant 1 takes the 8-bit instruction for every K).
  * Extents (2 N in the place of N), offsets, padding, aliasing and no-ops as for
  * tla_grouped_gemm; rows that do not start on dwords run at the few-row kernel's
  * rate.
@@ -436,7 +437,7 @@ int tla_gemm_blocks(const tla_gemm_blocks_args *args, void *stream);
  * the last blocks may be short.  A block of zeros, or one whose scale rounds to
  * 0, gets zero codes; so does a block with an infinity or a NaN, whose scale is
  * that infinity or NaN.  Q: row-major, pitch ldq >= K, any alignment; its padding
- * is not written.  M or K == 0 is a no-op; M and K at most 2^31 - 4096, with
+ * is not written; X, Q and scale must not overlap.  M or K == 0 is a no-op; M and K at most 2^31 - 4096, with
  * block_rows 128 K at most 2^30 - 128.
  */
 typedef struct {

@@ -1,5 +1,5 @@
 """The layers refuse what their calls would misread: offsets of another length than the
-experts need, before any kernel could read past them, and tokens of another form.""" 
+experts need, before any kernel could read past them, and tokens of another form."""
 import pytest
 import torch
 
