@@ -1,4 +1,4 @@
-"""The layers refuse what their calls would misread: offsets of another length than the
+"""The layers refuse what their calls would misread: fewer offsets than the
 experts need, before any kernel could read past them, and tokens of another form."""
 import pytest
 import torch
@@ -15,17 +15,12 @@ def layers():
             yield experts, call
 
 
-def test_offsets_of_another_length():
+def test_too_few_offsets():
     x = torch.zeros(5, 8, dtype=torch.bfloat16)
     for experts, call in layers():
-        for n in (0, experts, experts + 2):
-            with pytest.raises(ValueError, match="offsets must hold"):
+        for n in range(experts + 1):
+            with pytest.raises(ValueError, match="offsets must hold %d values" % (experts + 1)):
                 call(x, torch.zeros(n, dtype=torch.int32))
-        with pytest.raises(ValueError, match="offsets must hold"):
-            call(x, torch.zeros(experts + 1, 1, dtype=torch.int32))
-        if experts > 1:
-            with pytest.raises(ValueError, match="offsets must hold"):
-                call(x, None)
 
 
 def test_tokens_that_would_be_misread():
