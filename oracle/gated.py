@@ -26,21 +26,6 @@ def expand(scale, block_rows, rows, cols):
     return s.repeat_interleave(128, dim=-1)[..., :cols]
 
 
-def largest_terms(A, B, offsets):
-    """sum over blocks of 128 k of the largest |A B| in the block: A rows x K, B
-    groups x K x N, both with their scales in."""
-    rows, K = A.shape
-    out = torch.zeros(rows, B.shape[2], dtype=torch.float64)
-    for e, (lo, hi) in enumerate(grouped.spans(offsets)):
-        a, b = A[lo:hi].double().abs(), B[e].double().abs()
-        for k in range(0, K, 128):
-            top = torch.zeros(hi - lo, b.shape[1], dtype=torch.float64)
-            for i in range(k, min(k + 128, K)):
-                top = torch.maximum(top, a[:, i:i + 1] * b[i:i + 1])
-            out[lo:hi] += top
-    return out
-
-
 def round_e4m3(x):
     """float64 to the nearest e4m3 value (as float64), ties to even, at most +-448."""
     x = x.clamp(-448, 448)

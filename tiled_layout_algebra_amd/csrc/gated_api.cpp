@@ -96,7 +96,7 @@ int run(const Plan& plan, hipStream_t s) {
   }
 }
 
-// The checks that the three products share.  Returns 1 for nothing to do.
+// The checks that the three products share.
 int check_shape(int64_t groups, int64_t rows, int64_t N, int64_t K, int act, int w_order) {
   if (groups < 0 || rows < 0 || N < 0 || K < 0) return TLA_ERR_INVALID_ARG;
   if (!order_ok(w_order)) return TLA_ERR_INVALID_ARG;

@@ -112,7 +112,7 @@ __global__ __launch_bounds__(kThreads, kBView == kBElem ? 1 : 2) void grouped_ge
   // kGated: columns 0 .. 63 of B's slab are the gate's, the others the same
   // columns of the up projection; MFMA tile 0 of a wave the gate's, 1 the other's
   constexpr bool kTwo = kRole == kGated;
-  static_assert(kLoose || kRole == kPlain, "lines shorter than a chunk: gated_small.hip");
+  static_assert(kLoose || kRole == kPlain, "lines shorter than a chunk: gated_small_kernel");
   static_assert(!kWgrad || kNT, "the weight gradient sums over rows of both operands");
   static_assert(4 * WM * 64 * FN <= 2 * STAGE, "epilogue regions");
   __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * STAGE];

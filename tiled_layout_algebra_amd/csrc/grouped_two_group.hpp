@@ -53,10 +53,12 @@
 // columns x 4096, SiLU, gate and up kept: 820-845 us = 1320 TFLOP/s, of which the 400
 // MB written are 60 (MFMA busy 0.78).  kGateGrad at the same sizes, SiLU, hidden
 // written: 538 us; a tile's epilogue moves 640 KiB, and every compute unit does so at
-// once (busy 0.56).  Every other unit begun half a tile ahead, so that epilogues meet
+// once (busy 0.56); beside the sums and a part's gate and up 52 to 66 registers spill
+// there, none in the loop.  Every other unit begun half a tile ahead, so that epilogues meet
 // products: 616 instead of 579 then, its half tiles cost more.  Block scales: 8192^3
 // 440 us = 2500 TFLOP/s, e4m3 without scales 390 on that box, at 1.66 GHz both by the
-// card's power (busy 0.65); gated, 2048 x 8192 x 4096, 120 us, two rounds of tiles.
+// card's power (busy 0.65; 16 to 66 registers spill); gated, 2048 x 8192 x 4096, 120 us,
+// two rounds of tiles.
 #pragma once
 
 #include "gated_common.hpp"

@@ -126,7 +126,8 @@ int launch_gated_few_rows(const GroupedParams& p, int type, int mt, hipStream_t 
 
 // e4m3 with block scales, B K-contiguous: 256 x 256, 128 x 128 and 64 x 128
 // tiles for rows that start on dwords less than 8 MiB apart, and the kernel for
-// few rows, which takes any.  gated: role kGated.
+// few rows, which takes any.  gated: role kGated.  K < kMinKE4m3: fp32 sums in
+// the 64- and 128-row tiles and for few rows.
 int launch_blocks_two_group(const GroupedParams& p, bool gated, hipStream_t stream);
 int launch_blocks_direct(const GroupedParams& p, int bm, bool gated, hipStream_t stream);
 int launch_blocks_few_rows(const GroupedParams& p, int mt, bool gated, hipStream_t stream);
